@@ -330,7 +330,7 @@ def _attend(s):
         import block_sparse_long_fwd_b200 as moba
 
         more = {"kmean": s["kmean"], "block_size": s["block"], "topk": s["topk"]} if s["topk"] else {}
-        out, lse = moba.kv4_attend(s["q"], s["kv4"], s["lengths"], cu=s["cu"], max_q=s["n"], acc=s["acc"], **more)
+        out, lse = moba.kv4_attend(s["q"], s["kv4"], s["lengths"], cu=s["cu"], acc=s["acc"], **more)
     else:
         kv4, hkv, n = s["kv4"], s["heads_kv"], s["n"]
         batch, S = kv4.shape[0], kv4.shape[2] * TILE
