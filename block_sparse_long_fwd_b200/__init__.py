@@ -27,6 +27,8 @@ MOBA_ERR_DEVICE_TIMEOUT = 5
 MOBA_ERR_DEVICE_CHECK = 6
 HEAD_DIM = 128
 MAX_TOPK = 64
+KV4_TILE = 64
+KV4_TILE_BYTES = 9216
 
 # every entry point the header declares, with its ctypes signature
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -40,6 +42,12 @@ SIGNATURES = {
     "moba_pool": (_i32, [_vp, _i64, _i32, _i32, _i32, _vp, _vp]),
     "moba_gate": (_i32, [_vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _vp, _vp]),
     "moba_fwd_noalloc": (_i32, [_vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "moba_kv4_append": (_i32, [_vp, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp]),
+    "moba_kv4_load": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i64, _i64, _vp, _vp, _vp]),
+    "moba_kv4_pool": (_i32, [_vp, _vp, _i32, _i32, _i32, _i64, _i32, _vp, _vp]),
+    "moba_kv4_attend": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i64, _i32, _i32, _vp, _vp, _vp,
+                               _vp]),
+    "moba_kv4_evict": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp]),
     "moba_profile_begin": (_i32, []),
     "moba_profile_end": (_i32, [_vp, _vp, _vp]),
     "moba_last_error": (ctypes.c_char_p, []),
@@ -255,6 +263,167 @@ def gate(q: torch.Tensor, kmean: torch.Tensor, heads_kv: int, block_size: int, t
     _check(lib().moba_gate(q.data_ptr(), kp, S, Hq, heads_kv, d, block_size, topk, sel.data_ptr(),
                            _stream(stream)))
     return sel
+
+
+def kv4_cache(batch: int, heads_kv: int, capacity: int, device="cuda") -> torch.Tensor:
+    """An empty 4-bit key/value cache: uint8 [batch, heads_kv, tiles, 9216],
+    with room for ``capacity`` tokens a sequence (rounded up to whole tiles of
+    64 tokens). The caller keeps the sequences' lengths.
+    """
+    tiles = (capacity + KV4_TILE - 1) // KV4_TILE
+    return torch.zeros((batch, heads_kv, tiles, KV4_TILE_BYTES), dtype=torch.uint8, device=device)
+
+
+def _kv4(x: torch.Tensor, name: str = "kv4"):
+    if not (x.is_cuda and x.dtype == torch.uint8 and x.is_contiguous() and x.dim() == 4
+            and x.shape[3] == KV4_TILE_BYTES):
+        raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor [batch, heads_kv, tiles, {KV4_TILE_BYTES}]")
+    return x.shape[0], x.shape[1], x.shape[2] * KV4_TILE
+
+
+def _on(x, name: str, dtype, shape, device):
+    """Address of a contiguous tensor of this type, shape and device (None stays None)."""
+    if x is None:
+        return None
+    if x.dtype != dtype or tuple(x.shape) != tuple(shape) or x.device != device or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+    return x.data_ptr()
+
+
+def kv4_append(k: torch.Tensor, v: torch.Tensor, kv4: torch.Tensor, start: torch.Tensor, cu=None, acc=None,
+               stream=None) -> None:
+    """Store new tokens in a 4-bit cache.
+
+    k, v [T, Hkv, 128] bf16 hold the new tokens of the sequences one after
+    another; ``cu`` (int32 [batch + 1], on the GPU) gives their offsets, None
+    the same number for each. Sequence b's first one goes to place
+    ``start[b]`` (int32 [batch], on the GPU). ``acc`` (fp32 [batch, Hkv,
+    capacity]) is set to zero there.
+    """
+    batch, hkv, cap = _kv4(kv4)
+    dev = kv4.device
+    _dev_bf16(k, "k"), _dev_bf16(v, "v")
+    T = k.shape[0]
+    kp, vp = (_on(x, n, torch.bfloat16, (T, hkv, HEAD_DIM), dev) for x, n in ((k, "k"), (v, "v")))
+    cp = _on(cu, "cu", torch.int32, (batch + 1,), dev)
+    sp = _on(start, "start", torch.int32, (batch,), dev)
+    ap = _on(acc, "acc", torch.float32, (batch, hkv, cap), dev)
+    if T == 0:
+        return
+    with torch.cuda.device(dev):
+        _check(lib().moba_kv4_append(kp, vp, T, cp, sp, batch, hkv, HEAD_DIM, cap, kv4.data_ptr(), ap,
+                                     _stream(stream)))
+
+
+def kv4_load(kv4: torch.Tensor, lengths: torch.Tensor, n: int, first=None, stream=None):
+    """Tokens first[b] .. first[b] + n - 1 of a 4-bit cache (``first`` int32
+    [batch] on the GPU; None: from token 0) as bf16: (k, v), each
+    [batch, n, Hkv, 128], exact, zero from ``lengths[b]`` on.
+    """
+    batch, hkv, cap = _kv4(kv4)
+    dev = kv4.device
+    lp = _on(lengths, "lengths", torch.int32, (batch,), dev)
+    fp = _on(first, "first", torch.int32, (batch,), dev)
+    if not 0 <= n <= cap:
+        raise ValueError("n must be in [0, capacity]")
+    k, v = (torch.empty((batch, n, hkv, HEAD_DIM), dtype=torch.bfloat16, device=dev) for _ in "kv")
+    if n == 0:
+        return k, v
+    with torch.cuda.device(dev):
+        _check(lib().moba_kv4_load(kv4.data_ptr(), lp, fp, batch, hkv, HEAD_DIM, cap, n, k.data_ptr(), v.data_ptr(),
+                                   _stream(stream)))
+    return k, v
+
+
+def kv4_pool(kv4: torch.Tensor, lengths: torch.Tensor, block_size: int, kmean=None, stream=None) -> torch.Tensor:
+    """Mean keys of a 4-bit cache's complete blocks: fp32
+    [batch, Hkv, capacity // block_size, 128], zero for the other blocks.
+    """
+    batch, hkv, cap = _kv4(kv4)
+    dev = kv4.device
+    lp = _on(lengths, "lengths", torch.int32, (batch,), dev)
+    if block_size < 1:
+        raise ValueError("block_size must be positive")
+    shape = (batch, hkv, cap // block_size, HEAD_DIM)
+    if kmean is None:
+        kmean = torch.empty(shape, dtype=torch.float32, device=dev)
+    mp = _on(kmean, "kmean", torch.float32, shape, dev)
+    if shape[2]:
+        with torch.cuda.device(dev):
+            _check(lib().moba_kv4_pool(kv4.data_ptr(), lp, batch, hkv, HEAD_DIM, cap, block_size, mp, _stream(stream)))
+    return kmean
+
+
+def kv4_attend(q: torch.Tensor, kv4: torch.Tensor, lengths: torch.Tensor, cu=None, kmean=None, block_size: int = 0,
+               topk: int = 0, acc=None, out=None, lse=None, stream=None):
+    """Attention of each sequence's last tokens over its 4-bit cache.
+
+    q [T, Hq, 128] bf16 holds the queries of the sequences one after another
+    (``cu`` as in ``kv4_append``): those of the last tokens of each, which
+    ``lengths`` (int32 [batch], on the GPU) already counts. Every key at or
+    before a query is attended, or with ``kmean`` (``kv4_pool``'s) its own
+    block and the ``topk - 1`` best past blocks, as in ``fwd_chunk``.
+    ``acc`` (fp32 [batch, Hkv, capacity]) grows by the tokens' attention
+    weights. Returns (out [T, Hq, 128] bf16, lse [Hq, T] fp32).
+    """
+    batch, hkv, cap = _kv4(kv4)
+    dev = kv4.device
+    _dev_bf16(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [T, heads_q, head_dim]")
+    T, hq, d = q.shape
+    qp = _on(q, "q", torch.bfloat16, (T, hq, HEAD_DIM), dev)
+    cp = _on(cu, "cu", torch.int32, (batch + 1,), dev)
+    lp = _on(lengths, "lengths", torch.int32, (batch,), dev)
+    ap = _on(acc, "acc", torch.float32, (batch, hkv, cap), dev)
+    mp = None
+    if kmean is not None:
+        if block_size < 1 or topk < 1:
+            raise ValueError("kmean needs block_size and topk")
+        mp = _on(kmean, "kmean", torch.float32, (batch, hkv, cap // block_size, HEAD_DIM), dev)
+        mp = mp if kmean.numel() else None  # less than a block of room: every key is in the own block
+    elif block_size or topk:
+        raise ValueError("block_size and topk need kmean")
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((hq, T), dtype=torch.float32, device=dev) if lse is None else lse
+    op = _on(out, "out", torch.bfloat16, (T, hq, HEAD_DIM), dev)
+    ep = _on(lse, "lse", torch.float32, (hq, T), dev)
+    if T == 0:
+        return out, lse
+    with torch.cuda.device(dev):
+        _check(lib().moba_kv4_attend(qp, T, cp, kv4.data_ptr(), lp, mp, batch, hq, hkv, HEAD_DIM, cap, block_size,
+                                     topk, ap, op, ep, _stream(stream)))
+    return out, lse
+
+
+def kv4_evict(kv4: torch.Tensor, acc: torch.Tensor, lengths: torch.Tensor, budget: int, recent: int,
+              dst: torch.Tensor, dst_acc: torch.Tensor, stream=None):
+    """Bring a 4-bit cache down to ``budget`` tokens a sequence by accumulated
+    weight: the last ``recent`` tokens and the heaviest others of each kv head
+    go, in their order, into ``dst`` and ``dst_acc`` (another cache and its
+    weights, with room for the budget).
+
+    Returns (lengths int32 [batch] of the new cache, kept int32
+    [batch, Hkv, budget]: the old index of every kept token, padded with -1).
+    """
+    batch, hkv, cap = _kv4(kv4)
+    dev = kv4.device
+    db, dh, dcap = _kv4(dst, "dst")
+    if (db, dh) != (batch, hkv) or dst.device != dev:
+        raise ValueError("dst must be a cache of the same sequences and heads on the same device")
+    if acc is None or dst_acc is None:
+        raise ValueError("acc and dst_acc are required")
+    ap = _on(acc, "acc", torch.float32, (batch, hkv, cap), dev)
+    dp = _on(dst_acc, "dst_acc", torch.float32, (batch, hkv, dcap), dev)
+    lp = _on(lengths, "lengths", torch.int32, (batch,), dev)
+    if not 1 <= budget <= dcap or not 0 <= recent <= budget:
+        raise ValueError("budget must be in [1, dst's capacity] and recent in [0, budget]")
+    new = torch.empty_like(lengths)
+    kept = torch.empty((batch, hkv, budget), dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().moba_kv4_evict(kv4.data_ptr(), ap, lp, batch, hkv, HEAD_DIM, cap, budget, recent, dst.data_ptr(),
+                                    dp, dcap, kept.data_ptr(), new.data_ptr(), _stream(stream)))
+    return new, kept
 
 
 def device_status(stream=None) -> int:

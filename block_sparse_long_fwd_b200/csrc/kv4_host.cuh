@@ -1,0 +1,251 @@
+// Entry points of the 4-bit key/value cache (kv4.cuh, kv4_attn.cuh): argument
+// checks, scratch and launches. Included at the end of moba.cu, whose helpers
+// (fail, device_info, direct_run, launch_chained, ...) it uses.
+#pragma once
+
+#include "kv4.cuh"
+#include "kv4_attn.cuh"
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+// Shape of a cache: `capacity` tokens a sequence, in whole tiles.
+int check_cache(int batch, int heads, int d, int64_t capacity) {
+  if (batch < 1) return fail(MOBA_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
+  if (heads < 1) return fail(MOBA_ERR_INVALID_ARG, "heads_kv must be >= 1 (got %d)", heads);
+  if (d != MOBA_HEAD_DIM) return fail(MOBA_ERR_INVALID_ARG, "head_dim must be %d (got %d)", MOBA_HEAD_DIM, d);
+  if (capacity < 1 || capacity % MOBA_KV4_TILE)
+    return fail(MOBA_ERR_INVALID_ARG, "capacity must be a positive multiple of %d (got %lld)", MOBA_KV4_TILE,
+                (long long)capacity);
+  if (capacity > ((int64_t)1 << 30)) return fail(MOBA_ERR_UNSUPPORTED, "capacity above 2^30 tokens is not supported");
+  if ((int64_t)batch * heads > 65535)
+    return fail(MOBA_ERR_UNSUPPORTED, "more than 65535 (sequence, kv head) pairs are not supported");
+  return MOBA_OK;
+}
+
+size_t cache_bytes(int batch, int heads, int64_t capacity) {
+  return (size_t)batch * heads * (capacity / moba::kKv4Tile) * moba::kKv4TileBytes;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// The device, and an error that an earlier call's kernels left behind.
+int kv4_begin(DeviceInfo* dev, cudaStream_t st) {
+  int rc = device_info(dev);
+  if (rc) return rc;
+  return take_pending_status(*dev, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int moba_kv4_append(const void* k, const void* v, int64_t total, const int32_t* cu, const int32_t* start, int batch,
+                    int heads_kv, int head_dim, int64_t capacity, void* kv4, float* acc, cudaStream_t stream) {
+  g_err.clear();
+  if (!k || !v || !start || !kv4) return fail(MOBA_ERR_INVALID_ARG, "null pointer argument");
+  int rc = check_cache(batch, heads_kv, head_dim, capacity);
+  if (rc) return rc;
+  if (total < 0 || total > INT32_MAX) return fail(MOBA_ERR_INVALID_ARG, "total must be in [0, 2^31)");
+  if (!cu && total % batch) return fail(MOBA_ERR_INVALID_ARG, "without cu, total must be a multiple of batch");
+  if (!aligned16(k) || !aligned16(v) || !aligned16(kv4))
+    return fail(MOBA_ERR_INVALID_ARG, "k, v and kv4 must be 16-byte aligned");
+  if (!aligned4(cu) || !aligned4(start) || !aligned4(acc))
+    return fail(MOBA_ERR_INVALID_ARG, "cu, start and acc must be 4-byte aligned");
+  DeviceInfo dev;
+  rc = kv4_begin(&dev, stream);
+  if (rc) return rc;
+  if (total == 0) return finish_call(MOBA_OK, stream);
+  moba::Kv4AppendParams p;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.cu = cu;
+  p.start = start;
+  p.total = total;
+  p.tiles = capacity / moba::kKv4Tile;
+  p.batch = batch;
+  p.heads = heads_kv;
+  p.kv4 = static_cast<uint8_t*>(kv4);
+  p.acc = acc;
+  const int64_t threads = total * heads_kv * 16;
+  launch_chained(moba::kv4_append_kernel,
+                 dim3((unsigned)((threads + moba::kKv4AppendThreads - 1) / moba::kKv4AppendThreads)),
+                 dim3(moba::kKv4AppendThreads), 0, stream, p);
+  MOBA_CUDA(cudaGetLastError());
+  return finish_call(MOBA_OK, stream);
+}
+
+int moba_kv4_load(const void* kv4, const int32_t* lengths, const int32_t* first, int batch, int heads_kv, int head_dim,
+                  int64_t capacity, int64_t n, void* k, void* v, cudaStream_t stream) {
+  g_err.clear();
+  if (!kv4 || !lengths || !k || !v) return fail(MOBA_ERR_INVALID_ARG, "null pointer argument");
+  int rc = check_cache(batch, heads_kv, head_dim, capacity);
+  if (rc) return rc;
+  if (n < 0 || n > capacity) return fail(MOBA_ERR_INVALID_ARG, "n must be in [0, capacity]");
+  if (!aligned16(k) || !aligned16(v) || !aligned16(kv4))
+    return fail(MOBA_ERR_INVALID_ARG, "k, v and kv4 must be 16-byte aligned");
+  if (!aligned4(lengths) || !aligned4(first))
+    return fail(MOBA_ERR_INVALID_ARG, "lengths and first must be 4-byte aligned");
+  DeviceInfo dev;
+  rc = kv4_begin(&dev, stream);
+  if (rc) return rc;
+  if (n == 0) return finish_call(MOBA_OK, stream);
+  moba::Kv4LoadParams p;
+  p.kv4 = static_cast<const uint8_t*>(kv4);
+  p.lengths = lengths;
+  p.first = first;
+  p.tiles = capacity / moba::kKv4Tile;
+  p.n = n;
+  p.batch = batch;
+  p.heads = heads_kv;
+  p.k = static_cast<__nv_bfloat16*>(k);
+  p.v = static_cast<__nv_bfloat16*>(v);
+  const int64_t ctas = (n * batch * heads_kv * 16 + moba::kKv4LoadThreads - 1) / moba::kKv4LoadThreads;
+  if (ctas > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
+  launch_chained(moba::kv4_load_kernel, dim3((unsigned)ctas), dim3(moba::kKv4LoadThreads), 0, stream, p);
+  MOBA_CUDA(cudaGetLastError());
+  return finish_call(MOBA_OK, stream);
+}
+
+int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch, int heads_kv, int head_dim, int64_t capacity,
+                  int block_size, float* kmean, cudaStream_t stream) {
+  g_err.clear();
+  if (!kv4 || !lengths || !kmean) return fail(MOBA_ERR_INVALID_ARG, "null pointer argument");
+  int rc = check_cache(batch, heads_kv, head_dim, capacity);
+  if (rc) return rc;
+  rc = check_shape(capacity, heads_kv, heads_kv, head_dim, block_size, 1);
+  if (rc) return rc;
+  if (!aligned16(kv4) || !aligned16(kmean)) return fail(MOBA_ERR_INVALID_ARG, "kv4 and kmean must be 16-byte aligned");
+  if (!aligned4(lengths)) return fail(MOBA_ERR_INVALID_ARG, "lengths must be 4-byte aligned");
+  DeviceInfo dev;
+  rc = kv4_begin(&dev, stream);
+  if (rc) return rc;
+  moba::Kv4PoolParams p;
+  p.kv4 = static_cast<const uint8_t*>(kv4);
+  p.lengths = lengths;
+  p.tiles = capacity / moba::kKv4Tile;
+  p.heads = heads_kv;
+  p.B = block_size;
+  p.blocks = (int)(capacity / block_size);
+  p.kmean = kmean;
+  if (p.blocks) {
+    launch_chained(moba::kv4_pool_kernel, dim3(p.blocks, heads_kv, batch), dim3(moba::kKv4PoolThreads), 0, stream, p);
+    MOBA_CUDA(cudaGetLastError());
+  }
+  return finish_call(MOBA_OK, stream);
+}
+
+int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void* kv4, const int32_t* lengths,
+                    const float* kmean, int batch, int heads_q, int heads_kv, int head_dim, int64_t capacity,
+                    int block_size, int topk, float* acc, void* out, float* lse, cudaStream_t stream) {
+  g_err.clear();
+  if (!q || !kv4 || !lengths || !out || !lse) return fail(MOBA_ERR_INVALID_ARG, "null pointer argument");
+  int rc = check_cache(batch, heads_kv, head_dim, capacity);
+  if (rc) return rc;
+  if (heads_q < 1 || heads_q % heads_kv)
+    return fail(MOBA_ERR_INVALID_ARG, "heads_q (%d) must be a positive multiple of heads_kv (%d)", heads_q, heads_kv);
+  if (total < 0 || total * heads_q > INT32_MAX) return fail(MOBA_ERR_INVALID_ARG, "total * heads_q must be in [0, 2^31)");
+  if (!cu && total % batch) return fail(MOBA_ERR_INVALID_ARG, "without cu, total must be a multiple of batch");
+  if (kmean) {
+    rc = check_shape(capacity, heads_q, heads_kv, head_dim, block_size, topk);
+    if (rc) return rc;
+    if (capacity / block_size > MOBA_KV4_MAX_BLOCKS)
+      return fail(MOBA_ERR_UNSUPPORTED, "more than %d blocks in the capacity are not supported", MOBA_KV4_MAX_BLOCKS);
+    // at least as many picks as blocks: every key
+    if (topk >= (capacity + block_size - 1) / block_size) kmean = nullptr;
+  }
+  if (!aligned16(q) || !aligned16(kv4) || !aligned16(kmean) || !aligned16(out))
+    return fail(MOBA_ERR_INVALID_ARG, "q, kv4, kmean and out must be 16-byte aligned");
+  if (!aligned4(cu) || !aligned4(lengths) || !aligned4(acc) || !aligned4(lse))
+    return fail(MOBA_ERR_INVALID_ARG, "cu, lengths, acc and lse must be 4-byte aligned");
+  DeviceInfo dev;
+  rc = kv4_begin(&dev, stream);
+  if (rc) return rc;
+  if (total == 0) return finish_call(MOBA_OK, stream);
+  moba::Kv4AttnParams p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.kv4 = static_cast<const uint8_t*>(kv4);
+  p.lengths = lengths;
+  p.cu = cu;
+  p.kmean = kmean;
+  p.total = total;
+  p.tiles = capacity / moba::kKv4Tile;
+  p.batch = batch;
+  p.Hq = heads_q;
+  p.Hkv = heads_kv;
+  p.G = heads_q / heads_kv;
+  p.B = kmean ? block_size : 1;
+  p.topk = kmean ? topk : 1;
+  p.blocks = kmean ? (int)(capacity / block_size) : 0;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)moba::kHeadDim));
+  p.acc = acc;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  const Runner run = [&](uint8_t* ws, cudaStream_t st) -> int {
+    p.sel = reinterpret_cast<int32_t*>(ws);
+    const dim3 rows((unsigned)(total * heads_q));
+    if (kmean)
+      launch_chained(moba::kv4_gate_kernel, rows, dim3(moba::kKv4GateThreads), (size_t)p.blocks * 9, st, p);
+    launch_chained(moba::kv4_attn_kernel, rows, dim3(moba::kKv4AttnThreads), 0, st, p);
+    if (acc)
+      launch_chained(moba::kv4_weight_kernel, dim3((unsigned)(capacity / 8), heads_kv, batch),
+                     dim3(moba::kKv4AttnThreads), 0, st, p);
+    MOBA_CUDA(cudaGetLastError());
+    return MOBA_OK;
+  };
+  rc = direct_run((size_t)total * heads_q * p.topk * 4, run, stream);
+  return finish_call(rc, stream);
+}
+
+int moba_kv4_evict(const void* kv4, const float* acc, const int32_t* lengths, int batch, int heads_kv, int head_dim,
+                   int64_t capacity, int64_t budget, int64_t recent, void* dst_kv4, float* dst_acc,
+                   int64_t dst_capacity, int32_t* kept, int32_t* new_lengths, cudaStream_t stream) {
+  g_err.clear();
+  if (!kv4 || !acc || !lengths || !dst_kv4 || !dst_acc || !kept || !new_lengths)
+    return fail(MOBA_ERR_INVALID_ARG, "null pointer argument");
+  int rc = check_cache(batch, heads_kv, head_dim, capacity);
+  if (rc) return rc;
+  rc = check_cache(batch, heads_kv, head_dim, dst_capacity);
+  if (rc) return rc;
+  if (budget < 1 || budget > dst_capacity)
+    return fail(MOBA_ERR_INVALID_ARG, "budget must be in [1, dst_capacity] (got %lld)", (long long)budget);
+  if (recent < 0 || recent > budget)
+    return fail(MOBA_ERR_INVALID_ARG, "recent must be in [0, budget] (got %lld)", (long long)recent);
+  if (!aligned16(kv4) || !aligned16(dst_kv4)) return fail(MOBA_ERR_INVALID_ARG, "the caches must be 16-byte aligned");
+  if (!aligned4(acc) || !aligned4(lengths) || !aligned4(dst_acc) || !aligned4(kept) || !aligned4(new_lengths))
+    return fail(MOBA_ERR_INVALID_ARG, "acc, lengths, kept and new_lengths must be 4-byte aligned");
+  const size_t pairs = (size_t)batch * heads_kv;
+  if (overlap(kv4, cache_bytes(batch, heads_kv, capacity), dst_kv4, cache_bytes(batch, heads_kv, dst_capacity)) ||
+      overlap(acc, pairs * capacity * 4, dst_acc, pairs * dst_capacity * 4) ||
+      overlap(lengths, (size_t)batch * 4, new_lengths, (size_t)batch * 4))
+    return fail(MOBA_ERR_INVALID_ARG, "the outputs must not overlap the inputs");
+  DeviceInfo dev;
+  rc = kv4_begin(&dev, stream);
+  if (rc) return rc;
+  moba::Kv4EvictParams p;
+  p.kv4 = static_cast<const uint8_t*>(kv4);
+  p.acc = acc;
+  p.lengths = lengths;
+  p.tiles = capacity / moba::kKv4Tile;
+  p.dst_tiles = dst_capacity / moba::kKv4Tile;
+  p.batch = batch;
+  p.heads = heads_kv;
+  p.budget = (int)budget;
+  p.recent = (int)recent;
+  p.dst = static_cast<uint8_t*>(dst_kv4);
+  p.dst_acc = dst_acc;
+  p.kept = kept;
+  p.new_lengths = new_lengths;
+  launch_chained(moba::kv4_select_kernel, dim3(heads_kv, batch), dim3(moba::kKv4SelectThreads), 0, stream, p);
+  launch_chained(moba::kv4_move_kernel,
+                 dim3((unsigned)((budget * 16 + moba::kKv4MoveThreads - 1) / moba::kKv4MoveThreads), (unsigned)pairs),
+                 dim3(moba::kKv4MoveThreads), 0, stream, p);
+  MOBA_CUDA(cudaGetLastError());
+  return finish_call(MOBA_OK, stream);
+}
+
+}  // extern "C"

@@ -1656,3 +1656,5 @@ extern "C" int moba_fwd_noalloc(const void* q, const void* k, const void* v, int
   if (rc) return rc;
   return finish_call(run_forward(p, dev, q, k, v, out, lse, static_cast<uint8_t*>(scratch), stream), stream);
 }
+
+#include "kv4_host.cuh"

@@ -296,6 +296,137 @@ int moba_fwd_noalloc(const void* q, const void* k, const void* v,
                      int block_size, int topk, void* out, float* lse,
                      cudaStream_t stream);
 
+/*
+ * Key/value cache in 4 bits, for serving: prompts and new tokens are stored
+ * with moba_kv4_append, attended with moba_kv4_attend (every key, or MoBA's
+ * blocks by the means of moba_kv4_pool), read back as bf16 with
+ * moba_kv4_load (for moba_fwd_chunk, for instance), and brought down to a
+ * budget of the most attended tokens with moba_kv4_evict. The pages have no
+ * counterpart: they mention long-context serving (Kimi's requests: "MoBA
+ * (Mixture of Block Attention)" project summary, "Deployment"), whose cache
+ * this shortens from 512 bytes a token and kv head to 144.
+ *
+ * A value is held as scale * (code - zero) with 4-bit codes, and a scale of
+ * four significant bits (2^-17 .. 3840) and a 4-bit zero point for 32
+ * channels of a token: for a group's lo = min(x, 0) and hi = max(x, 0),
+ * scale = (hi - lo) / 15 rounded to the nearest scale, zero = -lo / scale and
+ * code = x / scale + zero, both rounded to the nearest whole number (halves
+ * up) and cut to 0 .. 15. Every such value is exactly a bf16 number. Inputs
+ * saturate at +-28800; a NaN is stored as zero.
+ *
+ * kv4        device buffer [batch][heads_kv][capacity / 64][9216 bytes], one
+ *            64-token tile of a kv head after another; its inner layout is
+ *            the library's (csrc/kv4.cuh). A new one needs no initialising.
+ * capacity   tokens a sequence has room for, a positive multiple of 64, at
+ *            most 2^30; batch * heads_kv at most 65535.
+ * lengths    device int32 [batch]: tokens in the cache. The caller keeps
+ *            them; no call changes them. They, cu and start are read on the
+ *            device, in stream order: nothing here waits for the GPU, and a
+ *            captured graph takes their values of the time of its replay.
+ * acc        device fp32 [batch][heads_kv][capacity]: the attention weight
+ *            each cached token has received so far, or NULL.
+ * cu         device int32 [batch + 1]: packed rows of sequence b are cu[b] ..
+ *            cu[b+1] - 1, non-decreasing, cu[0] >= 0; rows from cu[batch] on
+ *            belong to no sequence and are left alone. NULL: total / batch
+ *            rows each.
+ * Lengths outside [0, capacity] and tokens outside the capacity are a
+ * caller's error that only the device sees: the kernels cut or skip them and
+ * record MOBA_ERR_DEVICE_CHECK. Caches are 16-byte aligned, q, k, v, kmean
+ * and out too; the other buffers 4-byte. Ownership, stream, scratch and
+ * errors as moba_fwd.
+ */
+#define MOBA_KV4_TILE 64            /* tokens in a tile                     */
+#define MOBA_KV4_TILE_BYTES 9216    /* bytes of a tile                      */
+#define MOBA_KV4_MAX_BLOCKS 16384   /* capacity / block_size at most        */
+
+/*
+ * moba_kv4_append - store new tokens' keys and values.
+ *
+ * k, v       device bf16 [total][heads_kv][head_dim], packed by cu.
+ * start      device int32 [batch]: the place of each sequence's first new
+ *            token (its length before the call).
+ * acc        if not NULL, the new tokens' weights are set to zero.
+ */
+int moba_kv4_append(const void* k, const void* v, int64_t total,
+                    const int32_t* cu, const int32_t* start, int batch,
+                    int heads_kv, int head_dim, int64_t capacity, void* kv4,
+                    float* acc, cudaStream_t stream);
+
+/*
+ * moba_kv4_load - the cached values of tokens first[b] .. first[b] + n - 1 as
+ * bf16, exactly; zero from lengths[b] on and before token 0.
+ *
+ * first      device int32 [batch], or NULL for 0.
+ * n          tokens a sequence, 0 <= n <= capacity.
+ * k, v       device bf16 outputs [batch][n][heads_kv][head_dim].
+ */
+int moba_kv4_load(const void* kv4, const int32_t* lengths,
+                  const int32_t* first, int batch, int heads_kv, int head_dim,
+                  int64_t capacity, int64_t n, void* k, void* v,
+                  cudaStream_t stream);
+
+/*
+ * moba_kv4_pool - the mean cached key of every complete block (lengths[b] /
+ * block_size of them, from token 0), in fp32, summed in a fixed order; zero
+ * for the others.
+ *
+ * block_size a positive multiple of 128.
+ * kmean      device fp32 output [batch][heads_kv][capacity / block_size]
+ *            [head_dim] (whole blocks only).
+ */
+int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch,
+                  int heads_kv, int head_dim, int64_t capacity, int block_size,
+                  float* kmean, cudaStream_t stream);
+
+/*
+ * moba_kv4_attend - attention of the last tokens of each sequence over its
+ * cache: one token (a decode step), a chunk, or different numbers of tokens.
+ * Query row i of the n of sequence b stands at position lengths[b] - n + i
+ * (its own key is already in the cache) and attends the cached tokens at and
+ * before it: all of them, or with kmean its own block and the topk - 1 past
+ * blocks of the highest q . mean, as moba_fwd_chunk_means (scores are summed
+ * in fp64 here; ties to the lower block index). A row without keys (its
+ * position is negative) has out 0 and lse -infinity.
+ *
+ * q          device bf16 [total][heads_q][head_dim], packed by cu.
+ * kmean      device fp32 as moba_kv4_pool writes it, or NULL: every key, and
+ *            block_size and topk are not looked at.
+ * block_size, topk  with kmean, as moba_fwd (block_size a positive multiple
+ *            of 128, topk - 1 at most 64 unless topk covers the capacity).
+ * acc        if not NULL: acc[b][g][j] += the sum, over the query rows of
+ *            the sequence and the q heads of kv head g, of the softmax weight
+ *            of token j. In a fixed order.
+ * out        device bf16 output [total][heads_q][head_dim].
+ * lse        device fp32 output [heads_q][total], natural log.
+ */
+int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu,
+                    const void* kv4, const int32_t* lengths,
+                    const float* kmean, int batch, int heads_q, int heads_kv,
+                    int head_dim, int64_t capacity, int block_size, int topk,
+                    float* acc, void* out, float* lse, cudaStream_t stream);
+
+/*
+ * moba_kv4_evict - a cache of at most `budget` tokens a sequence out of a
+ * longer one, by accumulated attention weight: every kv head keeps the last
+ * `recent` tokens and, of the others, the budget - recent with the largest
+ * acc (equal weights: the lower index; a NaN counts below every number), in
+ * their order. A sequence of at most budget tokens keeps them all. Blocks of
+ * the new cache are consecutive kept tokens: its means are pooled anew.
+ *
+ * acc        device fp32 [batch][heads_kv][capacity]; required.
+ * dst_kv4, dst_acc, dst_capacity  the new cache and its weights, with
+ *            budget <= dst_capacity; places from the new length on are left
+ *            as they are. They must not overlap the old ones.
+ * kept       device int32 output [batch][heads_kv][budget]: the old index of
+ *            each kept token, ascending, padded with -1.
+ * new_lengths  device int32 output [batch]: min(length, budget); not lengths.
+ */
+int moba_kv4_evict(const void* kv4, const float* acc, const int32_t* lengths,
+                   int batch, int heads_kv, int head_dim, int64_t capacity,
+                   int64_t budget, int64_t recent, void* dst_kv4,
+                   float* dst_acc, int64_t dst_capacity, int32_t* kept,
+                   int32_t* new_lengths, cudaStream_t stream);
+
 /* Message of the last failed call on this host thread ("" if none). */
 const char* moba_last_error(void);
 

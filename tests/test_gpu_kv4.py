@@ -1,0 +1,580 @@
+"""The 4-bit key/value cache on the GPU against its numpy definition in fp64.
+
+Tolerances, from the arithmetic (u = 2^-24, half a step of fp32 at 1):
+  scores   128 exact products summed in fp32, in an order and rounding of the tensor core's choosing: at most
+           d = 140 * 2u * max sum |q k| / sqrt(128), the few roundings of the scale included;
+  weights  relative r = 2 d + 2^-21 (the exponential's and its argument's) + N u (the sum over N keys);
+  out      2^-8 |out| (its rounding to bf16) + (r + 2^-11 + N u) * sum w |v| (weights enter the products as fp16);
+           fp16 weights end at 2^-37 of the largest: + N * 2^-37 max |v|;
+  lse      d + 2^-21 + N u + 4 u |lse|;
+  acc      2 r times the weights + (rows + 2) u |acc|.
+What is stored, loaded, pooled over few bits and moved is compared bit for bit.
+"""
+import numpy as np
+import pytest
+
+import kv4_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import block_sparse_long_fwd_b200 as moba  # noqa: E402
+
+U = 2.0**-24
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def bf16(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(torch.bfloat16)
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def ok():
+    torch.cuda.synchronize()
+    assert moba.device_status() == moba.MOBA_OK
+
+
+def random_cache(lengths, hkv, capacity, seed, offset=0.5):
+    """A cache filled by the reference, with its values: (kv4 on the GPU, [k, v of each sequence])."""
+    rng = np.random.default_rng(seed)
+    tiles, vals = [], []
+    for _ in lengths:
+        mu = rng.standard_normal((hkv, 1, 128)) * offset
+        k = f64(bf16(rng.standard_normal((hkv, capacity, 128)) + mu))
+        v = f64(bf16(rng.standard_normal((hkv, capacity, 128))))
+        t = ref.pack(k, v)
+        tiles.append(t)
+        vals.append(ref.unpack(t))
+    return torch.from_numpy(np.stack(tiles)).cuda(), vals
+
+
+# ------------------------------------------------------------------ append and load
+
+
+@pytest.mark.parametrize("hkv,starts,news", [
+    (1, [0], [1]), (1, [0], [64]), (2, [0], [131]), (3, [63], [2]), (8, [5, 0, 127, 64], [1, 1, 1, 1]),
+    (2, [0, 100, 3], [65, 0, 200]), (1, [0, 7], [0, 0]),
+])
+@pytest.mark.parametrize("with_acc", [False, True])
+def test_append_stores_the_defined_bytes_and_nothing_else(hkv, starts, news, with_acc):
+    rng = np.random.default_rng(3)
+    batch, cap, T = len(news), 320, sum(news)
+    k, v = (bf16(rng.standard_normal((T + 5, hkv, 128)) * 2 + 0.3) for _ in "kv")
+    cu = np.concatenate(([0], np.cumsum(news)))
+    before = rng.integers(0, 256, (batch, hkv, cap // 64, 9216)).astype(np.uint8)
+    kv4 = torch.from_numpy(before.copy()).cuda()
+    acc = torch.ones(batch, hkv, cap, device="cuda") if with_acc else None
+    # five rows lie behind the last sequence
+    moba.kv4_append(k.cuda(), v.cuda(), kv4, ints(starts), cu=ints(cu), acc=acc)
+    ok()
+    want, want_acc = before.copy(), np.ones((batch, hkv, cap))
+    for b in range(batch):
+        rows = np.zeros((2, hkv, cap, 128))
+        at = slice(starts[b], starts[b] + news[b])
+        for s, x in enumerate((k, v)):
+            rows[s][:, at] = f64(x)[cu[b]:cu[b + 1]].transpose(1, 0, 2)
+        new = ref.pack(rows[0], rows[1])
+        for t in range(at.start, at.stop):
+            tile, i = t // 64, t % 64
+            for off in (0, 4608):
+                for a, z in ((off + 64 * i, 64), (off + 4096 + 8 * i, 8)):
+                    want[b, :, tile, a:a + z] = new[:, tile, a:a + z]
+        want_acc[b, :, at] = 0
+    assert np.array_equal(kv4.cpu().numpy(), want)
+    if with_acc:
+        assert np.array_equal(acc.cpu().numpy(), want_acc)
+
+
+def test_append_of_awkward_values():
+    # NaN, infinities, more than the largest stored value, subnormals, a span of one bf16 step, scales on both
+    # sides of a tie (255 and 272 are 17 and 18.13 times 15)
+    rng = np.random.default_rng(9)
+    x = f64(bf16(rng.standard_normal((64, 1, 128)) * np.exp2(rng.integers(-30, 16, (64, 1, 4))).repeat(32, -1)))
+    x[0, 0, :8] = [np.nan, np.inf, -np.inf, 3e38, -3e38, 1e-40, -1e-40, 0]
+    x[1] = 0.0
+    x[2] = 7.0
+    x[3] = -7.0
+    x[4] = np.resize(np.array([0.0, 255.0, 8.5, 25.5, 17.0]), 128)
+    x[5] = np.resize(np.array([-1.0, 1.0, 0.5, -0.5]) * 2.0**-15, 128)
+    x[6] = np.resize(np.arange(-9, 10) * 4.5, 128)
+    x[7] = np.nan
+    kv4 = moba.kv4_cache(1, 1, 64)
+    moba.kv4_append(bf16(x).cuda(), bf16(-x).cuda(), kv4, ints([0]))
+    k, v = moba.kv4_load(kv4, ints([64]), 64)
+    ok()
+    assert np.array_equal(f64(k)[0, :, 0], ref.stored(f64(bf16(x)))[:, 0])
+    assert np.array_equal(f64(v)[0, :, 0], ref.stored(f64(bf16(-x)))[:, 0])
+
+
+def test_append_without_offsets_takes_the_same_number_for_each():
+    rng = np.random.default_rng(4)
+    k, v = (bf16(rng.standard_normal((6, 2, 128))) for _ in "kv")
+    kv4 = moba.kv4_cache(3, 2, 64)
+    moba.kv4_append(k.cuda(), v.cuda(), kv4, ints([0, 10, 62]))
+    got = moba.kv4_load(kv4, ints([2, 12, 64]), 2, first=ints([0, 10, 62]))
+    ok()
+    for x, y in zip((k, v), got):
+        assert np.array_equal(f64(y), ref.stored(f64(x)).reshape(3, 2, 2, 128))
+
+
+def test_tokens_without_room_are_skipped_and_reported():
+    kv4 = moba.kv4_cache(2, 1, 64)
+    x = torch.ones(4, 1, 128, dtype=torch.bfloat16, device="cuda")
+    moba.kv4_append(x, x, kv4, ints([63, 0]))
+    assert moba.device_status() == moba.MOBA_ERR_DEVICE_CHECK
+    moba.kv4_append(x, x, kv4, ints([-1, 3]))
+    assert moba.device_status() == moba.MOBA_ERR_DEVICE_CHECK
+    k, _ = moba.kv4_load(kv4, ints([64, 64]), 64)
+    ok()
+    want = np.zeros((2, 64))
+    want[0, [63, 0]] = want[1, [0, 1, 3, 4]] = 1
+    assert np.array_equal(f64(k)[:, :, 0].max(-1) > 0.5, want > 0)
+
+
+@pytest.mark.parametrize("n,first", [(1, None), (70, None), (33, [0, 60, 250]), (256, [-3, 255, 100])])
+def test_load_gives_zero_outside_the_sequence(n, first):
+    lengths = [0, 77, 256]
+    kv4, vals = random_cache(lengths, 2, 256, 7)
+    k, v = moba.kv4_load(kv4, ints(lengths), n, first=None if first is None else ints(first))
+    ok()
+    for b, L in enumerate(lengths):
+        at = (first[b] if first else 0) + np.arange(n)
+        inside = (at >= 0) & (at < L)
+        for got, x in zip((k, v), vals[b]):
+            want = np.where(inside[:, None, None], x.transpose(1, 0, 2)[at.clip(0, 255)], 0)
+            assert np.array_equal(f64(got[b]), want)
+
+
+# ------------------------------------------------------------------ pool
+
+
+@pytest.mark.parametrize("hkv,lengths,block", [
+    (1, [128], 128), (1, [127], 128), (2, [0, 1000, 128 * 7, 1024], 128), (3, [1000, 1023], 256), (1, [1024], 1024),
+    (2, [1024, 700], 384),
+])
+def test_pool_gives_the_means_of_complete_blocks(hkv, lengths, block):
+    cap = 1024
+    kv4, vals = random_cache(lengths, hkv, cap, 11)
+    m = moba.kv4_pool(kv4, ints(lengths), block)
+    ok()
+    assert m.shape == (len(lengths), hkv, cap // block, 128)
+    for b, L in enumerate(lengths):
+        want = ref.means(vals[b][0], L, block, cap // block)
+        # one rounding of the mean, and of each of at most `block` partial sums of at most sum |k|
+        size = ref.means(np.abs(vals[b][0]), L, block, cap // block)
+        assert (np.abs(f64(m[b]) - want) <= (block + 1) * U * size).all()
+        assert (f64(m[b])[:, L // block:] == 0).all()
+
+
+def test_pool_of_less_than_a_block_is_empty():
+    kv4, _ = random_cache([64], 1, 64, 1)
+    assert moba.kv4_pool(kv4, ints([64]), 128).shape == (1, 1, 0, 128)
+
+
+# ------------------------------------------------------------------ attend
+
+
+def check_attend(got, q, vals, lengths, news, hkv, sparse=None, kmean=None, rows=None):
+    """got = (out, lse, acc or None, acc before); q [T, Hq, 128] fp64."""
+    out, lse, acc, acc0 = got
+    out, lse = f64(out), f64(lse)
+    G = q.shape[1] // hkv
+    t = 0
+    for b, (L, n) in enumerate(zip(lengths, news)):
+        for h in range(hkv):
+            qq = q[t:t + n, h * G:(h + 1) * G]
+            k, v = (x[h, :L] for x in vals[b])
+            mask = ref.seen(qq, L, n, None if kmean is None else kmean[b, h], *(sparse or ()))
+            r = ref.attend(qq, k, v, mask)
+            d = 140 * 2 * U * r["size"]
+            w = 2 * d + 2.0**-21 + L * U
+            top = np.abs(v).max(initial=0.0)
+            tol = 2.0**-8 * np.abs(r["out"]) + (w + 2.0**-11 + L * U) * r["spread"] + L * 2.0**-37 * top
+            o = out[t:t + n, h * G:(h + 1) * G]
+            assert (np.abs(o - r["out"]) <= tol).all(), (b, h, np.abs(o - r["out"]).max())
+            e = lse[h * G:(h + 1) * G, t:t + n].T
+            none = ~mask.any(-1)
+            assert (e[none] == -np.inf).all() and (o[none] == 0).all()
+            assert (np.abs(e[~none] - r["lse"][~none]) <= d + 2.0**-21 + L * U + 4 * U * np.abs(r["lse"][~none])).all()
+            if acc is not None:
+                a, a0 = f64(acc[b, h]), f64(acc0[b, h])
+                want = a0[:L] + r["weights"]
+                assert (np.abs(a[:L] - want) <= 2 * w * r["weights"] + (n * G + 2) * U * want).all()
+                assert np.array_equal(a[L:], a0[L:])
+        t += n
+
+
+def attend_case(hkv, G, lengths, news, sparse=None, acc=True, seed=0, cap=None, qscale=1.0, pad=3):
+    rng = np.random.default_rng(seed + 100)
+    cap = cap or -(-max(max(lengths), 1) // 64) * 64 + 64
+    kv4, vals = random_cache(lengths, hkv, cap, seed)
+    T = sum(news)
+    q = bf16(rng.standard_normal((T + pad, hkv * G, 128)) * qscale)
+    kmean = moba.kv4_pool(kv4, ints(lengths), sparse[0]) if sparse else None
+    a0 = torch.from_numpy(rng.random((len(lengths), hkv, cap)).astype(np.float32)).cuda() if acc else None
+    a = a0.clone() if acc else None
+    out = torch.full((T + pad, hkv * G, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((hkv * G, T + pad), 7.0, device="cuda")
+    cu = ints(np.concatenate(([0], np.cumsum(news))))
+    more = {"kmean": kmean, "block_size": sparse[0], "topk": sparse[1]} if sparse else {}
+    moba.kv4_attend(q.cuda(), kv4, ints(lengths), cu=cu, acc=a, out=out, lse=lse, **more)
+    ok()
+    # rows behind the last sequence are left alone
+    assert (out[T:] == 7).all() and (lse[:, T:] == 7).all()
+    check_attend((out[:T], lse[:, :T], a, a0), f64(q)[:T], vals, lengths, news, hkv, sparse,
+                 f64(kmean) if sparse else None)
+
+
+DENSE = [
+    # hkv, G, lengths, new tokens
+    (1, 1, [1], [1]),
+    (1, 1, [64], [1]),
+    (1, 1, [65], [1]),
+    (2, 4, [63], [1]),
+    (1, 1, [4096], [1]),
+    (2, 4, [1000], [1]),
+    (8, 4, [130, 1, 700, 64, 65], [1, 1, 1, 1, 1]),
+    (1, 8, [777], [1]),
+    (1, 16, [777], [1]),
+    (2, 3, [500, 129], [1, 1]),
+    (1, 5, [321], [7]),
+    (2, 4, [300, 64, 1, 200], [2, 64, 1, 0]),   # a sequence without queries
+    (1, 2, [0, 90], [0, 1]),                    # an empty one
+    (1, 2, [3, 90], [5, 2]),                    # more queries than tokens: rows without keys
+    (1, 1, [2000], [300]),
+    (2, 4, [700], [129]),
+    (1, 40, [200], [9]),
+]
+
+
+@pytest.mark.parametrize("hkv,G,lengths,news", DENSE)
+@pytest.mark.parametrize("acc", [False, True])
+def test_attention_over_every_key(hkv, G, lengths, news, acc):
+    attend_case(hkv, G, lengths, news, acc=acc, seed=len(lengths) + G)
+
+
+SPARSE = [
+    # hkv, G, lengths, new tokens, block, topk
+    (1, 1, [1], [1], 128, 2),
+    (1, 1, [128], [1], 128, 1),
+    (1, 1, [129], [1], 128, 2),
+    (2, 4, [2000], [1], 128, 4),
+    (1, 2, [1300, 100, 640, 641], [1, 1, 1, 1], 128, 3),
+    (2, 4, [1500], [9], 256, 3),
+    (1, 3, [900, 1025], [200, 3], 128, 2),
+    (1, 1, [4000], [1], 128, 17),
+    (1, 8, [3000], [2], 384, 3),
+    (1, 16, [1100], [5], 128, 3),
+    (1, 4, [700, 0, 3], [3, 0, 4], 128, 2),
+    (1, 2, [600], [1], 128, 1),
+]
+
+
+@pytest.mark.parametrize("hkv,G,lengths,news,block,topk", SPARSE)
+@pytest.mark.parametrize("acc", [False, True])
+def test_attention_over_chosen_blocks(hkv, G, lengths, news, block, topk, acc):
+    attend_case(hkv, G, lengths, news, sparse=(block, topk), acc=acc, seed=block + topk)
+
+
+@pytest.mark.parametrize("qscale", [1e-4, 30.0])
+def test_attention_of_small_and_large_scores(qscale):
+    # at 30 the softmax sits on a few keys and the running maximum moves far; the tolerances grow with the scores
+    attend_case(2, 4, [3000], [1], qscale=qscale, seed=3)
+    attend_case(1, 2, [1000], [40], qscale=qscale, seed=4)
+
+
+def test_equal_scores_go_to_the_lower_block():
+    # blocks 1, 3 and 4 are equal and best; topk 3 takes 1 and 3 beside the own block
+    hkv, cap, B = 1, 1024, 128
+    k = np.zeros((hkv, cap, 128))
+    for j, x in enumerate([0.0, 1.0, 0.5, 1.0, 1.0, 0.25]):
+        k[:, j * B:(j + 1) * B] = x
+    v = np.zeros((hkv, cap, 128))
+    v[0] = (np.arange(cap) // B)[:, None] == np.arange(128)
+    kv4 = torch.from_numpy(ref.pack(k, v)[None]).cuda()
+    q = torch.ones(1, 1, 128, dtype=torch.bfloat16, device="cuda")
+    length = ints([6 * B + 1])
+    out, _ = moba.kv4_attend(q, kv4, length, kmean=moba.kv4_pool(kv4, length, B), block_size=B, topk=3)
+    ok()
+    assert set(np.nonzero(f64(out)[0, 0] > 0)[0]) == {1, 3, 6}
+
+
+def test_garbage_behind_the_last_token_is_not_read_into_results():
+    # what lies behind the length, codes and parameters, may be anything
+    hkv, L, cap = 2, 333, 512
+    kv4, vals = random_cache([L], hkv, cap, 5)
+    q = bf16(np.random.default_rng(1).standard_normal((1, 8, 128))).cuda()
+    want = moba.kv4_attend(q, kv4, ints([L]))
+    dirty = kv4.clone()
+    for tile in range(cap // 64):
+        for i in range(64):
+            if tile * 64 + i >= L:
+                for off in (0, 4608):
+                    dirty[:, :, tile, off + 64 * i:off + 64 * i + 64] = 0xFF
+                    dirty[:, :, tile, off + 4096 + 8 * i:off + 4096 + 8 * i + 8] = 0xFF
+    got = moba.kv4_attend(q, dirty, ints([L]))
+    a, b = (torch.zeros(1, hkv, cap, device="cuda") for _ in "ab")
+    moba.kv4_attend(q, kv4, ints([L]), acc=a)
+    moba.kv4_attend(q, dirty, ints([L]), acc=b)
+    ok()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(a, b)
+
+
+def test_a_length_beyond_the_capacity_is_cut_and_reported():
+    kv4, vals = random_cache([128], 1, 128, 5)
+    q = bf16(np.random.default_rng(1).standard_normal((1, 2, 128))).cuda()
+    want = moba.kv4_attend(q, kv4, ints([128]))
+    ok()
+    got = moba.kv4_attend(q, kv4, ints([1000]))
+    assert moba.device_status() == moba.MOBA_ERR_DEVICE_CHECK
+    assert torch.equal(got[0], want[0])
+    ok()
+
+
+def test_the_same_call_gives_the_same_bits():
+    lengths = [5000, 33, 2000]
+    kv4, _ = random_cache(lengths, 2, 5056, 2)
+    q = bf16(np.random.default_rng(1).standard_normal((6, 8, 128))).cuda()
+    runs = []
+    for _ in range(3):
+        acc = torch.zeros(3, 2, 5056, device="cuda")
+        runs.append((*moba.kv4_attend(q, kv4, ints(lengths), acc=acc), acc))
+    ok()
+    for r in runs[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(r, runs[0]))
+
+
+# ------------------------------------------------------------------ evict
+
+
+def evict_case(hkv, lengths, budget, recent, acc, cap, dcap, seed=0):
+    kv4, vals = random_cache(lengths, hkv, cap, seed)
+    dst = torch.full((len(lengths), hkv, dcap // 64, 9216), 0xAB, dtype=torch.uint8, device="cuda")
+    dst_acc = torch.full((len(lengths), hkv, dcap), 5.0, device="cuda")
+    acc = torch.from_numpy(acc.astype(np.float32)).cuda()
+    new, kept = moba.kv4_evict(kv4, acc, ints(lengths), budget, recent, dst, dst_acc)
+    k, v = moba.kv4_load(dst, new, min(budget, dcap))
+    ok()
+    assert new.tolist() == [min(L, budget) for L in lengths]
+    for b, L in enumerate(lengths):
+        for h in range(hkv):
+            a = acc[b, h].double().cpu().numpy()
+            want = ref.evict(a, L, budget, recent)
+            n = len(want)
+            assert np.array_equal(kept[b, h, :n].cpu().numpy(), want) and (kept[b, h, n:] == -1).all()
+            assert np.array_equal(f64(k[b, :n, h]), vals[b][0][h, want])
+            assert np.array_equal(f64(v[b, :n, h]), vals[b][1][h, want])
+            assert np.array_equal(f64(dst_acc[b, h, :n]), a[want], equal_nan=True)
+            assert (dst_acc[b, h, n:] == 5).all()
+            raw = dst[b, h].cpu().numpy()
+            for t in range(n, dcap):  # places behind the kept tokens are left alone
+                for off in (0, 4608):
+                    i = t % 64
+                    assert (raw[t // 64, off + 64 * i:off + 64 * i + 64] == 0xAB).all()
+                    assert (raw[t // 64, off + 4096 + 8 * i:off + 4096 + 8 * i + 8] == 0xAB).all()
+
+
+@pytest.mark.parametrize("hkv,lengths,budget,recent", [
+    (1, [1], 1, 0), (1, [2], 1, 0), (1, [2], 1, 1), (1, [64], 64, 3), (1, [65], 64, 64), (2, [500, 0, 100, 101], 100, 10),
+    (1, [5000], 37, 0), (1, [5000], 4999, 1), (3, [1025, 2049], 1000, 1000), (1, [4000], 3, 2),
+])
+def test_evict_keeps_the_heaviest_and_the_last(hkv, lengths, budget, recent):
+    cap = -(-max(lengths) // 64) * 64
+    rng = np.random.default_rng(budget)
+    acc = np.exp(2 * rng.standard_normal((len(lengths), hkv, cap))) * (rng.random((len(lengths), hkv, cap)) > 0.1)
+    evict_case(hkv, lengths, budget, recent, acc, cap, -(-budget // 64) * 64 + 64)
+
+
+@pytest.mark.parametrize("kind", ["equal", "few", "zero", "signed", "special", "close"])
+def test_evict_of_awkward_weights(kind):
+    cap, rng = 2048, np.random.default_rng(8)
+    acc = {"equal": lambda: np.full((1, 2, cap), 0.25), "few": lambda: rng.integers(0, 3, (1, 2, cap)) / 2.0,
+           "zero": lambda: np.where(rng.random((1, 2, cap)) < 0.5, 0.0, -0.0),
+           "signed": lambda: rng.standard_normal((1, 2, cap)),
+           "special": lambda: rng.choice([np.nan, np.inf, -np.inf, 0.0, 1e-45, 1.0], (1, 2, cap)),
+           "close": lambda: 1.0 + rng.integers(0, 4, (1, 2, cap)) * 2.0**-23}[kind]()
+    evict_case(2, [2000], 700, 33, acc, cap, 704, seed=1)
+
+
+# ------------------------------------------------------------------ together, streams, graphs
+
+
+def test_a_request_from_prompt_to_eviction():
+    """A prompt is stored, attended, decoded with weights, evicted, and decoded on: every step against fp64."""
+    rng = np.random.default_rng(21)
+    batch, hkv, G, cap, B, topk = 2, 2, 2, 1024, 128, 3
+    prompts = [700, 451]
+    cu = np.concatenate(([0], np.cumsum(prompts)))
+    kv4, acc = moba.kv4_cache(batch, hkv, cap), torch.zeros(batch, hkv, cap, device="cuda")
+    k, v = (bf16(rng.standard_normal((sum(prompts), hkv, 128))) for _ in "kv")
+    lengths = ints([0, 0])
+    moba.kv4_append(k.cuda(), v.cuda(), kv4, lengths, cu=ints(cu), acc=acc)
+    lengths = lengths + ints(prompts)
+    vals = [[ref.stored(f64(x)[cu[b]:cu[b + 1]].transpose(1, 0, 2)) for x in (k, v)] for b in range(batch)]
+    q = bf16(rng.standard_normal((16 * batch, hkv * G, 128)))  # the prompts' last 16 tokens
+    a0 = acc.clone()
+    out, lse = moba.kv4_attend(q.cuda(), kv4, lengths, acc=acc)
+    ok()
+    check_attend((out, lse, acc, a0), f64(q), vals, prompts, [16, 16], hkv)
+
+    def step(kv4, acc, lengths, vals, sparse):
+        k, v = (bf16(rng.standard_normal((batch, hkv, 128))) for _ in "kv")
+        q = bf16(rng.standard_normal((batch, hkv * G, 128)))
+        moba.kv4_append(k.cuda(), v.cuda(), kv4, lengths, acc=acc)
+        lengths = lengths + 1
+        vals = [[np.concatenate((x, ref.stored(f64(y)[b][:, None])), 1) for x, y in zip(vals[b], (k, v))]
+                for b in range(batch)]
+        kmean = moba.kv4_pool(kv4, lengths, B) if sparse else None
+        a0 = acc.clone()
+        more = {"kmean": kmean, "block_size": B, "topk": topk} if sparse else {}
+        out, lse = moba.kv4_attend(q.cuda(), kv4, lengths, acc=acc, **more)
+        ok()
+        check_attend((out, lse, acc, a0), f64(q), vals, lengths.tolist(), [1, 1], hkv, (B, topk) if sparse else None,
+                     f64(kmean) if sparse else None)
+        return lengths, vals
+
+    for i in range(4):
+        lengths, vals = step(kv4, acc, lengths, vals, i % 2 == 0)
+    weights = f64(acc)
+    dst, dst_acc = moba.kv4_cache(batch, hkv, 512), torch.zeros(batch, hkv, 512, device="cuda")
+    old = lengths.tolist()
+    lengths, kept = moba.kv4_evict(kv4, acc, lengths, 400, 32, dst, dst_acc)
+    ok()
+    new = []
+    for b in range(batch):
+        at = [ref.evict(weights[b, h], old[b], 400, 32) for h in range(hkv)]
+        assert all(np.array_equal(kept[b, h].cpu().numpy(), at[h]) for h in range(hkv))
+        new.append([np.stack([x[h, at[h]] for h in range(hkv)]) for x in vals[b]])
+    for i in range(3):
+        lengths, new = step(dst, dst_acc, lengths, new, i % 2 == 0)
+    # and the cache read back serves the framework's bf16 attention
+    k, v = moba.kv4_load(dst, lengths, 403)
+    q = bf16(rng.standard_normal((3, hkv * G, 128))).cuda()
+    o1, e1 = moba.fwd_chunk(q, k[0], v[0], 128, 64)
+    o2, e2 = moba.kv4_attend(torch.cat((q, q)), dst, lengths)
+    ok()
+    assert (o1 - o2[:3]).abs().max() <= 2e-2 and (e1 - e2[:, :3]).abs().max() <= 1e-3
+
+
+def test_calls_on_other_streams():
+    lengths = [900, 1500]
+    kv4, vals = random_cache(lengths, 2, 1536, 2)
+    q = bf16(np.random.default_rng(1).standard_normal((2, 8, 128))).cuda()
+    lens = ints(lengths)
+    want = moba.kv4_attend(q, kv4, lens)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for s in (a, b):
+            with torch.cuda.stream(s):
+                got.append(moba.kv4_attend(q, kv4, lens))
+    got.append(moba.kv4_attend(q, kv4, lens, stream=a))
+    ok()
+    for o, e in got:
+        assert torch.equal(o, want[0]) and torch.equal(e, want[1])
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_a_captured_decode_step_takes_the_lengths_of_its_replay(sparse):
+    rng = np.random.default_rng(6)
+    hkv, G, cap, B = 2, 4, 1024, 128
+    kv4, vals = random_cache([600, 300], hkv, cap, 2)
+    lengths, acc = ints([600, 300]), torch.zeros(2, hkv, cap, device="cuda")
+    k, v = (torch.zeros(2, hkv, 128, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    q = torch.zeros(2, hkv * G, 128, dtype=torch.bfloat16, device="cuda")
+    kmean = moba.kv4_pool(kv4, lengths, B)
+    out, lse = torch.empty_like(q), torch.empty(hkv * G, 2, device="cuda")
+    more = {"kmean": kmean, "block_size": B, "topk": 3} if sparse else {}
+
+    def step():
+        moba.kv4_append(k, v, kv4, lengths, acc=acc)
+        lengths.add_(1)
+        moba.kv4_pool(kv4, lengths, B, kmean=kmean)
+        moba.kv4_attend(q, kv4, lengths, acc=acc, out=out, lse=lse, **more)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    lengths.copy_(ints([600, 300]))
+    acc.zero_()
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    for g in (g1, g2):  # two captured graphs of the same step, replayed in turn
+        with torch.cuda.graph(g):
+            step()
+    n = [600, 300]
+    for i in range(6):
+        x = [bf16(rng.standard_normal((2, hkv, 128))) for _ in "kv"]
+        y = bf16(rng.standard_normal((2, hkv * G, 128)))
+        k.copy_(x[0]), v.copy_(x[1]), q.copy_(y)
+        a0 = acc.clone()
+        (g1, g2)[i % 2].replay()
+        ok()
+        for b in range(2):
+            for s in range(2):
+                vals[b][s][:, n[b]] = ref.stored(f64(x[s])[b])
+            a0[b, :, n[b]] = 0
+        n = [n[0] + 1, n[1] + 1]
+        assert lengths.tolist() == n
+        check_attend((out, lse, acc, a0), f64(y), vals, n, [1, 1], hkv, (B, 3) if sparse else None,
+                     f64(kmean) if sparse else None)
+
+
+def test_failed_scratch_allocation_returns_oom(monkeypatch):
+    kv4, _ = random_cache([64], 1, 64, 1)
+    q = torch.zeros(1, 1, 128, dtype=torch.bfloat16, device="cuda")
+    monkeypatch.setenv("MOBA_TEST_SCRATCH_PAD", str(1 << 46))
+    with pytest.raises(moba.MobaError) as e:
+        moba.kv4_attend(q, kv4, ints([64]))
+    assert e.value.code == moba.MOBA_ERR_OOM
+    monkeypatch.delenv("MOBA_TEST_SCRATCH_PAD")
+    moba.kv4_attend(q, kv4, ints([64]))
+    ok()
+
+
+def test_calls_without_rows_do_nothing():
+    kv4, _ = random_cache([64], 1, 64, 1)
+    none = torch.empty(0, 1, 128, dtype=torch.bfloat16, device="cuda")
+    moba.kv4_append(none, none, kv4, ints([0]))
+    out, lse = moba.kv4_attend(none, kv4, ints([64]))
+    k, v = moba.kv4_load(kv4, ints([64]), 0)
+    ok()
+    assert out.shape == (0, 1, 128) and lse.shape == (1, 0) and k.shape == (1, 0, 1, 128)
+
+
+def test_offsets_beyond_32_bits():
+    # the last head's tiles start beyond 2^32 bytes
+    hkv, cap = 8, 64 * 70000
+    kv4 = torch.zeros(1, hkv, cap // 64, 9216, dtype=torch.uint8, device="cuda")
+    assert kv4.numel() > 1 << 32
+    rng = np.random.default_rng(2)
+    L = cap - 5
+    new = bf16(rng.standard_normal((300, hkv, 128)))
+    acc = torch.zeros(1, hkv, cap, device="cuda")
+    moba.kv4_append(new.cuda(), new.flip(0).cuda(), kv4, ints([L - 300]))
+    k, v = moba.kv4_load(kv4, ints([L]), 300, first=ints([L - 300]))
+    ok()
+    assert np.array_equal(f64(k)[0], ref.stored(f64(new))) and np.array_equal(f64(v)[0], ref.stored(f64(new))[::-1])
+    # zero keys score 0 against every query: their weights are equal, and their values zero
+    q = bf16(rng.standard_normal((1, hkv * 2, 128)))
+    out, lse = moba.kv4_attend(q.cuda(), kv4, ints([L]), acc=acc)
+    ok()
+    for h in range(hkv):
+        kk, vv = f64(k)[0, :, h], f64(v)[0, :, h]
+        z = f64(q)[0, 2 * h:2 * h + 2] @ kk.T / np.sqrt(128)
+        total = np.exp(z).sum(-1) + (L - 300)
+        want = np.exp(z) @ vv / total[:, None]
+        # L sums of equal size: fp32 sums of at most L / 2^10 terms in a chain
+        assert np.abs(f64(lse)[2 * h:2 * h + 2, 0] - np.log(total)).max() <= 2.0**-12
+        assert (np.abs(f64(out)[0, 2 * h:2 * h + 2] - want) <= 2.0**-7 * np.abs(want) + 2.0**-10 * np.abs(vv).max() * 300 / L).all()
+    assert abs(f64(acc)[0].sum(-1) - 2).max() <= 2.0**-8
