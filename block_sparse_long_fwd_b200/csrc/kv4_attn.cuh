@@ -1,228 +1,924 @@
-// Attention of a few query tokens over the 4-bit key/value cache (kv4.cuh):
-// gate, attention and the accumulated weights of the cached tokens.
+// Attention of the last query tokens of each sequence over the 4-bit
+// key/value cache (kv4.cuh): gate, attention, join and the accumulated weights
+// of the cached tokens.
 //
 // Query token i of the n of sequence b stands at position
 // lengths[b] - n + i and attends the cached tokens up to itself: all of them,
 // or, with block means, those of its own block and of the topk - 1 past
 // blocks of the highest score q . mean (ties to the lower block index).
+//
+// Work is cut into units: R consecutive rows (token, q head of one kv head) of
+// one sequence and kv head, with the 64-token tiles of the cache that at least
+// one of them attends. All units' tiles in a row are dealt out evenly, one
+// contiguous range to each CTA of a grid of one CTA per SM, wherever the units
+// begin and end: lengths that differ, and few units with many tiles, balance
+// by themselves. A unit that several CTAs share leaves a partial result in
+// each, and a second kernel joins them.
 #pragma once
 
 #include "kv4.cuh"
 
 namespace moba {
 
+struct __align__(16) Kv4Unit {
+  int32_t b, h;       // sequence, kv head
+  int32_t row0, rows; // first row (token * G + q head) and rows of the unit
+  int32_t t0, pos0;   // packed index and position of the sequence's first query
+  int32_t tiles;      // 64-token tiles
+  int32_t blocks;     // with a gate: entries of the unit's block list
+};
+
 struct Kv4AttnParams {
   const __nv_bfloat16* q;  // [total][Hq][128]
   const uint8_t* kv4;
   const int32_t *lengths, *cu;  // cu null: total / batch queries each
-  const float* kmean;           // [batch][Hkv][blocks][128], or null: every key
+  const float* kmean;           // [batch][Hkv][means][128], or null: every key
   int64_t total, tiles;
   int batch, Hq, Hkv, G;
-  int B, topk, blocks;          // with kmean; blocks = capacity / B
+  int B, topk, means;           // with kmean: block size, means = capacity / B
+  int blocks;                   // blocks of the capacity, the last one partial
+  int R, slots;                 // rows of a unit; unit slots per kv head
   float scale_log2;             // log2(e) / sqrt(128)
-  int32_t* sel;                 // [total][Hq][topk] scratch: ascending, padded with -1
   float* acc;                   // [batch][Hkv][tiles * 64], or null
   __nv_bfloat16* out;           // [total][Hq][128]
   float* lse;                   // [Hq][total]
+  // scratch
+  Kv4Unit* units;               // [slots * Hkv]
+  int64_t* before;              // [slots * Hkv + 1]: tiles of the units before
+  int2* start;                  // [ctas]: first unit of a CTA's range, tiles of it before the range
+  uint2* list;                  // [slots * Hkv][list_cap]: (block, rows that chose it), ascending
+  uint32_t* chosen;             // [slots * Hkv][blocks]: rows of the unit that chose the block
+  double* scores;               // [clusters][R][means]
+  float* part;                  // [2 * ctas][R * 130]: O, then m and l
+  int list_cap, ctas;
 };
 
-// Sequence and position of packed query token t (b = -1: behind the last).
-__device__ __forceinline__ int kv4_query(const Kv4AttnParams& p, int64_t t, int* pos) {
-  int b;
-  int64_t i, n;
-  if (p.cu) {
-    b = kv4_sequence(p.cu, p.batch, t);
-    if (b < 0) return -1;
-    i = t - p.cu[b];
-    n = p.cu[b + 1] - p.cu[b];
-  } else {
-    n = p.total / p.batch;
-    b = (int)(t / n);
-    i = t - b * n;
+// Queries of sequence b: packed index of the first and their number. Offsets
+// outside the rows are a caller's error, recorded and read as no query.
+__device__ __forceinline__ int kv4_queries(const Kv4AttnParams& p, int b, int* t0) {
+  if (!p.cu) {
+    const int n = (int)(p.total / p.batch);
+    *t0 = b * n;
+    return n;
   }
-  *pos = (int)(kv4_length(p.lengths, b, p.tiles * kKv4Tile) - n + i);
-  return b;
+  const int c0 = p.cu[b], c1 = p.cu[b + 1];
+  *t0 = c0;
+  if (c0 < 0 || c1 < c0 || c1 > p.total) {
+    record_status(MOBA_ERR_DEVICE_CHECK);
+    return 0;
+  }
+  return c1 - c0;
 }
 
-constexpr int kKv4GateThreads = 128;
+// First unit slot of sequence b, whose rows start at row t0 * G of a kv head:
+// each sequence has room for its rows / R, rounded up, without a scan over the
+// sequences before it (floor(x / R) grows by at least ceil(n / R) - 1).
+__device__ __forceinline__ int64_t kv4_first_slot(const Kv4AttnParams& p, int b, int t0) {
+  return (int64_t)t0 * p.G / p.R + b;
+}
 
-// One CTA per row (token, q head): scores of its past blocks in fp64 (the
-// products of a bf16 and an fp32 number are exact there, so that near ties
-// fall as in exact arithmetic), then topk - 1 rounds of the best block after
-// the previous one.
+// The unit of slot `slot` of kv head h; rows = 0 for an unused slot. Called
+// by one thread.
+__device__ __forceinline__ Kv4Unit kv4_unit_of(const Kv4AttnParams& p, int slot, int h) {
+  Kv4Unit u = {};
+  u.h = h;
+  int lo = 0, hi = p.batch;  // first_slot(lo) <= slot < first_slot(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    const int t = p.cu ? p.cu[mid] : (int)(mid * (p.total / p.batch));
+    if (kv4_first_slot(p, mid, t) <= slot) lo = mid;
+    else hi = mid;
+  }
+  int t0;
+  const int n = kv4_queries(p, lo, &t0);
+  const int64_t first = kv4_first_slot(p, lo, t0);
+  const int64_t row0 = (slot - first) * p.R;
+  if (row0 < 0 || row0 >= (int64_t)n * p.G) return u;
+  u.b = lo;
+  u.row0 = (int)row0;
+  u.rows = min(p.R, (int)((int64_t)n * p.G - row0));
+  u.t0 = t0;
+  u.pos0 = kv4_length(p.lengths, lo, p.tiles * kKv4Tile) - n;
+  return u;
+}
+
+// Position of the unit's last row: the last key that any of its rows attends.
+__device__ __forceinline__ int kv4_last_pos(const Kv4AttnParams& p, const Kv4Unit& u) {
+  return u.pos0 + (u.row0 + u.rows - 1) / p.G;
+}
+
+// ------------------------------------------------------------------ gate
+
+constexpr int kKv4GateThreads = 256;
+constexpr int kKv4GateRegs = 8;  // scores a lane keeps: rows with up to 256 past blocks select from registers
+
+// The best candidate after (ps, pj) in (score descending, block ascending)
+// order, over the warp.
+__device__ __forceinline__ void kv4_warp_best(double& s, int& j) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    const double s2 = __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    const int j2 = __shfl_xor_sync(0xFFFFFFFFu, j, d);
+    if (j2 >= 0 && (j < 0 || s2 > s || (s2 == s && j2 < j))) {
+      s = s2;
+      j = j2;
+    }
+  }
+}
+
+__device__ __forceinline__ bool kv4_after(double s, int j, double ps, int pj) {
+  return pj < 0 || s < ps || (s == ps && j > pj);
+}
+
+__device__ __forceinline__ void kv4_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One cluster per unit (looping over units): its CTAs score the past blocks
+// for all rows of the unit, the first CTA selects and lists. Scores are sums
+// in fp64 of products that are exact there (bf16 times fp32), so near ties
+// fall as in exact arithmetic; they are a few per cent of the work of the
+// attention itself (one mean per block of at least 128 keys).
 __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
-  extern __shared__ double scores[];  // [blocks], then flags
-  __shared__ double best_s[kKv4GateThreads];
-  __shared__ int best_j[kKv4GateThreads];
-  const int64_t row = blockIdx.x;
-  const int64_t t = row / p.Hq;
-  const int hq = (int)(row - t * p.Hq), tid = threadIdx.x;
-  int32_t* sel = p.sel + row * p.topk;
-  int pos = -1;
-  const int b = kv4_query(p, t, &pos);
-  if (b < 0 || pos < 0) {
-    for (int i = tid; i < p.topk; i += kKv4GateThreads) sel[i] = -1;
-    return;
-  }
-  const int own = pos / p.B;
-  const float* means = p.kmean + ((int64_t)b * p.Hkv + hq / p.G) * p.blocks * kHeadDim;
-  const __nv_bfloat16* q = p.q + row * kHeadDim;
-  uint8_t* picked = reinterpret_cast<uint8_t*>(scores + p.blocks);
-  for (int j = tid; j < own; j += kKv4GateThreads) {
-    double s = 0.0;
-    for (int c = 0; c < kHeadDim; ++c)
-      s = fma((double)__bfloat162float(q[c]), (double)means[(int64_t)j * kHeadDim + c], s);
-    scores[j] = s;
-    picked[j] = 0;
-  }
-  __syncthreads();
-  const int picks = min(p.topk - 1, own);
-  for (int r = 0; r < picks; ++r) {
-    double s = 0.0;
-    int bj = -1;
-    for (int j = tid; j < own; j += kKv4GateThreads)
-      if (!picked[j] && (bj < 0 || scores[j] > s)) s = scores[j], bj = j;
-    best_s[tid] = s;
-    best_j[tid] = bj;
+  __shared__ float q[32][kHeadDim];
+  __shared__ Kv4Unit s_unit;
+  __shared__ uint32_t warp_sums[32];
+  uint32_t rank, csize;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+  const int cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  double* scores = p.scores + (int64_t)cluster * p.R * p.means;
+  const int nu = p.slots * p.Hkv;
+  for (int ui = cluster; ui < nu; ui += clusters) {
+    if (tid == 0) s_unit = kv4_unit_of(p, ui / p.Hkv, ui % p.Hkv);
     __syncthreads();
-    for (int d = kKv4GateThreads / 2; d > 0; d >>= 1) {
-      if (tid < d) {
-        const int o = best_j[tid + d], m = best_j[tid];
-        if (o >= 0 && (m < 0 || best_s[tid + d] > best_s[tid] || (best_s[tid + d] == best_s[tid] && o < m))) {
-          best_s[tid] = best_s[tid + d];
-          best_j[tid] = o;
+    Kv4Unit u = s_unit;
+    const int last = u.rows ? kv4_last_pos(p, u) : -1;
+    const int own = last < 0 ? 0 : last / p.B;  // past blocks of the last row
+    uint32_t* chosen = p.chosen + (int64_t)ui * p.blocks;
+    if (last >= 0) {
+      for (int i = tid; i < u.rows * kHeadDim; i += kKv4GateThreads) {
+        const int r = i / kHeadDim, c = i % kHeadDim, rr = u.row0 + r;
+        q[r][c] = __bfloat162float(
+            p.q[((int64_t)(u.t0 + rr / p.G) * p.Hq + u.h * p.G + rr % p.G) * kHeadDim + c]);
+      }
+      for (int j = rank * kKv4GateThreads + tid; j < p.blocks; j += csize * kKv4GateThreads) chosen[j] = 0;
+    }
+    __syncthreads();
+    if (last >= 0) {
+      const float* means = p.kmean + ((int64_t)u.b * p.Hkv + u.h) * p.means * kHeadDim;
+      const int n = min(own, p.means);
+      for (int j = rank * (kKv4GateThreads / 32) + warp; j < n; j += csize * (kKv4GateThreads / 32)) {
+        const float4 m = __ldg(reinterpret_cast<const float4*>(means + (int64_t)j * kHeadDim) + lane);
+        for (int r = 0; r < u.rows; ++r) {
+          const float4 x = *reinterpret_cast<const float4*>(&q[r][lane * 4]);
+          double s = (double)x.x * m.x;
+          s = fma((double)x.y, (double)m.y, s);
+          s = fma((double)x.z, (double)m.z, s);
+          s = fma((double)x.w, (double)m.w, s);
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+          if (lane == 0) scores[(int64_t)r * p.means + j] = s;
+        }
+      }
+    }
+    kv4_cluster_sync();
+    if (rank == 0) {
+      if (last >= 0) {
+        for (int r = warp; r < u.rows; r += kKv4GateThreads / 32) {
+          const int pos = u.pos0 + (u.row0 + r) / p.G;
+          if (pos < 0) continue;
+          const int mine = pos / p.B, picks = min(p.topk - 1, mine);
+          const uint32_t bit = 1u << r;
+          if (lane == 0) atomicOr(&chosen[mine], bit);
+          if (picks == mine) {
+            for (int j = lane; j < mine; j += 32) atomicOr(&chosen[j], bit);
+            continue;
+          }
+          const double* sc = scores + (int64_t)r * p.means;
+          double ps = 0.0;
+          int pj = -1;
+          if (mine <= 32 * kKv4GateRegs) {
+            double mv[kKv4GateRegs];
+#pragma unroll
+            for (int i = 0; i < kKv4GateRegs; ++i) mv[i] = i * 32 + lane < mine ? __ldcg(sc + i * 32 + lane) : 0.0;
+            for (int k = 0; k < picks; ++k) {
+              double s = 0.0;
+              int j = -1;
+#pragma unroll
+              for (int i = 0; i < kKv4GateRegs; ++i) {
+                const int jj = i * 32 + lane;
+                if (jj < mine && kv4_after(mv[i], jj, ps, pj) && (j < 0 || mv[i] > s)) s = mv[i], j = jj;
+              }
+              kv4_warp_best(s, j);
+              if (j < 0) break;  // only NaN scores are left
+              if (lane == 0) atomicOr(&chosen[j], bit);
+              ps = s;
+              pj = j;
+            }
+          } else {
+            for (int k = 0; k < picks; ++k) {
+              double s = 0.0;
+              int j = -1;
+              for (int jj = lane; jj < mine; jj += 32) {
+                const double v = __ldcg(sc + jj);
+                if (kv4_after(v, jj, ps, pj) && (j < 0 || v > s)) s = v, j = jj;
+              }
+              kv4_warp_best(s, j);
+              if (j < 0) break;
+              if (lane == 0) atomicOr(&chosen[j], bit);
+              ps = s;
+              pj = j;
+            }
+          }
         }
       }
       __syncthreads();
-    }
-    if (tid == 0 && best_j[0] >= 0) picked[best_j[0]] = 1;
-    __syncthreads();
-  }
-  if (tid == 0) {
-    int n = 0;
-    for (int j = 0; j < own && n < p.topk - 1; ++j)
-      if (picked[j]) sel[n++] = j;
-    sel[n++] = own;
-    while (n < p.topk) sel[n++] = -1;
-  }
-}
-
-constexpr int kKv4AttnThreads = 128;
-
-// Scaled log2 score of one key for half a warp: 8 channels a lane.
-__device__ __forceinline__ float kv4_score(const float (&q)[8], const uint8_t* tile, int tok, int lane) {
-  const uint32_t word = *reinterpret_cast<const uint32_t*>(tile + kv4_word_off(tok, lane, false));
-  const uint32_t par = *reinterpret_cast<const uint16_t*>(tile + kKv4Params + tok * 8 + (lane >> 2) * 2);
-  float x[8], s = 0.f;
-  kv4_decode(word, par, x);
-#pragma unroll
-  for (int c = 0; c < 8; ++c) s = fmaf(q[c], x[c], s);
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-  return s;
-}
-
-__device__ __forceinline__ void kv4_load_q(const Kv4AttnParams& p, int64_t row, int lane, float (&q)[8]) {
-  const uint4 raw = *(reinterpret_cast<const uint4*>(p.q + row * kHeadDim) + lane);
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    q[2 * j] = __uint_as_float(w[j] << 16);
-    q[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-  }
-}
-
-// One CTA per row; each half-warp takes every eighth key with a running
-// maximum and sum, and the eight are joined at the end.
-__global__ void __launch_bounds__(kKv4AttnThreads) kv4_attn_kernel(Kv4AttnParams p) {
-  grid_dependency_sync();
-  __shared__ float s_m[8], s_l[8], s_o[8][kHeadDim];
-  const int64_t row = blockIdx.x;
-  const int64_t t = row / p.Hq;
-  const int hq = (int)(row - t * p.Hq);
-  int pos = -1;
-  const int b = kv4_query(p, t, &pos);
-  if (b < 0) return;
-  const int lane = threadIdx.x & 15, hw = threadIdx.x >> 4;
-  float q[8], o[8] = {}, m = -INFINITY, l = 0.f;
-  kv4_load_q(p, row, lane, q);
-  const uint8_t* base = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, b, hq / p.G, 0);
-  const int32_t* sel = p.sel + row * p.topk;
-  const int parts = p.kmean ? p.topk : 1;
-  for (int i = 0; i < parts; ++i) {
-    int u0 = 0, u1 = pos + 1;
-    if (p.kmean) {
-      if (sel[i] < 0) break;
-      u0 = sel[i] * p.B;
-      u1 = min(u0 + p.B, pos + 1);
-    }
-    for (int u = u0 + (hw & ~1); u < u1; u += 8) {  // both halves of a warp stay together
-      const int key = u + (hw & 1);
-      const bool in = key < u1;
-      const uint8_t* tile = base + (int64_t)((in ? key : u) / kKv4Tile) * kKv4TileBytes;
-      const int tok = (in ? key : u) % kKv4Tile;
-      const float s = kv4_score(q, tile, tok, lane) * p.scale_log2;
-      if (!in) continue;
-      const float m2 = fmaxf(m, s);
-      const float a = exp2f(m - m2), e = exp2f(s - m2);
-      const uint8_t* half = tile + kKv4Half;
-      float x[8];
-      kv4_decode(*reinterpret_cast<const uint32_t*>(half + kv4_word_off(tok, lane, true)),
-                 *reinterpret_cast<const uint16_t*>(half + kKv4Params + tok * 8 + (lane >> 2) * 2), x);
-      l = l * a + e;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) o[c] = o[c] * a + e * x[c];
-      m = m2;
-    }
-  }
-  if (lane == 0) s_m[hw] = m, s_l[hw] = l;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) s_o[hw][lane * 8 + c] = o[c];
-  __syncthreads();
-  float mm = -INFINITY, ll = 0.f, oo = 0.f;
-  for (int i = 0; i < 8; ++i) mm = fmaxf(mm, s_m[i]);
-  if (mm > -INFINITY)
-    for (int i = 0; i < 8; ++i) {
-      const float a = exp2f(s_m[i] - mm);
-      ll += s_l[i] * a;
-      oo += s_o[i][threadIdx.x] * a;
-    }
-  p.out[row * kHeadDim + threadIdx.x] = __float2bfloat16(ll > 0.f ? oo / ll : 0.f);
-  if (threadIdx.x == 0)
-    p.lse[(int64_t)hq * p.total + t] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
-}
-
-// Accumulated weights: half a warp per cached token of a kv head, over the
-// rows of that head in order.
-__global__ void __launch_bounds__(kKv4AttnThreads) kv4_weight_kernel(Kv4AttnParams p) {
-  grid_dependency_sync();
-  const int b = blockIdx.z, h = blockIdx.y;
-  const int lane = threadIdx.x & 15;
-  const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
-  const int key = blockIdx.x * (kKv4AttnThreads / 16) + (threadIdx.x >> 4);
-  const bool in = key < len;
-  if (__all_sync(0xFFFFFFFFu, !in)) return;
-  const int64_t t0 = p.cu ? p.cu[b] : b * (p.total / p.batch), t1 = p.cu ? p.cu[b + 1] : t0 + p.total / p.batch;
-  const uint8_t* tile = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, b, h, (in ? key : 0) / kKv4Tile);
-  float sum = 0.f;
-  for (int64_t t = t0; t < t1; ++t) {
-    const int pos = (int)(len - (t1 - t));
-    for (int g = 0; g < p.G; ++g) {
-      const int hq = h * p.G + g;
-      const int64_t row = t * p.Hq + hq;
-      float q[8];
-      kv4_load_q(p, row, lane, q);
-      const float s = kv4_score(q, tile, (in ? key : 0) % kKv4Tile, lane) * p.scale_log2;
-      bool seen = in && key <= pos;
-      if (p.kmean && seen) {
-        seen = false;
-        for (int i = 0; i < p.topk; ++i) seen |= p.sel[row * p.topk + i] == key / p.B;
+      // the chosen blocks in order; the last one (the last row's own) may be partial
+      uint2* list = p.list + (int64_t)ui * p.list_cap;
+      uint32_t n = 0;
+      if (last >= 0) {
+        for (int j0 = 0; j0 <= own; j0 += kKv4GateThreads) {
+          const int j = j0 + tid;
+          const uint32_t rows = j <= own ? __ldcg(chosen + j) : 0;
+          uint32_t total;
+          const uint32_t at = n + kv4_block_scan(rows != 0, warp_sums, &total);
+          if (rows && at < (uint32_t)p.list_cap) list[at] = make_uint2(j, rows);
+          n += total;
+        }
+        n = min(n, (uint32_t)p.list_cap);
       }
-      if (seen) sum += exp2f(s - p.lse[(int64_t)hq * p.total + t] * 1.4426950408889634f);
+      if (tid == 0) {
+        u.blocks = n;
+        u.tiles = n ? (int)(n - 1) * (p.B / kKv4Tile) + (last - own * p.B) / kKv4Tile + 1 : 0;
+        p.units[ui] = u;
+      }
+    }
+    // the next unit reuses the scores
+    kv4_cluster_sync();
+  }
+}
+
+// ------------------------------------------------------------------ plan
+
+// CTAs that get a range of `all` tiles: every one gets at least a tile.
+__device__ __forceinline__ int kv4_ctas(const Kv4AttnParams& p, int64_t all) {
+  return (int)min((int64_t)p.ctas, all);
+}
+
+constexpr int kKv4PlanThreads = 1024;
+
+// One CTA: the units (the gate has already written them where there is one),
+// the tiles before each, and where each CTA's range starts.
+__global__ void __launch_bounds__(kKv4PlanThreads) kv4_plan_kernel(Kv4AttnParams p) {
+  grid_dependency_sync();
+  __shared__ int64_t warp_sums[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nu = p.slots * p.Hkv;
+  int64_t done = 0;
+  for (int u0 = 0; u0 < nu; u0 += kKv4PlanThreads) {
+    const int ui = u0 + tid;
+    int64_t tiles = 0;
+    if (ui < nu) {
+      if (p.kmean) {
+        tiles = p.units[ui].tiles;
+      } else {
+        Kv4Unit u = kv4_unit_of(p, ui / p.Hkv, ui % p.Hkv);
+        const int last = u.rows ? kv4_last_pos(p, u) : -1;
+        u.tiles = last < 0 ? 0 : last / kKv4Tile + 1;
+        tiles = u.tiles;
+        p.units[ui] = u;
+      }
+    }
+    int64_t s = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, d);
+      if (lane >= d) s += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = s;
+    __syncthreads();
+    int64_t base = done;
+    for (int i = 0; i < 32; ++i) {
+      if (i < warp) base += warp_sums[i];
+      done += warp_sums[i];
+    }
+    if (ui < nu) p.before[ui] = base + s - tiles;
+  }
+  if (tid == 0) p.before[nu] = done;
+  __syncthreads();
+  const int ctas = kv4_ctas(p, done);
+  for (int c = tid; c < ctas; c += kKv4PlanThreads) {
+    const int64_t x = done * c / ctas;
+    int lo = 0, hi = nu;  // the last unit that begins at or before tile x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.before[mid] <= x) lo = mid;
+      else hi = mid;
+    }
+    p.start[c] = make_int2(lo, (int)(x - p.before[lo]));
+  }
+}
+
+// ------------------------------------------------------------------ attention
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 x 8 transpose of 16-bit values held by a warp.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+// Scale and zero point of two parameters (low and high half), ready for the
+// four nibbles of a 16-bit code group: a nibble at bit 0 under fp16's 1024 is
+// 1024 + c, at bit 4 it is 1024 + 16 c; minus 1024 + z, or over 16 minus
+// 64 + z, leaves c - z, and the product with the scale is exact.
+struct Kv4Par {
+  uint32_t s, z, z16;
+};
+__device__ __forceinline__ Kv4Par kv4_par(uint32_t pp) {
+  Kv4Par r;
+  r.s = pp & 0x7F807F80u;
+  r.z = (pp & 0x000F000Fu) | 0x64006400u;
+  r.z16 = h2_sub(0x63806380u, r.z);  // 960 - (1024 + z)
+  return r;
+}
+__device__ __forceinline__ void kv4_pairs(uint32_t w, const Kv4Par& p, uint32_t (&x)[4]) {
+  const uint32_t h = w >> 8;
+  x[0] = h2_mul(h2_sub((w & 0x000F000Fu) | 0x64006400u, p.z), p.s);
+  x[1] = h2_mul(h2_fma((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, p.z16), p.s);
+  x[2] = h2_mul(h2_sub((h & 0x000F000Fu) | 0x64006400u, p.z), p.s);
+  x[3] = h2_mul(h2_fma((h & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, p.z16), p.s);
+}
+
+// A query row enters the products as fp16: times the power of two that brings
+// its largest channel to [2^14, 2^15). bf16's eight bits then stay exact but
+// for channels 2^29 times smaller than the largest. Returns the row's fragment
+// of this lane (channels 32 (lane % 4) .. + 31 as eight steps of two pairs) and
+// the scale that turns its products into log2 scores.
+__device__ __forceinline__ float kv4_query_fragment(const __nv_bfloat16* row, float scale_log2, uint32_t (&f)[16]) {
+  uint4 raw[4] = {};
+  if (row) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(row) + i);
+  }
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
+  uint32_t top = 0;  // largest magnitude, as bf16 bits (a NaN above all)
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+  top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+  top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+  const int e = (int)(top >> 7);  // biased exponent; 0: zero or subnormal, 255: not finite
+  // 2^k with e - 127 + k = 14, in two factors that are normal numbers
+  const int k = (e == 0 || e == 255) ? 0 : 141 - e;
+  const int k1 = k / 2, k2 = k - k1;
+  const float f1 = __int_as_float((127 + k1) << 23), f2 = __int_as_float((127 + k2) << 23);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    f[i] = pack_half2(__uint_as_float(w[i] << 16) * f1 * f2, __uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2);
+  return scale_log2 * __int_as_float((127 - k1) << 23) * __int_as_float((127 - k2) << 23);
+}
+
+// Token (of 16) that row r of the score product holds: neighbours, swapped
+// for every other pair, so that the value rows which a lane quad reads next
+// are two of even and two of odd index.
+__device__ __forceinline__ int kv4_token_of(int r) { return (r & ~1) | ((r ^ (r >> 1)) & 1); }
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+template <int NT_, int WARPS_, int DEPTH_>
+struct Kv4Cfg {
+  static constexpr int NT = NT_;            // groups of eight query rows
+  static constexpr int R = 8 * NT;
+  static constexpr int WARPS = WARPS_;
+  static constexpr int DEPTH = DEPTH_;      // half tiles a warp holds: one in use, the others on their way
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int OLD = kHeadDim + 4;  // row stride of the O exchange (spreads the quads over the banks)
+  static constexpr bool QREG = NT == 1;     // query fragments in registers, else in shared memory
+  struct Shared {
+    uint8_t ring[WARPS][DEPTH][kKv4Half];   // 32 tokens: key codes, key parameters, value codes, value parameters
+    float o[WARPS][R][OLD];
+    float2 ml[2][WARPS][R];
+    uint2 q[QREG ? 1 : NT][8][32];
+    float qs[R];
+    uint64_t full[WARPS][DEPTH];
+    int2 info[WARPS][DEPTH];                // first key of the half tile, rows that attend it
+    int abort_flag;
+  };
+};
+
+using Kv4Few = Kv4Cfg<1, 16, 2>;   // up to 8 rows
+using Kv4Many = Kv4Cfg<4, 8, 2>;   // up to 32 rows
+
+constexpr int kKv4HalfTok = kKv4Tile / 2;
+constexpr int kKv4HalfParams = kKv4HalfTok * kKv4Row;         // 2048: offset of the parameters of 32 tokens
+constexpr int kKv4HalfRows = kKv4HalfParams + kKv4HalfTok * 8;  // 2304: their keys (or values)
+constexpr float kKv4Low = -1e30f;  // running maximum before the first score
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p) {
+  constexpr int NT = C::NT, R = C::R;
+  grid_dependency_sync();
+  extern __shared__ uint8_t smem_raw[];
+  auto* sh = reinterpret_cast<typename C::Shared*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::WARPS * C::DEPTH; ++i) mbar_init(&sh->full[0][0] + i, 1);
+    sh->abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const int64_t all = p.before[p.slots * p.Hkv];
+  const int ctas = kv4_ctas(p, all);
+  if (cta >= ctas) return;
+  const int n = (int)(all * (cta + 1) / ctas - all * cta / ctas);  // tiles of this CTA, at least one
+  const int2 start = p.start[cta];
+
+  // Every warp works alone on half tiles (32 tokens) warp, warp + WARPS, ... of the CTA's range and fetches its own
+  // ahead: the four pieces of one by bulk copies of four lanes. `issue` walks the units as far as its half tile.
+  int c_ui = start.x, c_base = -2 * start.y, c_end = c_base + 2 * p.units[start.x].tiles;
+  auto issue = [&](int k) {
+    const int x = warp + C::WARPS * k;
+    if (x >= 2 * n) return;
+    while (x >= c_end) {
+      c_base = c_end;
+      c_end += 2 * p.units[++c_ui].tiles;
+    }
+    const int off = (x - c_base) >> 1;
+    int key = off * kKv4Tile;
+    uint32_t rows = 0xFFFFFFFFu;
+    if (p.kmean) {
+      const int tpb = p.B / kKv4Tile, at = off / tpb;
+      const uint2 e = p.list[(int64_t)c_ui * p.list_cap + at];
+      key = (int)e.x * p.B + (off - at * tpb) * kKv4Tile;
+      rows = e.y;
+    }
+    const int half = x & 1, d = k % C::DEPTH;
+    uint64_t* bar = &sh->full[warp][d];
+    if (lane == 0) {
+      sh->info[warp][d] = make_int2(key + half * kKv4HalfTok, (int)rows);
+      mbar_arrive_expect_tx(bar, 2 * kKv4HalfRows);
+    }
+    __syncwarp();
+    if (lane < 4) {
+      const Kv4Unit& u = p.units[c_ui];
+      const int par = lane & 1, vals = lane >> 1;
+      const uint8_t* src = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, u.b, u.h, key / kKv4Tile) + vals * kKv4Half +
+                           (par ? kKv4Params + half * (kKv4HalfTok * 8) : half * kKv4HalfParams);
+      bulk_load(sh->ring[warp][d] + vals * kKv4HalfRows + par * kKv4HalfParams, src,
+                par ? kKv4HalfTok * 8 : kKv4HalfParams, bar);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < C::DEPTH; ++k) issue(k);
+
+  const int r = lane >> 2, qd = lane & 3;
+  const int tok0 = kv4_token_of(r);
+  const int vchunk = (r ^ (qd & 2 ? 4 : 0)) * 8;
+  const int ve0 = 2 * qd + (qd & 1), ve1 = 2 * qd + ((qd & 1) ^ 1);
+  bool dead = false;
+  int death = 0;  // the half tile that never came
+  int done = 0, seg = 0, k = 0;  // tiles of the range behind us, units, half tiles of this warp
+  for (int ui = start.x, off = start.y; done < n; ++ui, off = 0) {
+    const Kv4Unit u = p.units[ui];
+    if (u.tiles <= off) continue;
+    const int take = min(n - done, u.tiles - off);
+    // the rows' fragments, scales, and last keys (of this lane's two rows of each group of eight)
+    uint32_t qf[16];
+    float qs[NT][2];
+    int last[NT][2];
+    const int first_pos = u.pos0 + u.row0 / p.G, last_pos = kv4_last_pos(p, u);
+    if constexpr (C::QREG) {
+      const int rr = u.row0 + r;
+      const __nv_bfloat16* row =
+          r < u.rows ? p.q + ((int64_t)(u.t0 + rr / p.G) * p.Hq + u.h * p.G + rr % p.G) * kHeadDim + qd * 32 : nullptr;
+      const float s = kv4_query_fragment(row, p.scale_log2, qf);
+      qs[0][0] = __shfl_sync(0xFFFFFFFFu, s, qd * 8);
+      qs[0][1] = __shfl_sync(0xFFFFFFFFu, s, qd * 8 + 4);
+    } else {
+      // every warp is past the previous unit's tiles (the exchange's barriers)
+      for (int nt = warp; nt < NT; nt += C::WARPS) {
+        const int x = nt * 8 + r, rr = u.row0 + x;
+        const __nv_bfloat16* row =
+            x < u.rows ? p.q + ((int64_t)(u.t0 + rr / p.G) * p.Hq + u.h * p.G + rr % p.G) * kHeadDim + qd * 32
+                       : nullptr;
+        const float s = kv4_query_fragment(row, p.scale_log2, qf);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sh->q[nt][i][lane] = make_uint2(qf[2 * i], qf[2 * i + 1]);
+        if (qd == 0) sh->qs[x] = s;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) qs[nt][0] = sh->qs[nt * 8 + 2 * qd], qs[nt][1] = sh->qs[nt * 8 + 2 * qd + 1];
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int row = nt * 8 + 2 * qd + x;
+        last[nt][x] = row < u.rows ? u.pos0 + (u.row0 + row) / p.G : -1;
+      }
+    const uint32_t all_rows = u.rows == 32 ? 0xFFFFFFFFu : (1u << u.rows) - 1;
+
+    float o[NT][8][4] = {}, m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = kKv4Low, l[nt][0] = l[nt][1] = 0.f;
+
+    for (; warp + C::WARPS * k < 2 * (done + take); ++k) {
+      const int d = k % C::DEPTH;
+      if (!dead && !mbar_wait(&sh->full[warp][d], (k / C::DEPTH) & 1, &sh->abort_flag)) dead = true, death = k;
+      if (dead) continue;
+      const uint8_t* kt = sh->ring[warp][d];
+      const uint8_t* vt = kt + kKv4HalfRows;
+      const int2 info = sh->info[warp][d];
+
+      // scores: keys x rows, 16 keys at a time
+      float sc[2][NT][4];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int ta = tok0 + g * 16, tb = ta + 8;
+        const uint4 wa = *reinterpret_cast<const uint4*>(kt + ta * kKv4Row + qd * 16);
+        const uint4 wb = *reinterpret_cast<const uint4*>(kt + tb * kKv4Row + qd * 16);
+        const uint32_t pa = *reinterpret_cast<const uint16_t*>(kt + kKv4HalfParams + ta * 8 + qd * 2);
+        const uint32_t pb = *reinterpret_cast<const uint16_t*>(kt + kKv4HalfParams + tb * 8 + qd * 2);
+        const Kv4Par fa = kv4_par(__byte_perm(pa, 0, 0x1010)), fb = kv4_par(__byte_perm(pb, 0, 0x1010));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sc[g][nt][0] = sc[g][nt][1] = sc[g][nt][2] = sc[g][nt][3] = 0.f;
+        const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xb[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t a[4], b[4];
+          kv4_pairs(xa[w], fa, a);
+          kv4_pairs(xb[w], fb, b);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint2 q0, q1;
+            if constexpr (C::QREG) {
+              q0 = make_uint2(qf[4 * w], qf[4 * w + 1]);
+              q1 = make_uint2(qf[4 * w + 2], qf[4 * w + 3]);
+            } else {
+              q0 = sh->q[nt][2 * w][lane];
+              q1 = sh->q[nt][2 * w + 1][lane];
+            }
+            mma_f16(sc[g][nt], a[0], b[0], a[1], b[1], q0.x, q0.y);
+            mma_f16(sc[g][nt], a[2], b[2], a[3], b[3], q1.x, q1.y);
+          }
+        }
+      }
+      // keys behind a row's position, and blocks that a row did not choose
+      const bool edge = info.x + kKv4HalfTok - 1 > first_pos;
+      if (edge || ((uint32_t)info.y & all_rows) != all_rows) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int key = info.x + tok0 + g * 16 + (x >> 1) * 8;
+              const uint32_t row = nt * 8 + 2 * qd + (x & 1);
+              if (key > last[nt][x & 1] || !((uint32_t)info.y >> row & 1u)) sc[g][nt][x] = -INFINITY;
+            }
+      }
+      // weights 2^(score - m). The reference m moves when a score exceeds it by more than 15, to 12 below
+      // the largest: weights then lie under 2^15, which fp16 holds, and end 2^-37 below the largest
+      uint32_t pf[NT][2][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float t[2][4], top = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            t[g][x] = fmaf(sc[g][nt][x], qs[nt][x & 1], -m[nt][x & 1]);
+            top = fmaxf(top, t[g][x]);
+          }
+        if (__any_sync(0xFFFFFFFFu, top > 15.f)) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float mx = fmaxf(fmaxf(sc[0][nt][x], sc[0][nt][x + 2]), fmaxf(sc[1][nt][x], sc[1][nt][x + 2])) * qs[nt][x];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+            if (mx > m[nt][x] + 15.f) {
+              const float a = ex2_approx(m[nt][x] - (mx - 12.f));
+              m[nt][x] = mx - 12.f;
+              l[nt][x] *= a;
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt) o[nt][mt][x] *= a, o[nt][mt][x + 2] *= a;
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) t[g][x] = fmaf(sc[g][nt][x], qs[nt][x & 1], -m[nt][x & 1]);
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float e[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) e[x] = ex2_approx(t[g][x]);
+          l[nt][0] += e[0] + e[2];
+          l[nt][1] += e[1] + e[3];
+          pf[nt][g][0] = movmatrix(pack_half2(e[0], e[1]));
+          pf[nt][g][1] = movmatrix(pack_half2(e[2], e[3]));
+        }
+      }
+      // O^T += V^T P^T: channels x rows
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint2 w[2][2];
+        Kv4Par fp[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int t0 = ve0 + g * 16 + f * 8, t1 = ve1 + g * 16 + f * 8;
+          w[f][0] = *reinterpret_cast<const uint2*>(vt + t0 * kKv4Row + vchunk);
+          w[f][1] = *reinterpret_cast<const uint2*>(vt + t1 * kKv4Row + vchunk);
+          uint32_t p0 = *reinterpret_cast<const uint16_t*>(vt + kKv4HalfParams + t0 * 8 + (r >> 1) * 2);
+          uint32_t p1 = *reinterpret_cast<const uint16_t*>(vt + kKv4HalfParams + t1 * 8 + (r >> 1) * 2);
+          if (edge) {  // what lies behind the last token may hold anything
+            if (info.x + t0 > last_pos) p0 = 0;
+            if (info.x + t1 > last_pos) p1 = 0;
+          }
+          fp[f] = kv4_par(__byte_perm(p0, p1, 0x5410));
+        }
+        if (g == 1) {  // the half tile is in registers: fetch the next one into its place
+          __syncwarp();
+          issue(k + C::DEPTH);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a[2][2][4];  // [channel parity][keys 0-7, 8-15][nibble]
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const uint32_t x0 = h ? w[f][0].y : w[f][0].x, x1 = h ? w[f][1].y : w[f][1].x;
+            kv4_pairs(__byte_perm(x0, x1, 0x5410), fp[f], a[0][f]);
+            kv4_pairs(__byte_perm(x0, x1, 0x7632), fp[f], a[1][f]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(o[nt][h * 4 + j], a[0][0][j], a[1][0][j], a[0][1][j], a[1][1][j], pf[nt][g][0], pf[nt][g][1]);
+        }
+      }
+    }
+
+    // ---- join the warps' results
+    float2(&ml)[C::WARPS][R] = sh->ml[seg & 1];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][x], d);
+        if (r == 0) ml[warp][nt * 8 + 2 * qd + x] = make_float2(m[nt][x], l[nt][x]);
+      }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int row = nt * 8 + 2 * qd + x;
+        float mm = kKv4Low;
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, ml[w][row].x);
+        const float a = ex2_approx(m[nt][x] - mm);
+        // channel 16 r + c lies at c * 8 + r: the lanes of a quad column fall on neighbouring banks
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          sh->o[warp][row][(2 * mt) * 8 + r] = o[nt][mt][x] * a;
+          sh->o[warp][row][(2 * mt + 1) * 8 + r] = o[nt][mt][x + 2] * a;
+        }
+      }
+    __syncthreads();
+    const bool whole = off == 0 && take == u.tiles;
+    float* part = p.part + (int64_t)(2 * cta + (off == 0 ? 1 : 0)) * (R * 130);
+    for (int idx = threadIdx.x; idx < u.rows * kHeadDim; idx += C::THREADS) {
+      const int row = idx >> 7, at = idx & 127;
+      float mm = kKv4Low, ll = 0.f, oo = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, ml[w][row].x);
+#pragma unroll
+      for (int w = 0; w < C::WARPS; ++w) {
+        const float2 x = ml[w][row];
+        ll += x.y * ex2_approx(x.x - mm);
+        oo += sh->o[w][row][at];
+      }
+      if (whole) {
+        const int rr = u.row0 + row;
+        const int64_t t = u.t0 + rr / p.G;
+        const int hq = u.h * p.G + rr % p.G;
+        p.out[(t * p.Hq + hq) * kHeadDim + (at & 7) * 16 + (at >> 3)] = __float2bfloat16(ll > 0.f ? oo / ll : 0.f);
+        if (at == 0) p.lse[(int64_t)hq * p.total + t] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+      } else {
+        part[idx] = oo;
+        if (at == 0) {
+          part[R * kHeadDim + 2 * row] = mm;
+          part[R * kHeadDim + 2 * row + 1] = ll;
+        }
+      }
+    }
+    done += take;
+    ++seg;
+  }
+  if (dead) {
+    // the block's shared memory lives until the copies under way have landed
+    const int issued = min(death + C::DEPTH, (2 * n - warp + C::WARPS - 1) / C::WARPS);
+    for (int i = death; i < issued; ++i) {
+      const uint64_t t0 = clock64();
+      while (!mbar_try_wait(&sh->full[warp][i % C::DEPTH], (i / C::DEPTH) & 1) &&
+             (uint64_t)(clock64() - t0) < (1ull << 31)) {
+      }
     }
   }
-  if (in && lane == 0) p.acc[((int64_t)b * p.Hkv + h) * p.tiles * kKv4Tile + key] += sum;
+}
+
+// ------------------------------------------------------------------ join
+
+constexpr int kKv4JoinThreads = 128;
+
+// The CTA whose range holds tile x of `all`.
+__device__ __forceinline__ int kv4_cta_of(int64_t x, int64_t all, int ctas) {
+  return (int)(((x + 1) * ctas + all - 1) / all) - 1;
+}
+
+// One warp per (unit, row) whose tiles lie in more than one CTA's range: the
+// partial results in order. Rows without keys get their zero here.
+__global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams p) {
+  grid_dependency_sync();
+  const int lane = threadIdx.x & 31;
+  const int64_t idx = ((int64_t)blockIdx.x * kKv4JoinThreads + threadIdx.x) >> 5;
+  const int ui = (int)(idx / p.R), row = (int)(idx % p.R);
+  if (ui >= p.slots * p.Hkv) return;
+  const Kv4Unit u = p.units[ui];
+  if (row >= u.rows) return;
+  int c0 = 0, c1 = -1;
+  if (u.tiles) {
+    const int64_t all = p.before[p.slots * p.Hkv], x = p.before[ui];
+    const int ctas = kv4_ctas(p, all);
+    c0 = kv4_cta_of(x, all, ctas);
+    c1 = kv4_cta_of(x + u.tiles - 1, all, ctas);
+    if (c0 == c1) return;  // written by the CTA itself
+  }
+  const int per = p.R * 130;
+  float mm = kKv4Low, ll = 0.f;
+  float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0; c <= c1; ++c) {
+    const float* part = p.part + (int64_t)(2 * c + (c == c0 ? 1 : 0)) * per;
+    const float2 x = __ldcg(reinterpret_cast<const float2*>(part + p.R * kHeadDim) + row);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(part + row * kHeadDim) + lane);
+    const float m2 = fmaxf(mm, x.x);
+    const float a = ex2_approx(mm - m2), e = ex2_approx(x.x - m2);
+    ll = ll * a + x.y * e;
+    oo.x = oo.x * a + v.x * e;
+    oo.y = oo.y * a + v.y * e;
+    oo.z = oo.z * a + v.z * e;
+    oo.w = oo.w * a + v.w * e;
+    mm = m2;
+  }
+  const int rr = u.row0 + row;
+  const int64_t t = u.t0 + rr / p.G;
+  const int hq = u.h * p.G + rr % p.G;
+  const float inv = ll > 0.f ? 1.f / ll : 0.f;
+  __nv_bfloat16* out = p.out + (t * p.Hq + hq) * kHeadDim;
+  const float v[4] = {oo.x, oo.y, oo.z, oo.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = lane * 4 + i;
+    out[(at & 7) * 16 + (at >> 3)] = __float2bfloat16(v[i] * inv);
+  }
+  if (lane == 0) p.lse[(int64_t)hq * p.total + t] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+}
+
+// ------------------------------------------------------------------ accumulated weights
+
+constexpr int kKv4WeightThreads = 128;
+
+// acc[key] += sum over the rows of the kv head of 2^(score - lse): one warp per
+// 64-token tile, whose keys it widens once and holds in registers; all rows of
+// the sequence pass by, eight at a time, in order.
+__global__ void __launch_bounds__(kKv4WeightThreads, 2) kv4_weight_kernel(Kv4AttnParams p) {
+  grid_dependency_sync();
+  const int lane = threadIdx.x & 31, r = lane >> 2, qd = lane & 3;
+  const int64_t tile = (int64_t)blockIdx.x * (kKv4WeightThreads / 32) + (threadIdx.x >> 5);
+  const int b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
+  int t0;
+  const int n = kv4_queries(p, b, &t0);
+  const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
+  const int key0 = (int)(tile * kKv4Tile), pos0 = len - n, rows = n * p.G;
+  if (n == 0 || key0 >= len || tile >= p.tiles) return;
+  const int64_t slot0 = kv4_first_slot(p, b, t0);
+  const int block = key0 / p.B;
+  const uint8_t* kt = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, b, h, tile);
+  uint32_t a[4][4][8];  // [16 keys][word][pair of the first, of the second eight keys]
+  bool loaded = false;
+  float sum[4][2] = {};
+  // rows before the first key's position attend nothing here
+  int r0 = key0 > pos0 ? (key0 - pos0) * p.G / 8 * 8 : 0;
+  for (; r0 < rows; r0 += 8) {
+    uint32_t picked = 0xFFu;
+    if (p.kmean) {
+      const int64_t ui = (slot0 + r0 / p.R) * p.Hkv + h;
+      picked = p.chosen[ui * p.blocks + block] >> (r0 % p.R) & 0xFFu;
+      if (!picked) continue;
+    }
+    if (!loaded) {
+      loaded = true;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int ta = g * 16 + r, tb = ta + 8;
+        const uint4 wa = __ldg(reinterpret_cast<const uint4*>(kt + ta * kKv4Row + qd * 16));
+        const uint4 wb = __ldg(reinterpret_cast<const uint4*>(kt + tb * kKv4Row + qd * 16));
+        const uint32_t pa = __ldg(reinterpret_cast<const uint16_t*>(kt + kKv4Params + ta * 8 + qd * 2));
+        const uint32_t pb = __ldg(reinterpret_cast<const uint16_t*>(kt + kKv4Params + tb * 8 + qd * 2));
+        const Kv4Par fa = kv4_par(__byte_perm(pa, 0, 0x1010)), fb = kv4_par(__byte_perm(pb, 0, 0x1010));
+        const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xb[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t y[4], z[4];
+          kv4_pairs(xa[w], fa, y);
+          kv4_pairs(xb[w], fb, z);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a[g][w][2 * j] = y[j], a[g][w][2 * j + 1] = z[j];
+        }
+      }
+    }
+    uint32_t qf[16];
+    const int rr = r0 + r;
+    const __nv_bfloat16* row =
+        rr < rows ? p.q + ((int64_t)(t0 + rr / p.G) * p.Hq + h * p.G + rr % p.G) * kHeadDim + qd * 32 : nullptr;
+    const float s = kv4_query_fragment(row, p.scale_log2, qf);
+    // this lane's two rows: scale, log2 of the sum, last key
+    float qs[2], le[2];
+    int last[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      qs[x] = __shfl_sync(0xFFFFFFFFu, s, (2 * qd + x) * 4);
+      const int row2 = r0 + 2 * qd + x;
+      const bool on = row2 < rows && (picked >> (2 * qd + x) & 1u);
+      last[x] = on ? pos0 + row2 / p.G : -1;
+      le[x] = on ? p.lse[(int64_t)(h * p.G + row2 % p.G) * p.total + t0 + row2 / p.G] * 1.4426950408889634f : 0.f;
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float sc[4] = {};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        mma_f16(sc, a[g][w][0], a[g][w][1], a[g][w][2], a[g][w][3], qf[4 * w], qf[4 * w + 1]);
+        mma_f16(sc, a[g][w][4], a[g][w][5], a[g][w][6], a[g][w][7], qf[4 * w + 2], qf[4 * w + 3]);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int key = key0 + g * 16 + r + (x >> 1) * 8;
+        const float e = ex2_approx(fmaf(sc[x], qs[x & 1], -le[x & 1]));
+        if (key <= last[x & 1]) sum[g][x >> 1] += e;
+      }
+    }
+  }
+  if (!loaded) return;
+  float* acc = p.acc + ((int64_t)b * p.Hkv + h) * p.tiles * kKv4Tile + key0;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float v = sum[g][x];
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+      const int at = g * 16 + x * 8 + r;
+      if (qd == 0 && key0 + at < len) acc[at] += v;
+    }
 }
 
 }  // namespace moba

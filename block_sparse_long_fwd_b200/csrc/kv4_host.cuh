@@ -33,10 +33,38 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+template <class C>
+constexpr size_t kv4_attn_smem() {
+  return sizeof(typename C::Shared) + 128;
+}
+
+template <class C>
+void launch_kv4_attn(const moba::Kv4AttnParams& p, cudaStream_t st) {
+  launch_chained(moba::kv4_attn_kernel<C>, dim3(p.ctas), dim3(C::THREADS), kv4_attn_smem<C>(), st, p);
+}
+
+template <class C>
+cudaError_t set_kv4_attn_smem() {
+  return cudaFuncSetAttribute(moba::kv4_attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)kv4_attn_smem<C>());
+}
+
+bool g_kv4_ready[64] = {};
+
 // The device, and an error that an earlier call's kernels left behind.
 int kv4_begin(DeviceInfo* dev, cudaStream_t st) {
   int rc = device_info(dev);
   if (rc) return rc;
+  int d = 0;
+  MOBA_CUDA(cudaGetDevice(&d));
+  {
+    std::lock_guard<std::mutex> lk(g_dev_mu);
+    if (!g_kv4_ready[d]) {
+      MOBA_CUDA(set_kv4_attn_smem<moba::Kv4Few>());
+      MOBA_CUDA(set_kv4_attn_smem<moba::Kv4Many>());
+      g_kv4_ready[d] = true;
+    }
+  }
   return take_pending_status(*dev, st);
 }
 
@@ -178,26 +206,70 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   p.Hq = heads_q;
   p.Hkv = heads_kv;
   p.G = heads_q / heads_kv;
-  p.B = kmean ? block_size : 1;
-  p.topk = kmean ? topk : 1;
-  p.blocks = kmean ? (int)(capacity / block_size) : 0;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)moba::kHeadDim));
   p.acc = acc;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
+  p.B = kmean ? block_size : moba::kKv4Tile;
+  p.topk = kmean ? topk : 0;
+  p.means = kmean ? (int)(capacity / block_size) : 0;
+  p.blocks = kmean ? (int)((capacity + block_size - 1) / block_size) : 0;
+  const bool few = total * p.G <= (int64_t)moba::Kv4Few::R * batch;
+  p.R = few ? moba::Kv4Few::R : moba::Kv4Many::R;
+  const int64_t slots = total * p.G / p.R + batch;
+  if (slots * heads_kv > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
+  p.slots = (int)slots;
+  p.ctas = dev.sms;
+  const int64_t nu = slots * heads_kv;
+  p.list_cap = kmean ? (int)std::min<int64_t>(p.blocks, (int64_t)p.R * topk) : 0;
+  // the gate: up to 8 CTAs share a unit's scores while there are few units
+  int csize = 1;
+  while (csize < 8 && nu * csize * 2 <= dev.sms) csize *= 2;
+  const int64_t clusters = std::min<int64_t>(nu, 4 * dev.sms / csize);
+  Carve c;
+  const size_t o_units = c.take((size_t)nu * sizeof(moba::Kv4Unit)), o_before = c.take((size_t)(nu + 1) * 8);
+  const size_t o_start = c.take((size_t)p.ctas * 8), o_list = c.take((size_t)nu * p.list_cap * 8);
+  const size_t o_chosen = c.take((size_t)nu * p.blocks * 4);
+  const size_t o_scores = c.take((size_t)clusters * p.R * p.means * 8);
+  const size_t o_part = c.take((size_t)2 * p.ctas * p.R * 130 * 4);
   const Runner run = [&](uint8_t* ws, cudaStream_t st) -> int {
-    p.sel = reinterpret_cast<int32_t*>(ws);
-    const dim3 rows((unsigned)(total * heads_q));
-    if (kmean)
-      launch_chained(moba::kv4_gate_kernel, rows, dim3(moba::kKv4GateThreads), (size_t)p.blocks * 9, st, p);
-    launch_chained(moba::kv4_attn_kernel, rows, dim3(moba::kKv4AttnThreads), 0, st, p);
-    if (acc)
-      launch_chained(moba::kv4_weight_kernel, dim3((unsigned)(capacity / 8), heads_kv, batch),
-                     dim3(moba::kKv4AttnThreads), 0, st, p);
+    p.units = reinterpret_cast<moba::Kv4Unit*>(ws + o_units);
+    p.before = reinterpret_cast<int64_t*>(ws + o_before);
+    p.start = reinterpret_cast<int2*>(ws + o_start);
+    p.list = reinterpret_cast<uint2*>(ws + o_list);
+    p.chosen = reinterpret_cast<uint32_t*>(ws + o_chosen);
+    p.scores = reinterpret_cast<double*>(ws + o_scores);
+    p.part = reinterpret_cast<float*>(ws + o_part);
+    if (kmean) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)(clusters * csize));
+      cfg.blockDim = dim3(moba::kKv4GateThreads);
+      cfg.stream = st;
+      cudaLaunchAttribute attr[2];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      attr[1].id = cudaLaunchAttributeClusterDimension;
+      attr[1].val.clusterDim.x = csize;
+      attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 2;
+      MOBA_CUDA(cudaLaunchKernelEx(&cfg, moba::kv4_gate_kernel, p));
+    }
+    launch_chained(moba::kv4_plan_kernel, dim3(1), dim3(moba::kKv4PlanThreads), 0, st, p);
+    if (few) launch_kv4_attn<moba::Kv4Few>(p, st);
+    else launch_kv4_attn<moba::Kv4Many>(p, st);
+    launch_chained(moba::kv4_join_kernel,
+                   dim3((unsigned)((nu * p.R * 32 + moba::kKv4JoinThreads - 1) / moba::kKv4JoinThreads)),
+                   dim3(moba::kKv4JoinThreads), 0, st, p);
+    if (acc) {
+      const int per = moba::kKv4WeightThreads / 32;
+      launch_chained(moba::kv4_weight_kernel, dim3((unsigned)((p.tiles + per - 1) / per), batch * heads_kv),
+                     dim3(moba::kKv4WeightThreads), 0, st, p);
+    }
     MOBA_CUDA(cudaGetLastError());
     return MOBA_OK;
   };
-  rc = direct_run((size_t)total * heads_q * p.topk * 4, run, stream);
+  rc = direct_run(c.off, run, stream);
   return finish_call(rc, stream);
 }
 

@@ -200,15 +200,20 @@ def check_attend(got, q, vals, lengths, news, hkv, sparse=None, kmean=None, rows
             top = np.abs(v).max(initial=0.0)
             tol = 2.0**-8 * np.abs(r["out"]) + (w + 2.0**-11 + L * U) * r["spread"] + L * 2.0**-37 * top
             o = out[t:t + n, h * G:(h + 1) * G]
-            assert (np.abs(o - r["out"]) <= tol).all(), (b, h, np.abs(o - r["out"]).max())
+            off = np.abs(o - r["out"])
+            assert bool((off <= tol).all()), (b, h, off.max(), (off / tol).max())
             e = lse[h * G:(h + 1) * G, t:t + n].T
             none = ~mask.any(-1)
+            r["lse"][none] = 0
             assert (e[none] == -np.inf).all() and (o[none] == 0).all()
-            assert (np.abs(e[~none] - r["lse"][~none]) <= d + 2.0**-21 + L * U + 4 * U * np.abs(r["lse"][~none])).all()
+            e = np.where(none, 0, e)
+            off, tol = np.abs(e - r["lse"])[~none], (d + 2.0**-21 + L * U + 4 * U * np.abs(r["lse"]))[~none]
+            assert bool((off <= tol).all()), (b, h, off.max(), (off / tol).max())
             if acc is not None:
                 a, a0 = f64(acc[b, h]), f64(acc0[b, h])
                 want = a0[:L] + r["weights"]
-                assert (np.abs(a[:L] - want) <= 2 * w * r["weights"] + (n * G + 2) * U * want).all()
+                off, tol = np.abs(a[:L] - want), 2 * w * r["weights"] + (n * G + 2) * U * want
+                assert bool((off <= tol).all()), (b, h, off.max(), (off / tol).max())
                 assert np.array_equal(a[L:], a0[L:])
         t += n
 
