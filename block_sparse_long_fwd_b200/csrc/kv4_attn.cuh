@@ -9,11 +9,11 @@
 //
 // Work is cut into units: R consecutive rows (token, q head of one kv head) of
 // one sequence and kv head, with the 64-token tiles of the cache that at least
-// one of them attends. All units' tiles in a row are dealt out evenly, one
-// contiguous range to each CTA of a grid of one CTA per SM, wherever the units
-// begin and end: lengths that differ, and few units with many tiles, balance
-// by themselves. A unit that several CTAs share leaves a partial result in
-// each, and a second kernel joins them.
+// one of them attends. All units' tiles in a row are dealt out evenly, in half
+// tiles, one contiguous range to each warp of a grid of one CTA per SM,
+// wherever the units begin and end: lengths that differ, and few units with
+// many tiles, balance by themselves. A unit that several warps share is joined
+// in shared memory, and by a second kernel where it crosses CTAs.
 #pragma once
 
 #include "kv4.cuh"
@@ -44,24 +44,23 @@ struct Kv4AttnParams {
   float* lse;                   // [Hq][total]
   // scratch
   Kv4Unit* units;               // [slots * Hkv]
-  int64_t* before;              // [slots * Hkv + 1]: tiles of the units before
-  int2* start;                  // [ctas]: first unit of a CTA's range, tiles of it before the range
+  int64_t* before;              // [slots * Hkv + 1]: half tiles of the units before
   uint2* list;                  // [slots * Hkv][list_cap]: (block, rows that chose it), ascending
   uint32_t* chosen;             // [slots * Hkv][blocks]: rows of the unit that chose the block
   double* scores;               // [clusters][R][means]
   float* part;                  // [2 * ctas][R * 130]: O, then m and l
-  int list_cap, ctas;
+  int list_cap, ctas, warps;    // warps of a CTA
 };
 
 // Queries of sequence b: packed index of the first and their number. Offsets
 // outside the rows are a caller's error, recorded and read as no query.
-__device__ __forceinline__ int kv4_queries(const Kv4AttnParams& p, int b, int* t0) {
-  if (!p.cu) {
+__device__ __forceinline__ int kv4_queries(const Kv4AttnParams& p, const int32_t* cu, int b, int* t0) {
+  if (!cu) {
     const int n = (int)(p.total / p.batch);
     *t0 = b * n;
     return n;
   }
-  const int c0 = p.cu[b], c1 = p.cu[b + 1];
+  const int c0 = cu[b], c1 = cu[b + 1];
   *t0 = c0;
   if (c0 < 0 || c1 < c0 || c1 > p.total) {
     record_status(MOBA_ERR_DEVICE_CHECK);
@@ -77,20 +76,21 @@ __device__ __forceinline__ int64_t kv4_first_slot(const Kv4AttnParams& p, int b,
   return (int64_t)t0 * p.G / p.R + b;
 }
 
-// The unit of slot `slot` of kv head h; rows = 0 for an unused slot. Called
-// by one thread.
-__device__ __forceinline__ Kv4Unit kv4_unit_of(const Kv4AttnParams& p, int slot, int h) {
+// The unit of slot `slot` of kv head h; rows = 0 for an unused slot. cu and
+// lengths are p's or a copy of them.
+__device__ __forceinline__ Kv4Unit kv4_unit_of(const Kv4AttnParams& p, const int32_t* cu, const int32_t* lengths,
+                                               int slot, int h) {
   Kv4Unit u = {};
   u.h = h;
   int lo = 0, hi = p.batch;  // first_slot(lo) <= slot < first_slot(hi)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    const int t = p.cu ? p.cu[mid] : (int)(mid * (p.total / p.batch));
+    const int t = cu ? cu[mid] : (int)(mid * (p.total / p.batch));
     if (kv4_first_slot(p, mid, t) <= slot) lo = mid;
     else hi = mid;
   }
   int t0;
-  const int n = kv4_queries(p, lo, &t0);
+  const int n = kv4_queries(p, cu, lo, &t0);
   const int64_t first = kv4_first_slot(p, lo, t0);
   const int64_t row0 = (slot - first) * p.R;
   if (row0 < 0 || row0 >= (int64_t)n * p.G) return u;
@@ -98,7 +98,7 @@ __device__ __forceinline__ Kv4Unit kv4_unit_of(const Kv4AttnParams& p, int slot,
   u.row0 = (int)row0;
   u.rows = min(p.R, (int)((int64_t)n * p.G - row0));
   u.t0 = t0;
-  u.pos0 = kv4_length(p.lengths, lo, p.tiles * kKv4Tile) - n;
+  u.pos0 = kv4_length(lengths, lo, p.tiles * kKv4Tile) - n;
   return u;
 }
 
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams
   double* scores = p.scores + (int64_t)cluster * p.R * p.means;
   const int nu = p.slots * p.Hkv;
   for (int ui = cluster; ui < nu; ui += clusters) {
-    if (tid == 0) s_unit = kv4_unit_of(p, ui / p.Hkv, ui % p.Hkv);
+    if (tid == 0) s_unit = kv4_unit_of(p, p.cu, p.lengths, ui / p.Hkv, ui % p.Hkv);
     __syncthreads();
     Kv4Unit u = s_unit;
     const int last = u.rows ? kv4_last_pos(p, u) : -1;
@@ -263,36 +263,53 @@ __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams
 
 // ------------------------------------------------------------------ plan
 
-// CTAs that get a range of `all` tiles: every one gets at least a tile.
+// CTAs that get a range of `all` half tiles: as many as leave no warp idle.
 __device__ __forceinline__ int kv4_ctas(const Kv4AttnParams& p, int64_t all) {
-  return (int)min((int64_t)p.ctas, all);
+  return (int)min((int64_t)p.ctas, (all + p.warps - 1) / p.warps);
 }
 
-constexpr int kKv4PlanThreads = 1024;
+// Where each warp's range begins: every CTA scans all units' tiles for itself
+// (they follow from the lengths alone, or the gate has left them), which is
+// a round trip to L2 where a kernel of its own was 6 to 9 us with its launch.
+// The units that the CTA's range touches, and the half tiles before them, are
+// left in scratch for the rest of the CTA and for the join (units of several
+// CTAs get the same values from each); CTA 0 leaves those without tiles.
+// `copy`: shared memory for the offsets and lengths, `room` words.
+struct Kv4Range {
+  int n;          // half tiles of this warp
+  int unit, off;  // its first unit, half tiles of it that lie before the range
+  bool any;       // the CTA has some
+};
 
-// One CTA: the units (the gate has already written them where there is one),
-// the tiles before each, and where each CTA's range starts.
-__global__ void __launch_bounds__(kKv4PlanThreads) kv4_plan_kernel(Kv4AttnParams p) {
-  grid_dependency_sync();
-  __shared__ int64_t warp_sums[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+template <int WARPS>
+__device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* copy, int room) {
+  constexpr int THREADS = 32 * WARPS;
+  __shared__ int64_t warp_sums[WARPS], bound[WARPS + 1];
+  __shared__ int2 s_start[WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
   const int nu = p.slots * p.Hkv;
-  int64_t done = 0;
-  for (int u0 = 0; u0 < nu; u0 += kKv4PlanThreads) {
-    const int ui = u0 + tid;
-    int64_t tiles = 0;
-    if (ui < nu) {
-      if (p.kmean) {
-        tiles = p.units[ui].tiles;
-      } else {
-        Kv4Unit u = kv4_unit_of(p, ui / p.Hkv, ui % p.Hkv);
-        const int last = u.rows ? kv4_last_pos(p, u) : -1;
-        u.tiles = last < 0 ? 0 : last / kKv4Tile + 1;
-        tiles = u.tiles;
-        p.units[ui] = u;
-      }
+  const int32_t *cu = p.cu, *lengths = p.lengths;
+  if (!p.kmean && 2 * p.batch + 1 <= room) {
+    for (int i = tid; i < p.batch; i += THREADS) copy[i] = p.lengths[i];
+    lengths = copy;
+    if (cu) {
+      for (int i = tid; i <= p.batch; i += THREADS) copy[p.batch + i] = p.cu[i];
+      cu = copy + p.batch;
     }
-    int64_t s = tiles;
+    __syncthreads();
+  }
+  auto unit = [&](int ui) {
+    Kv4Unit u = {};
+    if (ui >= nu) return u;
+    if (p.kmean) return p.units[ui];
+    u = kv4_unit_of(p, cu, lengths, ui / p.Hkv, ui % p.Hkv);
+    const int last = u.rows ? kv4_last_pos(p, u) : -1;
+    u.tiles = last < 0 ? 0 : last / kKv4Tile + 1;
+    return u;
+  };
+  // sum over the block; `before` of the own thread
+  auto scan = [&](int64_t x, int64_t* before) {
+    int64_t s = x;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, d);
@@ -301,51 +318,85 @@ __global__ void __launch_bounds__(kKv4PlanThreads) kv4_plan_kernel(Kv4AttnParams
     __syncthreads();
     if (lane == 31) warp_sums[warp] = s;
     __syncthreads();
-    int64_t base = done;
-    for (int i = 0; i < 32; ++i) {
+    int64_t base = 0, sum = 0;
+    for (int i = 0; i < WARPS; ++i) {
       if (i < warp) base += warp_sums[i];
-      done += warp_sums[i];
+      sum += warp_sums[i];
     }
-    if (ui < nu) p.before[ui] = base + s - tiles;
+    *before = base + s - x;
+    return sum;
+  };
+  Kv4Unit u = unit(tid);
+  int64_t before, all = scan(2 * u.tiles, &before);
+  const bool once = nu <= THREADS;
+  for (int u0 = THREADS; u0 < nu; u0 += THREADS) {
+    int64_t unused;
+    all += scan(2 * unit(u0 + tid).tiles, &unused);
   }
-  if (tid == 0) p.before[nu] = done;
+  const int ctas = kv4_ctas(p, all);
+  if (tid <= WARPS) bound[tid] = cta < ctas ? all * (cta * WARPS + tid) / (ctas * WARPS) : all;  // start of warp tid
   __syncthreads();
-  const int ctas = kv4_ctas(p, done);
-  for (int c = tid; c < ctas; c += kKv4PlanThreads) {
-    const int64_t x = done * c / ctas;
-    int lo = 0, hi = nu;  // the last unit that begins at or before tile x
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.before[mid] <= x) lo = mid;
-      else hi = mid;
+  const int64_t lo = bound[0], hi = bound[WARPS];
+  if (cta == 0 && tid == 0) p.before[nu] = all;
+  int64_t done = 0;
+  for (int u0 = 0; u0 < nu; u0 += THREADS) {
+    const int ui = u0 + tid;
+    if (!once) {
+      u = unit(ui);
+      const int64_t sum = scan(2 * u.tiles, &before);
+      before += done;
+      done += sum;
     }
-    p.start[c] = make_int2(lo, (int)(x - p.before[lo]));
+    if (ui < nu) {
+      const int64_t end = before + 2 * u.tiles;
+      const bool mine = u.tiles > 0 && before < hi && end > lo;
+      if (mine) {
+        p.before[ui] = before;
+        for (int w = 0; w < WARPS; ++w) {
+          const int64_t x = bound[w];
+          if (x >= before && x < end) s_start[w] = make_int2(ui, (int)(x - before));
+        }
+      }
+      if (!p.kmean && (mine || (cta == 0 && u.tiles == 0))) p.units[ui] = u;
+    }
   }
+  __syncthreads();
+  Kv4Range g;
+  g.any = hi > lo;
+  g.n = (int)(bound[warp + 1] - bound[warp]);
+  g.unit = g.n ? s_start[warp].x : 0;
+  g.off = g.n ? s_start[warp].y : 0;
+  return g;
 }
 
 // ------------------------------------------------------------------ attention
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same onto zero.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // 8 x 8 transpose of 16-bit values held by a warp.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
-__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -357,33 +408,41 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
   return d;
 }
 
-// Scale and zero point of two parameters (low and high half), ready for the
-// four nibbles of a 16-bit code group: a nibble at bit 0 under fp16's 1024 is
-// 1024 + c, at bit 4 it is 1024 + 16 c; minus 1024 + z, or over 16 minus
-// 64 + z, leaves c - z, and the product with the scale is exact.
+// A nibble at bit 4 under fp16's 64 is 64 + c, and t (64 + c) - t (64 + z) is
+// one fused multiply-add without a rounding: 64 + z has seven significant bits
+// and t four, so the product fits fp16's eleven, and the difference is
+// t (c - z). (A nibble at bit 0 stands under 1024: eleven bits and four, so a
+// subtraction and a multiplication for each pair instead, and the kernel is
+// bound by instructions.) t is a 64th of the scale, so that t (64 + z) stays
+// below fp16's largest number; t is a multiple of 2^-23, so all stays exact.
 struct Kv4Par {
-  uint32_t s, z, z16;
+  uint32_t t, tz;  // t and -t (64 + z), of two tokens (or of one, twice)
 };
+// (a & mask) | top in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t top) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(top));
+  return d;
+}
 __device__ __forceinline__ Kv4Par kv4_par(uint32_t pp) {
   Kv4Par r;
-  r.s = pp & 0x7F807F80u;
-  r.z = (pp & 0x000F000Fu) | 0x64006400u;
-  r.z16 = h2_sub(0x63806380u, r.z);  // 960 - (1024 + z)
+  r.t = h2_mul(pp & 0x7F807F80u, 0x24002400u);  // 2^-6
+  r.tz = h2_mul(and_or(pp << 4, 0x00F000F0u, 0xD400D400u), r.t);
   return r;
 }
+// t (c - z) for nibbles 0..3 of both halves of a word.
 __device__ __forceinline__ void kv4_pairs(uint32_t w, const Kv4Par& p, uint32_t (&x)[4]) {
-  const uint32_t h = w >> 8;
-  x[0] = h2_mul(h2_sub((w & 0x000F000Fu) | 0x64006400u, p.z), p.s);
-  x[1] = h2_mul(h2_fma((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, p.z16), p.s);
-  x[2] = h2_mul(h2_sub((h & 0x000F000Fu) | 0x64006400u, p.z), p.s);
-  x[3] = h2_mul(h2_fma((h & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, p.z16), p.s);
+  x[0] = h2_fma(and_or(w << 4, 0x00F000F0u, 0x54005400u), p.t, p.tz);
+  x[1] = h2_fma(and_or(w, 0x00F000F0u, 0x54005400u), p.t, p.tz);
+  x[2] = h2_fma(and_or(w >> 4, 0x00F000F0u, 0x54005400u), p.t, p.tz);
+  x[3] = h2_fma(and_or(w >> 8, 0x00F000F0u, 0x54005400u), p.t, p.tz);
 }
 
 // A query row enters the products as fp16: times the power of two that brings
 // its largest channel to [2^14, 2^15). bf16's eight bits then stay exact but
-// for channels 2^29 times smaller than the largest. Returns the row's fragment
-// of this lane (channels 32 (lane % 4) .. + 31 as eight steps of two pairs) and
-// the scale that turns its products into log2 scores.
+// for channels 2^28 times smaller than the largest, whose error is 2^-40 of it.
+// f: this lane's channels 32 (lane % 4) .. + 31 as eight steps of two pairs.
+// Returns the factor that turns products into log2 scores.
 __device__ __forceinline__ float kv4_query_fragment(const __nv_bfloat16* row, float scale_log2, uint32_t (&f)[16]) {
   uint4 raw[4] = {};
   if (row) {
@@ -404,7 +463,7 @@ __device__ __forceinline__ float kv4_query_fragment(const __nv_bfloat16* row, fl
 #pragma unroll
   for (int i = 0; i < 16; ++i)
     f[i] = pack_half2(__uint_as_float(w[i] << 16) * f1 * f2, __uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2);
-  return scale_log2 * __int_as_float((127 - k1) << 23) * __int_as_float((127 - k2) << 23);
+  return 64.f * scale_log2 * __int_as_float((127 - k1) << 23) * __int_as_float((127 - k2) << 23);
 }
 
 // Token (of 16) that row r of the score product holds: neighbours, swapped
@@ -419,29 +478,43 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-template <int NT_, int WARPS_, int DEPTH_>
+// A finished row: lane l's channels 4 l .. 4 l + 3, as a 64th of their sum.
+__device__ __forceinline__ void kv4_write_row(const Kv4AttnParams& p, const Kv4Unit& u, int row, int lane, float m,
+                                              float l, float4 o) {
+  const int rr = u.row0 + row;
+  const int64_t t = u.t0 + rr / p.G;
+  const int hq = u.h * p.G + rr % p.G;
+  const float inv = l > 0.f ? 64.f / l : 0.f;
+  reinterpret_cast<uint2*>(p.out + (t * p.Hq + hq) * kHeadDim)[lane] =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (lane == 0) p.lse[(int64_t)hq * p.total + t] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int NT_, int WARPS_, bool QREG_>
 struct Kv4Cfg {
   static constexpr int NT = NT_;            // groups of eight query rows
   static constexpr int R = 8 * NT;
   static constexpr int WARPS = WARPS_;
-  static constexpr int DEPTH = DEPTH_;      // half tiles a warp holds: one in use, the others on their way
   static constexpr int THREADS = 32 * WARPS;
-  static constexpr int OLD = kHeadDim + 4;  // row stride of the O exchange (spreads the quads over the banks)
-  static constexpr bool QREG = NT == 1;     // query fragments in registers, else in shared memory
+  static constexpr bool QREG = QREG_;       // query fragments in registers, else in shared memory
+  static constexpr int PIECE = R * kHeadDim * 4;
   struct Shared {
-    uint8_t ring[WARPS][DEPTH][kKv4Half];   // 32 tokens: key codes, key parameters, value codes, value parameters
-    float o[WARPS][R][OLD];
-    float2 ml[2][WARPS][R];
-    uint2 q[QREG ? 1 : NT][8][32];
-    float qs[R];
-    uint64_t full[WARPS][DEPTH];
-    int2 info[WARPS][DEPTH];                // first key of the half tile, rows that attend it
+    // 2 x 32 tokens a warp (key codes, key parameters, value codes, value parameters): one half tile in use, one on
+    // its way; at the end, the warp's partial result of a unit that it began
+    uint8_t ring[WARPS][2][kKv4Half];
+    uint8_t piece[WARPS][PIECE];            // the warp's partial result of a unit that it did not begin
+    float2 ml[WARPS][2][R];                 // their maxima and sums
+    uint2 q[QREG ? 1 : WARPS][NT][8][32];
+    uint64_t full[WARPS][2];
+    int unit[2 * WARPS];                    // units of the partial results, -1 for none
+    int begins[2 * WARPS], ends[2 * WARPS];
     int abort_flag;
   };
+  static_assert(2 * kKv4Half >= PIECE, "a partial result fits the warp's ring");
 };
 
-using Kv4Few = Kv4Cfg<1, 16, 2>;   // up to 8 rows
-using Kv4Many = Kv4Cfg<4, 8, 2>;   // up to 32 rows
+using Kv4Few = Kv4Cfg<1, 16, true>;    // up to 8 rows
+using Kv4Many = Kv4Cfg<2, 8, false>;   // up to 16 rows
 
 constexpr int kKv4HalfTok = kKv4Tile / 2;
 constexpr int kKv4HalfParams = kKv4HalfTok * kKv4Row;         // 2048: offset of the parameters of 32 tokens
@@ -456,54 +529,59 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
   auto* sh = reinterpret_cast<typename C::Shared*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::WARPS * C::DEPTH; ++i) mbar_init(&sh->full[0][0] + i, 1);
+    for (int i = 0; i < 2 * C::WARPS; ++i) mbar_init(&sh->full[0][0] + i, 1);
     sh->abort_flag = 0;
     fence_barrier_init();
   }
-  __syncthreads();
-  const int64_t all = p.before[p.slots * p.Hkv];
-  const int ctas = kv4_ctas(p, all);
-  if (cta >= ctas) return;
-  const int n = (int)(all * (cta + 1) / ctas - all * cta / ctas);  // tiles of this CTA, at least one
-  const int2 start = p.start[cta];
+  if (threadIdx.x < 2 * C::WARPS) sh->unit[threadIdx.x] = -1;
+  const Kv4Range range = kv4_plan<C::WARPS>(p, reinterpret_cast<int32_t*>(&sh->piece), sizeof(sh->piece) / 4);
+  if (!range.any) return;
+  const int n = range.n;
 
-  // Every warp works alone on half tiles (32 tokens) warp, warp + WARPS, ... of the CTA's range and fetches its own
-  // ahead: the four pieces of one by bulk copies of four lanes. `issue` walks the units as far as its half tile.
-  int c_ui = start.x, c_base = -2 * start.y, c_end = c_base + 2 * p.units[start.x].tiles;
-  auto issue = [&](int k) {
-    const int x = warp + C::WARPS * k;
-    if (x >= 2 * n) return;
-    while (x >= c_end) {
-      c_base = c_end;
-      c_end += 2 * p.units[++c_ui].tiles;
+  // A warp fetches its own half tiles, two ahead: the four pieces of one by bulk copies of four lanes. `issue` walks
+  // the units as far as its half tile.
+  const int piece = (lane & 2 ? kKv4Half : 0) + (lane & 1 ? kKv4Params : 0);
+  const int piece_half = lane & 1 ? kKv4HalfTok * 8 : kKv4HalfParams;  // its bytes, and from half to half
+  const int piece_dst = (lane & 2 ? kKv4HalfRows : 0) + (lane & 1 ? kKv4HalfParams : 0);
+  const int tpb = p.B / kKv4Tile;
+  int c_ui = range.unit - 1, c_off = range.off, c_left = n, c_end = 0, c_at = 0, c_in = 0;
+  const uint8_t* c_src = nullptr;
+  int key_a = 0, key_b = 0;             // first keys of the half tile in use and of the next
+  uint32_t rows_a = ~0u, rows_b = ~0u;  // rows that chose their blocks
+  auto issue = [&](int d) {
+    key_a = key_b;
+    rows_a = rows_b;
+    if (c_left <= 0) return;
+    if (c_off >= c_end) {  // on to the next unit that has tiles
+      c_off -= c_end;
+      do c_end = 2 * p.units[++c_ui].tiles;
+      while (c_end == 0);
+      const Kv4Unit u = p.units[c_ui];
+      c_src = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, u.b, u.h, 0) + piece;
+      c_at = (c_off >> 1) / tpb;
+      c_in = (c_off >> 1) - c_at * tpb;
     }
-    const int off = (x - c_base) >> 1;
-    int key = off * kKv4Tile;
-    uint32_t rows = 0xFFFFFFFFu;
-    if (p.kmean) {
-      const int tpb = p.B / kKv4Tile, at = off / tpb;
-      const uint2 e = p.list[(int64_t)c_ui * p.list_cap + at];
-      key = (int)e.x * p.B + (off - at * tpb) * kKv4Tile;
-      rows = e.y;
-    }
-    const int half = x & 1, d = k % C::DEPTH;
     uint64_t* bar = &sh->full[warp][d];
-    if (lane == 0) {
-      sh->info[warp][d] = make_int2(key + half * kKv4HalfTok, (int)rows);
-      mbar_arrive_expect_tx(bar, 2 * kKv4HalfRows);
+    if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kKv4HalfRows);
+    int tile = c_off >> 1;
+    const int half = c_off & 1;
+    if (p.kmean) {
+      if (c_in == tpb) c_in = 0, ++c_at;
+      const uint2 e = p.list[(int64_t)c_ui * p.list_cap + c_at];
+      tile = (int)e.x * tpb + c_in;
+      rows_b = e.y;
+      c_in += half;
     }
+    key_b = tile * kKv4Tile + half * kKv4HalfTok;
+    ++c_off;
+    --c_left;
     __syncwarp();
-    if (lane < 4) {
-      const Kv4Unit& u = p.units[c_ui];
-      const int par = lane & 1, vals = lane >> 1;
-      const uint8_t* src = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, u.b, u.h, key / kKv4Tile) + vals * kKv4Half +
-                           (par ? kKv4Params + half * (kKv4HalfTok * 8) : half * kKv4HalfParams);
-      bulk_load(sh->ring[warp][d] + vals * kKv4HalfRows + par * kKv4HalfParams, src,
-                par ? kKv4HalfTok * 8 : kKv4HalfParams, bar);
-    }
+    if (lane < 4)
+      bulk_load(sh->ring[warp][d] + piece_dst, c_src + (int64_t)tile * kKv4TileBytes + half * piece_half, piece_half,
+                bar);
   };
-#pragma unroll
-  for (int k = 0; k < C::DEPTH; ++k) issue(k);
+  issue(0);
+  issue(1);
 
   const int r = lane >> 2, qd = lane & 3;
   const int tok0 = kv4_token_of(r);
@@ -511,59 +589,48 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
   const int ve0 = 2 * qd + (qd & 1), ve1 = 2 * qd + ((qd & 1) ^ 1);
   bool dead = false;
   int death = 0;  // the half tile that never came
-  int done = 0, seg = 0, k = 0;  // tiles of the range behind us, units, half tiles of this warp
-  for (int ui = start.x, off = start.y; done < n; ++ui, off = 0) {
+  int k = 0;      // half tiles of this warp behind us
+  for (int ui = range.unit, off = range.off; k < n; ++ui, off = 0) {
     const Kv4Unit u = p.units[ui];
-    if (u.tiles <= off) continue;
-    const int take = min(n - done, u.tiles - off);
+    const int stop = k + min(n - k, 2 * u.tiles - off);
+    if (stop == k) continue;
     // the rows' fragments, scales, and last keys (of this lane's two rows of each group of eight)
     uint32_t qf[16];
     float qs[NT][2];
     int last[NT][2];
     const int first_pos = u.pos0 + u.row0 / p.G, last_pos = kv4_last_pos(p, u);
-    if constexpr (C::QREG) {
-      const int rr = u.row0 + r;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int x = nt * 8 + r, rr = u.row0 + x;
       const __nv_bfloat16* row =
-          r < u.rows ? p.q + ((int64_t)(u.t0 + rr / p.G) * p.Hq + u.h * p.G + rr % p.G) * kHeadDim + qd * 32 : nullptr;
+          x < u.rows ? p.q + ((int64_t)(u.t0 + rr / p.G) * p.Hq + u.h * p.G + rr % p.G) * kHeadDim + qd * 32 : nullptr;
       const float s = kv4_query_fragment(row, p.scale_log2, qf);
-      qs[0][0] = __shfl_sync(0xFFFFFFFFu, s, qd * 8);
-      qs[0][1] = __shfl_sync(0xFFFFFFFFu, s, qd * 8 + 4);
-    } else {
-      // every warp is past the previous unit's tiles (the exchange's barriers)
-      for (int nt = warp; nt < NT; nt += C::WARPS) {
-        const int x = nt * 8 + r, rr = u.row0 + x;
-        const __nv_bfloat16* row =
-            x < u.rows ? p.q + ((int64_t)(u.t0 + rr / p.G) * p.Hq + u.h * p.G + rr % p.G) * kHeadDim + qd * 32
-                       : nullptr;
-        const float s = kv4_query_fragment(row, p.scale_log2, qf);
+      qs[nt][0] = __shfl_sync(0xFFFFFFFFu, s, qd * 8);
+      qs[nt][1] = __shfl_sync(0xFFFFFFFFu, s, qd * 8 + 4);
+      if constexpr (!C::QREG) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sh->q[nt][i][lane] = make_uint2(qf[2 * i], qf[2 * i + 1]);
-        if (qd == 0) sh->qs[x] = s;
+        for (int i = 0; i < 8; ++i) sh->q[warp][nt][i][lane] = make_uint2(qf[2 * i], qf[2 * i + 1]);  // read back by itself
       }
-      __syncthreads();
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) qs[nt][0] = sh->qs[nt * 8 + 2 * qd], qs[nt][1] = sh->qs[nt * 8 + 2 * qd + 1];
+      for (int x2 = 0; x2 < 2; ++x2) {
+        const int row2 = nt * 8 + 2 * qd + x2;
+        last[nt][x2] = row2 < u.rows ? u.pos0 + (u.row0 + row2) / p.G : -1;
+      }
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int row = nt * 8 + 2 * qd + x;
-        last[nt][x] = row < u.rows ? u.pos0 + (u.row0 + row) / p.G : -1;
-      }
-    const uint32_t all_rows = u.rows == 32 ? 0xFFFFFFFFu : (1u << u.rows) - 1;
+    const uint32_t all_rows = (1u << u.rows) - 1;
 
     float o[NT][8][4] = {}, m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = kKv4Low, l[nt][0] = l[nt][1] = 0.f;
 
-    for (; warp + C::WARPS * k < 2 * (done + take); ++k) {
-      const int d = k % C::DEPTH;
-      if (!dead && !mbar_wait(&sh->full[warp][d], (k / C::DEPTH) & 1, &sh->abort_flag)) dead = true, death = k;
+    const int k0 = k;
+    for (; k < stop; ++k) {
+      const int d = k & 1;
+      if (!dead && !mbar_wait(&sh->full[warp][d], (k >> 1) & 1, &sh->abort_flag)) dead = true, death = k;
       if (dead) continue;
-      const uint8_t* kt = sh->ring[warp][d];
-      const uint8_t* vt = kt + kKv4HalfRows;
-      const int2 info = sh->info[warp][d];
+      uint8_t* slot = sh->ring[warp][d];
+      const uint8_t* kt = slot;
+      const uint8_t* vt = slot + kKv4HalfRows;
 
       // scores: keys x rows, 16 keys at a time
       float sc[2][NT][4];
@@ -575,8 +642,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
         const uint32_t pa = *reinterpret_cast<const uint16_t*>(kt + kKv4HalfParams + ta * 8 + qd * 2);
         const uint32_t pb = *reinterpret_cast<const uint16_t*>(kt + kKv4HalfParams + tb * 8 + qd * 2);
         const Kv4Par fa = kv4_par(__byte_perm(pa, 0, 0x1010)), fb = kv4_par(__byte_perm(pb, 0, 0x1010));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) sc[g][nt][0] = sc[g][nt][1] = sc[g][nt][2] = sc[g][nt][3] = 0.f;
         const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xb[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -590,26 +655,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
               q0 = make_uint2(qf[4 * w], qf[4 * w + 1]);
               q1 = make_uint2(qf[4 * w + 2], qf[4 * w + 3]);
             } else {
-              q0 = sh->q[nt][2 * w][lane];
-              q1 = sh->q[nt][2 * w + 1][lane];
+              q0 = sh->q[warp][nt][2 * w][lane];
+              q1 = sh->q[warp][nt][2 * w + 1][lane];
             }
-            mma_f16(sc[g][nt], a[0], b[0], a[1], b[1], q0.x, q0.y);
+            if (w == 0) mma_f16_first(sc[g][nt], a[0], b[0], a[1], b[1], q0.x, q0.y);
+            else mma_f16(sc[g][nt], a[0], b[0], a[1], b[1], q0.x, q0.y);
             mma_f16(sc[g][nt], a[2], b[2], a[3], b[3], q1.x, q1.y);
           }
         }
       }
       // keys behind a row's position, and blocks that a row did not choose
-      const bool edge = info.x + kKv4HalfTok - 1 > first_pos;
-      if (edge || ((uint32_t)info.y & all_rows) != all_rows) {
+      const bool edge = key_a + kKv4HalfTok - 1 > first_pos;
+      if (edge && key_a + lane > last_pos) {
+        // what lies behind the last token may hold anything: its values' scales become zero
+        *reinterpret_cast<uint2*>(slot + kKv4HalfRows + kKv4HalfParams + lane * 8) = make_uint2(0, 0);
+        fence_proxy_async_smem();  // before the copy that will overwrite them
+      }
+      if (edge || (rows_a & all_rows) != all_rows) {
+        __syncwarp();
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const int key = info.x + tok0 + g * 16 + (x >> 1) * 8;
+              const int key = key_a + tok0 + g * 16 + (x >> 1) * 8;
               const uint32_t row = nt * 8 + 2 * qd + (x & 1);
-              if (key > last[nt][x & 1] || !((uint32_t)info.y >> row & 1u)) sc[g][nt][x] = -INFINITY;
+              if (key > last[nt][x & 1] || !(rows_a >> row & 1u)) sc[g][nt][x] = -INFINITY;
             }
       }
       // weights 2^(score - m). The reference m moves when a score exceeds it by more than 15, to 12 below
@@ -618,13 +690,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float t[2][4], top = -INFINITY;
+        auto shifted = [&] {
+          const uint64_t qs2 = f2_pack(qs[nt][0], qs[nt][1]), m2 = f2_pack(-m[nt][0], -m[nt][1]);
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int x = 0; x < 4; x += 2) {
+              const uint64_t y = f2_fma(f2_pack(sc[g][nt][x], sc[g][nt][x + 1]), qs2, m2);
+              t[g][x] = f2_lo(y);
+              t[g][x + 1] = f2_hi(y);
+            }
+        };
+        shifted();
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            t[g][x] = fmaf(sc[g][nt][x], qs[nt][x & 1], -m[nt][x & 1]);
-            top = fmaxf(top, t[g][x]);
-          }
+          for (int x = 0; x < 4; ++x) top = fmaxf(top, t[g][x]);
         if (__any_sync(0xFFFFFFFFu, top > 15.f)) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
@@ -639,18 +720,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
               for (int mt = 0; mt < 8; ++mt) o[nt][mt][x] *= a, o[nt][mt][x + 2] *= a;
             }
           }
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) t[g][x] = fmaf(sc[g][nt][x], qs[nt][x & 1], -m[nt][x & 1]);
+          shifted();
         }
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           float e[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) e[x] = ex2_approx(t[g][x]);
-          l[nt][0] += e[0] + e[2];
-          l[nt][1] += e[1] + e[3];
+          const uint64_t sum = f2_add(f2_pack(l[nt][0], l[nt][1]), f2_add(f2_pack(e[0], e[1]), f2_pack(e[2], e[3])));
+          l[nt][0] = f2_lo(sum);
+          l[nt][1] = f2_hi(sum);
           pf[nt][g][0] = movmatrix(pack_half2(e[0], e[1]));
           pf[nt][g][1] = movmatrix(pack_half2(e[2], e[3]));
         }
@@ -665,18 +744,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
           const int t0 = ve0 + g * 16 + f * 8, t1 = ve1 + g * 16 + f * 8;
           w[f][0] = *reinterpret_cast<const uint2*>(vt + t0 * kKv4Row + vchunk);
           w[f][1] = *reinterpret_cast<const uint2*>(vt + t1 * kKv4Row + vchunk);
-          uint32_t p0 = *reinterpret_cast<const uint16_t*>(vt + kKv4HalfParams + t0 * 8 + (r >> 1) * 2);
-          uint32_t p1 = *reinterpret_cast<const uint16_t*>(vt + kKv4HalfParams + t1 * 8 + (r >> 1) * 2);
-          if (edge) {  // what lies behind the last token may hold anything
-            if (info.x + t0 > last_pos) p0 = 0;
-            if (info.x + t1 > last_pos) p1 = 0;
-          }
+          const uint32_t p0 = *reinterpret_cast<const uint16_t*>(vt + kKv4HalfParams + t0 * 8 + (r >> 1) * 2);
+          const uint32_t p1 = *reinterpret_cast<const uint16_t*>(vt + kKv4HalfParams + t1 * 8 + (r >> 1) * 2);
           fp[f] = kv4_par(__byte_perm(p0, p1, 0x5410));
         }
-        if (g == 1) {  // the half tile is in registers: fetch the next one into its place
-          __syncwarp();
-          issue(k + C::DEPTH);
-        }
+        if (g == 1) __syncwarp();  // the half tile is in registers: the next but one may take its place
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t a[2][2][4];  // [channel parity][keys 0-7, 8-15][nibble]
@@ -693,75 +765,115 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
               mma_f16(o[nt][h * 4 + j], a[0][0][j], a[1][0][j], a[0][1][j], a[1][1][j], pf[nt][g][0], pf[nt][g][1]);
         }
       }
+      issue(d);
     }
 
-    // ---- join the warps' results
-    float2(&ml)[C::WARPS][R] = sh->ml[seg & 1];
+    // ---- this warp's part of the unit: all of it is a result, else a piece to be joined
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][x], d);
-        if (r == 0) ml[warp][nt * 8 + 2 * qd + x] = make_float2(m[nt][x], l[nt][x]);
-      }
-    __syncthreads();
+    const bool begins = off == 0, ends = off + (k - k0) == 2 * u.tiles;
+    // lane: channels 16 r .. 16 r + 15 of rows 2 qd, 2 qd + 1 of each group of eight (a 64th of them so far)
+    if (begins && ends) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int row = nt * 8 + 2 * qd + x;
-        float mm = kKv4Low;
+        for (int x = 0; x < 2; ++x) {
+          const int row = nt * 8 + 2 * qd + x;
+          if (row >= u.rows) continue;
+          const int rr = u.row0 + row;
+          const int64_t t = u.t0 + rr / p.G;
+          const int hq = u.h * p.G + rr % p.G;
+          const float inv = l[nt][x] > 0.f ? 64.f / l[nt][x] : 0.f;
+          uint32_t y[8];
 #pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, ml[w][row].x);
-        const float a = ex2_approx(m[nt][x] - mm);
-        // channel 16 r + c lies at c * 8 + r: the lanes of a quad column fall on neighbouring banks
-#pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
-          sh->o[warp][row][(2 * mt) * 8 + r] = o[nt][mt][x] * a;
-          sh->o[warp][row][(2 * mt + 1) * 8 + r] = o[nt][mt][x + 2] * a;
+          for (int mt = 0; mt < 8; ++mt) y[mt] = pack_bf16x2(o[nt][mt][x] * inv, o[nt][mt][x + 2] * inv);
+          uint4* out = reinterpret_cast<uint4*>(p.out + (t * p.Hq + hq) * kHeadDim + 16 * r);
+          out[0] = make_uint4(y[0], y[1], y[2], y[3]);
+          out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+          if (r == 0)
+            p.lse[(int64_t)hq * p.total + t] =
+                l[nt][x] > 0.f ? (m[nt][x] + log2f(l[nt][x])) * 0.6931471805599453f : -INFINITY;
         }
+    } else {
+      const int which = begins ? 1 : 0;
+      if (lane == 0) {
+        sh->unit[2 * warp + which] = ui;
+        sh->begins[2 * warp + which] = begins;
+        sh->ends[2 * warp + which] = ends;
       }
-    __syncthreads();
-    const bool whole = off == 0 && take == u.tiles;
-    float* part = p.part + (int64_t)(2 * cta + (off == 0 ? 1 : 0)) * (R * 130);
-    for (int idx = threadIdx.x; idx < u.rows * kHeadDim; idx += C::THREADS) {
-      const int row = idx >> 7, at = idx & 127;
-      float mm = kKv4Low, ll = 0.f, oo = 0.f;
+      // a unit that this warp begins and does not end is its last: its ring is free
+      __syncwarp();
+      float* at = reinterpret_cast<float*>(which ? &sh->ring[warp][0][0] : sh->piece[warp]);
 #pragma unroll
-      for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, ml[w][row].x);
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int w = 0; w < C::WARPS; ++w) {
-        const float2 x = ml[w][row];
-        ll += x.y * ex2_approx(x.x - mm);
-        oo += sh->o[w][row][at];
-      }
-      if (whole) {
-        const int rr = u.row0 + row;
-        const int64_t t = u.t0 + rr / p.G;
-        const int hq = u.h * p.G + rr % p.G;
-        p.out[(t * p.Hq + hq) * kHeadDim + (at & 7) * 16 + (at >> 3)] = __float2bfloat16(ll > 0.f ? oo / ll : 0.f);
-        if (at == 0) p.lse[(int64_t)hq * p.total + t] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
-      } else {
-        part[idx] = oo;
-        if (at == 0) {
-          part[R * kHeadDim + 2 * row] = mm;
-          part[R * kHeadDim + 2 * row + 1] = ll;
+        for (int x = 0; x < 2; ++x) {
+          const int row = nt * 8 + 2 * qd + x;
+          float4* to = reinterpret_cast<float4*>(at + row * kHeadDim + 16 * r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            to[i ^ (r & 3)] = make_float4(o[nt][2 * i][x], o[nt][2 * i][x + 2], o[nt][2 * i + 1][x],
+                                          o[nt][2 * i + 1][x + 2]);  // spread over the banks
+          if (r == 0) sh->ml[warp][which][row] = make_float2(m[nt][x], l[nt][x]);
         }
-      }
     }
-    done += take;
-    ++seg;
   }
   if (dead) {
     // the block's shared memory lives until the copies under way have landed
-    const int issued = min(death + C::DEPTH, (2 * n - warp + C::WARPS - 1) / C::WARPS);
-    for (int i = death; i < issued; ++i) {
+    for (int i = death; i < min(death + 2, n); ++i) {
       const uint64_t t0 = clock64();
-      while (!mbar_try_wait(&sh->full[warp][i % C::DEPTH], (i / C::DEPTH) & 1) &&
-             (uint64_t)(clock64() - t0) < (1ull << 31)) {
+      while (!mbar_try_wait(&sh->full[warp][i & 1], (i >> 1) & 1) && (uint64_t)(clock64() - t0) < (1ull << 31)) {
       }
     }
+  }
+  __syncthreads();
+
+  // ---- join the CTA's pieces: those of a unit follow one another. One warp per (unit, row)
+  int item = 0;
+  for (int s = 0; s < 2 * C::WARPS;) {
+    const int ui = sh->unit[s];
+    if (ui < 0) {
+      ++s;
+      continue;
+    }
+    int e = s + 1, fin = s;  // the pieces s .. fin
+    while (e < 2 * C::WARPS && (sh->unit[e] < 0 || sh->unit[e] == ui)) {
+      if (sh->unit[e] == ui) fin = e;
+      ++e;
+    }
+    const int rows = p.units[ui].rows;
+    for (int row = 0; row < rows; ++row, ++item) {
+      if (item % C::WARPS != warp) continue;
+      const Kv4Unit u = p.units[ui];
+      float mm = kKv4Low, ll = 0.f;
+      for (int i = s; i <= fin; ++i)
+        if (sh->unit[i] == ui) mm = fmaxf(mm, sh->ml[i >> 1][i & 1][row].x);
+      float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = s; i <= fin; ++i) {
+        if (sh->unit[i] != ui) continue;
+        const float2 x = sh->ml[i >> 1][i & 1][row];
+        const float a = ex2_approx(x.x - mm);
+        const float* from = reinterpret_cast<const float*>(i & 1 ? &sh->ring[i >> 1][0][0] : sh->piece[i >> 1]);
+        const float4 v = reinterpret_cast<const float4*>(from + row * kHeadDim)[lane ^ (lane >> 2 & 3)];
+        ll = fmaf(x.y, a, ll);
+        oo.x = fmaf(v.x, a, oo.x);
+        oo.y = fmaf(v.y, a, oo.y);
+        oo.z = fmaf(v.z, a, oo.z);
+        oo.w = fmaf(v.w, a, oo.w);
+      }
+      if (sh->begins[s] && sh->ends[fin]) {
+        kv4_write_row(p, u, row, lane, mm, ll, oo);
+      } else {
+        float* part = p.part + (int64_t)(2 * cta + (sh->begins[s] ? 1 : 0)) * (R * 130);
+        reinterpret_cast<float4*>(part + row * kHeadDim)[lane] = oo;
+        if (lane == 0) *reinterpret_cast<float2*>(part + R * kHeadDim + 2 * row) = make_float2(mm, ll);
+      }
+    }
+    s = e;
   }
 }
 
@@ -769,19 +881,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
 
 constexpr int kKv4JoinThreads = 128;
 
-// The CTA whose range holds tile x of `all`.
+// The CTA whose range holds half tile x of `all`: the last one that begins at
+// or before it.
 __device__ __forceinline__ int kv4_cta_of(int64_t x, int64_t all, int ctas) {
   return (int)(((x + 1) * ctas + all - 1) / all) - 1;
 }
 
-// One warp per (unit, row) whose tiles lie in more than one CTA's range: the
-// partial results in order. Rows without keys get their zero here.
+// One CTA per (unit, row) whose tiles lie in more than one CTA's range: each
+// of its warps takes every fourth partial result, all at once (a loop that
+// carries the maximum along waits for each in turn: 38 us for 64 of them
+// against 4), and the four sums meet in a fixed order. Rows without keys get
+// their zero here.
 __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
-  const int lane = threadIdx.x & 31;
-  const int64_t idx = ((int64_t)blockIdx.x * kKv4JoinThreads + threadIdx.x) >> 5;
-  const int ui = (int)(idx / p.R), row = (int)(idx % p.R);
-  if (ui >= p.slots * p.Hkv) return;
+  __shared__ float s_l[kKv4JoinThreads / 32];
+  __shared__ float4 s_o[kKv4JoinThreads / 32][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ui = blockIdx.x / p.R, row = blockIdx.x % p.R;
   const Kv4Unit u = p.units[ui];
   if (row >= u.rows) return;
   int c0 = 0, c1 = -1;
@@ -789,37 +905,42 @@ __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams
     const int64_t all = p.before[p.slots * p.Hkv], x = p.before[ui];
     const int ctas = kv4_ctas(p, all);
     c0 = kv4_cta_of(x, all, ctas);
-    c1 = kv4_cta_of(x + u.tiles - 1, all, ctas);
+    c1 = kv4_cta_of(x + 2 * u.tiles - 1, all, ctas);
     if (c0 == c1) return;  // written by the CTA itself
   }
-  const int per = p.R * 130;
-  float mm = kKv4Low, ll = 0.f;
-  float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0; c <= c1; ++c) {
-    const float* part = p.part + (int64_t)(2 * c + (c == c0 ? 1 : 0)) * per;
-    const float2 x = __ldcg(reinterpret_cast<const float2*>(part + p.R * kHeadDim) + row);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(part + row * kHeadDim) + lane);
-    const float m2 = fmaxf(mm, x.x);
-    const float a = ex2_approx(mm - m2), e = ex2_approx(x.x - m2);
-    ll = ll * a + x.y * e;
-    oo.x = oo.x * a + v.x * e;
-    oo.y = oo.y * a + v.y * e;
-    oo.z = oo.z * a + v.z * e;
-    oo.w = oo.w * a + v.w * e;
-    mm = m2;
-  }
-  const int rr = u.row0 + row;
-  const int64_t t = u.t0 + rr / p.G;
-  const int hq = u.h * p.G + rr % p.G;
-  const float inv = ll > 0.f ? 1.f / ll : 0.f;
-  __nv_bfloat16* out = p.out + (t * p.Hq + hq) * kHeadDim;
-  const float v[4] = {oo.x, oo.y, oo.z, oo.w};
+  const int64_t per = p.R * 130;
+  auto part = [&](int c) { return p.part + (2 * c + (c == c0 ? 1 : 0)) * per; };
+  auto ml = [&](int c) { return __ldcg(reinterpret_cast<const float2*>(part(c) + p.R * kHeadDim) + row); };
+  float mm = kKv4Low;
+  for (int c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, ml(c).x);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int at = lane * 4 + i;
-    out[(at & 7) * 16 + (at >> 3)] = __float2bfloat16(v[i] * inv);
+  for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, d));
+  float ll = 0.f;
+  float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int c = c0 + warp; c <= c1; c += 4) {
+    const float2 x = ml(c);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(part(c) + row * kHeadDim) + lane);
+    const float e = ex2_approx(x.x - mm);
+    ll = fmaf(x.y, e, ll);
+    oo.x = fmaf(v.x, e, oo.x);
+    oo.y = fmaf(v.y, e, oo.y);
+    oo.z = fmaf(v.z, e, oo.z);
+    oo.w = fmaf(v.w, e, oo.w);
   }
-  if (lane == 0) p.lse[(int64_t)hq * p.total + t] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+  s_o[warp][lane] = oo;
+  if (lane == 0) s_l[warp] = ll;
+  __syncthreads();
+  if (warp) return;
+  for (int w = 1; w < kKv4JoinThreads / 32; ++w) {
+    const float4 v = s_o[w][lane];
+    ll += s_l[w];
+    oo.x += v.x;
+    oo.y += v.y;
+    oo.z += v.z;
+    oo.w += v.w;
+  }
+  kv4_write_row(p, u, row, lane, mm, ll, oo);
 }
 
 // ------------------------------------------------------------------ accumulated weights
@@ -835,7 +956,7 @@ __global__ void __launch_bounds__(kKv4WeightThreads, 2) kv4_weight_kernel(Kv4Att
   const int64_t tile = (int64_t)blockIdx.x * (kKv4WeightThreads / 32) + (threadIdx.x >> 5);
   const int b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
   int t0;
-  const int n = kv4_queries(p, b, &t0);
+  const int n = kv4_queries(p, p.cu, b, &t0);
   const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
   const int key0 = (int)(tile * kKv4Tile), pos0 = len - n, rows = n * p.G;
   if (n == 0 || key0 >= len || tile >= p.tiles) return;

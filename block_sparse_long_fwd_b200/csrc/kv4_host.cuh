@@ -217,9 +217,10 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   const bool few = total * p.G <= (int64_t)moba::Kv4Few::R * batch;
   p.R = few ? moba::Kv4Few::R : moba::Kv4Many::R;
   const int64_t slots = total * p.G / p.R + batch;
-  if (slots * heads_kv > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
+  if (slots * heads_kv * p.R > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
   p.slots = (int)slots;
   p.ctas = dev.sms;
+  p.warps = few ? moba::Kv4Few::WARPS : moba::Kv4Many::WARPS;
   const int64_t nu = slots * heads_kv;
   p.list_cap = kmean ? (int)std::min<int64_t>(p.blocks, (int64_t)p.R * topk) : 0;
   // the gate: up to 8 CTAs share a unit's scores while there are few units
@@ -228,14 +229,13 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   const int64_t clusters = std::min<int64_t>(nu, 4 * dev.sms / csize);
   Carve c;
   const size_t o_units = c.take((size_t)nu * sizeof(moba::Kv4Unit)), o_before = c.take((size_t)(nu + 1) * 8);
-  const size_t o_start = c.take((size_t)p.ctas * 8), o_list = c.take((size_t)nu * p.list_cap * 8);
+  const size_t o_list = c.take((size_t)nu * p.list_cap * 8);
   const size_t o_chosen = c.take((size_t)nu * p.blocks * 4);
   const size_t o_scores = c.take((size_t)clusters * p.R * p.means * 8);
   const size_t o_part = c.take((size_t)2 * p.ctas * p.R * 130 * 4);
   const Runner run = [&](uint8_t* ws, cudaStream_t st) -> int {
     p.units = reinterpret_cast<moba::Kv4Unit*>(ws + o_units);
     p.before = reinterpret_cast<int64_t*>(ws + o_before);
-    p.start = reinterpret_cast<int2*>(ws + o_start);
     p.list = reinterpret_cast<uint2*>(ws + o_list);
     p.chosen = reinterpret_cast<uint32_t*>(ws + o_chosen);
     p.scores = reinterpret_cast<double*>(ws + o_scores);
@@ -255,12 +255,9 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
       cfg.numAttrs = 2;
       MOBA_CUDA(cudaLaunchKernelEx(&cfg, moba::kv4_gate_kernel, p));
     }
-    launch_chained(moba::kv4_plan_kernel, dim3(1), dim3(moba::kKv4PlanThreads), 0, st, p);
     if (few) launch_kv4_attn<moba::Kv4Few>(p, st);
     else launch_kv4_attn<moba::Kv4Many>(p, st);
-    launch_chained(moba::kv4_join_kernel,
-                   dim3((unsigned)((nu * p.R * 32 + moba::kKv4JoinThreads - 1) / moba::kKv4JoinThreads)),
-                   dim3(moba::kKv4JoinThreads), 0, st, p);
+    launch_chained(moba::kv4_join_kernel, dim3((unsigned)(nu * p.R)), dim3(moba::kKv4JoinThreads), 0, st, p);
     if (acc) {
       const int per = moba::kKv4WeightThreads / 32;
       launch_chained(moba::kv4_weight_kernel, dim3((unsigned)((p.tiles + per - 1) / per), batch * heads_kv),

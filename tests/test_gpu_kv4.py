@@ -297,6 +297,23 @@ def test_attention_of_small_and_large_scores(qscale):
     attend_case(1, 2, [1000], [40], qscale=qscale, seed=4)
 
 
+@pytest.mark.parametrize("kscale,vscale", [(2.0**-9, 2.0**-9), (1.0, 5000.0), (6000.0, 1.0), (2000.0, 2.0**-12)])
+def test_attention_over_keys_and_values_of_every_size(kscale, vscale):
+    # scales from the smallest to the largest: nothing overflows or flushes on the way to the products. One channel
+    # in 32 is twenty times the others (a zero point at either end of its range)
+    rng = np.random.default_rng(17)
+    L, hkv, G = 500, 2, 4
+    x = rng.standard_normal((2, hkv, 512, 128))
+    x[..., ::32] *= np.where(rng.random((2, hkv, 512, 4)) < 0.5, 20, 1)
+    k, v = x[0] * kscale, x[1] * vscale
+    tiles = ref.pack(f64(bf16(k)), f64(bf16(v)))
+    q = bf16(rng.standard_normal((1, hkv * G, 128)) / kscale)
+    a = torch.zeros(1, hkv, 512, device="cuda")
+    out, lse = moba.kv4_attend(q.cuda(), torch.from_numpy(tiles[None]).cuda(), ints([L]), acc=a)
+    ok()
+    check_attend((out, lse, a, torch.zeros_like(a)), f64(q), [ref.unpack(tiles)], [L], [1], hkv)
+
+
 def test_equal_scores_go_to_the_lower_block():
     # blocks 1, 3 and 4 are equal and best; topk 3 takes 1 and 3 beside the own block
     hkv, cap, B = 1, 1024, 128
