@@ -525,8 +525,8 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p) {
   constexpr int NT = C::NT, R = C::R;
   grid_dependency_sync();
-  extern __shared__ uint8_t smem_raw[];
-  auto* sh = reinterpret_cast<typename C::Shared*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  auto* sh = reinterpret_cast<typename C::Shared*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2 * C::WARPS; ++i) mbar_init(&sh->full[0][0] + i, 1);
@@ -545,8 +545,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
   const int piece_dst = (lane & 2 ? kKv4HalfRows : 0) + (lane & 1 ? kKv4HalfParams : 0);
   const int tpb = p.B / kKv4Tile;
   int c_ui = range.unit - 1, c_off = range.off, c_left = n, c_end = 0, c_at = 0, c_in = 0;
-  const uint8_t* c_src = nullptr;
-  int key_a = 0, key_b = 0;             // first keys of the half tile in use and of the next
+  const uint8_t* c_src = nullptr;       // the lane's piece of the half tile (with a gate, of the sequence's first)
+  int key_a = 0, key_b = 0, c_key = 0;  // first keys of the half tile in use, of the next and of the one after
   uint32_t rows_a = ~0u, rows_b = ~0u;  // rows that chose their blocks
   auto issue = [&](int d) {
     key_a = key_b;
@@ -558,27 +558,34 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
       while (c_end == 0);
       const Kv4Unit u = p.units[c_ui];
       c_src = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, u.b, u.h, 0) + piece;
-      c_at = (c_off >> 1) / tpb;
-      c_in = (c_off >> 1) - c_at * tpb;
+      if (p.kmean) {
+        c_at = (c_off >> 1) / tpb;
+        c_in = (c_off >> 1) - c_at * tpb;
+      } else {
+        c_src += (int64_t)(c_off >> 1) * kKv4TileBytes + (c_off & 1) * piece_half;
+        c_key = c_off * kKv4HalfTok;
+      }
     }
     uint64_t* bar = &sh->full[warp][d];
     if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kKv4HalfRows);
-    int tile = c_off >> 1;
-    const int half = c_off & 1;
+    const uint8_t* src = c_src;
     if (p.kmean) {
       if (c_in == tpb) c_in = 0, ++c_at;
       const uint2 e = p.list[(int64_t)c_ui * p.list_cap + c_at];
-      tile = (int)e.x * tpb + c_in;
+      const int tile = (int)e.x * tpb + c_in, half = c_off & 1;
+      src += (int64_t)tile * kKv4TileBytes + half * piece_half;
+      key_b = tile * kKv4Tile + half * kKv4HalfTok;
       rows_b = e.y;
       c_in += half;
+    } else {
+      key_b = c_key;
+      c_key += kKv4HalfTok;
+      c_src += c_off & 1 ? kKv4TileBytes - piece_half : piece_half;
     }
-    key_b = tile * kKv4Tile + half * kKv4HalfTok;
     ++c_off;
     --c_left;
     __syncwarp();
-    if (lane < 4)
-      bulk_load(sh->ring[warp][d] + piece_dst, c_src + (int64_t)tile * kKv4TileBytes + half * piece_half, piece_half,
-                bar);
+    if (lane < 4) bulk_load(sh->ring[warp][d] + piece_dst, src, piece_half, bar);
   };
   issue(0);
   issue(1);
@@ -596,7 +603,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
     if (stop == k) continue;
     // the rows' fragments, scales, and last keys (of this lane's two rows of each group of eight)
     uint32_t qf[16];
-    float qs[NT][2];
+    uint64_t qs[NT];
     int last[NT][2];
     const int first_pos = u.pos0 + u.row0 / p.G, last_pos = kv4_last_pos(p, u);
 #pragma unroll
@@ -605,8 +612,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
       const __nv_bfloat16* row =
           x < u.rows ? p.q + ((int64_t)(u.t0 + rr / p.G) * p.Hq + u.h * p.G + rr % p.G) * kHeadDim + qd * 32 : nullptr;
       const float s = kv4_query_fragment(row, p.scale_log2, qf);
-      qs[nt][0] = __shfl_sync(0xFFFFFFFFu, s, qd * 8);
-      qs[nt][1] = __shfl_sync(0xFFFFFFFFu, s, qd * 8 + 4);
+      qs[nt] = f2_pack(__shfl_sync(0xFFFFFFFFu, s, qd * 8), __shfl_sync(0xFFFFFFFFu, s, qd * 8 + 4));
       if constexpr (!C::QREG) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) sh->q[warp][nt][i][lane] = make_uint2(qf[2 * i], qf[2 * i + 1]);  // read back by itself
@@ -619,9 +625,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
     }
     const uint32_t all_rows = (1u << u.rows) - 1;
 
-    float o[NT][8][4] = {}, m[NT][2], l[NT][2];
+    float o[NT][8][4] = {};
+    uint64_t nm[NT], l2[NT];  // minus the reference, and the sum, of the lane's two rows
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = kKv4Low, l[nt][0] = l[nt][1] = 0.f;
+    for (int nt = 0; nt < NT; ++nt) nm[nt] = f2_pack(-kKv4Low, -kKv4Low), l2[nt] = 0;
 
     const int k0 = k;
     for (; k < stop; ++k) {
@@ -689,37 +696,35 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
       uint32_t pf[NT][2][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float t[2][4], top = -INFINITY;
+        float t[2][4];
         auto shifted = [&] {
-          const uint64_t qs2 = f2_pack(qs[nt][0], qs[nt][1]), m2 = f2_pack(-m[nt][0], -m[nt][1]);
 #pragma unroll
           for (int g = 0; g < 2; ++g)
 #pragma unroll
             for (int x = 0; x < 4; x += 2) {
-              const uint64_t y = f2_fma(f2_pack(sc[g][nt][x], sc[g][nt][x + 1]), qs2, m2);
+              const uint64_t y = f2_fma(f2_pack(sc[g][nt][x], sc[g][nt][x + 1]), qs[nt], nm[nt]);
               t[g][x] = f2_lo(y);
               t[g][x + 1] = f2_hi(y);
             }
         };
         shifted();
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) top = fmaxf(top, t[g][x]);
+        const float top = fmaxf(fmax3(fmax3(t[0][0], t[0][1], t[0][2]), fmax3(t[0][3], t[1][0], t[1][1]), t[1][2]), t[1][3]);
         if (__any_sync(0xFFFFFFFFu, top > 15.f)) {
+          float a2[2], n2[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float mx = fmaxf(fmaxf(sc[0][nt][x], sc[0][nt][x + 2]), fmaxf(sc[1][nt][x], sc[1][nt][x + 2])) * qs[nt][x];
+            const float q1 = x ? f2_hi(qs[nt]) : f2_lo(qs[nt]), m1 = -(x ? f2_hi(nm[nt]) : f2_lo(nm[nt]));
+            float mx = fmaxf(fmaxf(sc[0][nt][x], sc[0][nt][x + 2]), fmaxf(sc[1][nt][x], sc[1][nt][x + 2])) * q1;
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-            if (mx > m[nt][x] + 15.f) {
-              const float a = ex2_approx(m[nt][x] - (mx - 12.f));
-              m[nt][x] = mx - 12.f;
-              l[nt][x] *= a;
+            for (int d2 = 4; d2 < 32; d2 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d2));
+            const bool move = mx > m1 + 15.f;
+            n2[x] = move ? 12.f - mx : -m1;
+            a2[x] = move ? ex2_approx(m1 - (mx - 12.f)) : 1.f;
 #pragma unroll
-              for (int mt = 0; mt < 8; ++mt) o[nt][mt][x] *= a, o[nt][mt][x + 2] *= a;
-            }
+            for (int mt = 0; mt < 8; ++mt) o[nt][mt][x] *= a2[x], o[nt][mt][x + 2] *= a2[x];
           }
+          nm[nt] = f2_pack(n2[0], n2[1]);
+          l2[nt] = f2_pack(f2_lo(l2[nt]) * a2[0], f2_hi(l2[nt]) * a2[1]);
           shifted();
         }
 #pragma unroll
@@ -727,9 +732,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
           float e[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) e[x] = ex2_approx(t[g][x]);
-          const uint64_t sum = f2_add(f2_pack(l[nt][0], l[nt][1]), f2_add(f2_pack(e[0], e[1]), f2_pack(e[2], e[3])));
-          l[nt][0] = f2_lo(sum);
-          l[nt][1] = f2_hi(sum);
+          l2[nt] = f2_add(l2[nt], f2_add(f2_pack(e[0], e[1]), f2_pack(e[2], e[3])));
           pf[nt][g][0] = movmatrix(pack_half2(e[0], e[1]));
           pf[nt][g][1] = movmatrix(pack_half2(e[2], e[3]));
         }
@@ -769,6 +772,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
     }
 
     // ---- this warp's part of the unit: all of it is a result, else a piece to be joined
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = -f2_lo(nm[nt]), m[nt][1] = -f2_hi(nm[nt]);
+      l[nt][0] = f2_lo(l2[nt]), l[nt][1] = f2_hi(l2[nt]);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -35,7 +35,7 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 
 template <class C>
 constexpr size_t kv4_attn_smem() {
-  return sizeof(typename C::Shared) + 128;
+  return sizeof(typename C::Shared);
 }
 
 template <class C>
