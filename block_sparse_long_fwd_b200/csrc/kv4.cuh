@@ -100,52 +100,62 @@ __device__ __forceinline__ uint32_t kv4_scale_code(float step) {
   return min(max(code, kKv4ScaleMin), kKv4ScaleMax);
 }
 
-// floor(x / s + 1/2) for |x| <= 28800 and a scale s: the rounded product with
-// 1/s is off by one at most, and the remainder x - r s is exact in fp32 (x and
-// s r have few bits), so comparing it with s/2 settles it.
-__device__ __forceinline__ float kv4_round_quotient(float x, float s, float inv) {
-  float r = rintf(x * inv);
-  const float d = fmaf(-r, s, x);
-  if (d >= 0.5f * s) r += 1.f;
-  if (d < -0.5f * s) r -= 1.f;
-  return r;
-}
+// A nudge for floor(x / s + 1/2): x has 8 significant bits and s four, so a
+// quotient between 1/2 and 16 that is not k + 1/2 is at least 2^-10 away from
+// it, while x * fl(1/s) is off by less than 2^-18: with the nudge added, halves
+// go up and nothing else moves.
+constexpr float kKv4Nudge = 1.f / 4096;
 
-// One lane's eight channels of a row; four neighbouring lanes hold a group.
-// Returns the code word, and the group's parameter.
-__device__ __forceinline__ uint32_t kv4_quantise(uint4 raw, uint32_t* par) {
-  float x[8];
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+// A group of 32 channels (bf16, four uint4) of a row: its four code words, and
+// its parameter. One thread holds a whole group: no exchange, and scale and
+// zero point are found once for 32 codes, which then take two fused
+// multiply-adds each: floor(x / s + z + 1/2) / 16 saturated to [0, 1], and
+// that by just under 16 onto 2^23, rounded down.
+__device__ __forceinline__ uint4 kv4_quantise(const uint4 (&raw)[4], uint32_t* par) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
   float lo = 0.f, hi = 0.f;
+  __nv_bfloat162 lo2 = __float2bfloat162_rn(0.f), hi2 = lo2;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[2 * j] = __uint_as_float(w[j] << 16);
-    x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  for (int i = 0; i < 16; ++i) {
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+    lo2 = __hmin2_nan(lo2, x);
+    hi2 = __hmax2_nan(hi2, x);
   }
+  lo = fminf(__low2float(lo2), __high2float(lo2));
+  hi = fmaxf(__low2float(hi2), __high2float(hi2));
+  // a NaN stays in lo2 and hi2; with magnitudes over 28800 it takes the way through fp32
+  const float sum = (__low2float(lo2) + __high2float(lo2)) + (__low2float(hi2) + __high2float(hi2));
+  const bool odd = !(sum == sum) || lo < -kKv4Top || hi > kKv4Top;
+  auto clean = [](float x) { return x == x ? fminf(fmaxf(x, -kKv4Top), kKv4Top) : 0.f; };
+  if (odd) {
+    lo = hi = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    x[j] = x[j] == x[j] ? fminf(fmaxf(x[j], -kKv4Top), kKv4Top) : 0.f;  // a NaN is stored as zero
-    lo = fminf(lo, x[j]);
-    hi = fmaxf(hi, x[j]);
-  }
-#pragma unroll
-  for (int d = 1; d < 4; d <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, d));
-    hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, d));
+    for (int i = 0; i < 16; ++i) {
+      const float x = clean(__uint_as_float(w[i] << 16)), y = clean(__uint_as_float(w[i] & 0xFFFF0000u));
+      lo = fminf(lo, fminf(x, y));
+      hi = fmaxf(hi, fmaxf(x, y));
+    }
   }
   const uint32_t code = kv4_scale_code(__fdiv_rn(hi - lo, 15.f));
-  const float s = kv4_scale(code << 7);
-  const float inv = __fdiv_rn(1.f, s);
-  const float z = fminf(kv4_round_quotient(-lo, s, inv), 15.f);
-  uint32_t word = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float c0 = fminf(fmaxf(kv4_round_quotient(x[2 * j], s, inv) + z, 0.f), 15.f);
-    const float c1 = fminf(fmaxf(kv4_round_quotient(x[2 * j + 1], s, inv) + z, 0.f), 15.f);
-    word |= (uint32_t)c0 << (4 * j) | (uint32_t)c1 << (4 * j + 16);
-  }
+  const float inv = __frcp_rn(kv4_scale(code << 7));
+  const float z = fminf(__fadd_rd(fmaf(-lo, inv, 0.5f + kKv4Nudge), 8388608.f) - 8388608.f, 15.f);
+  const float k = inv * 0.0625f, c0 = (z + (0.5f + kKv4Nudge)) * 0.0625f;
   *par = code << 7 | (uint32_t)z;
-  return word;
+  auto one = [&](float x) {
+    if (odd) x = clean(x);
+    return __float_as_uint(__fmaf_rd(__saturatef(fmaf(x, k, c0)), 16.f - 1.f / 16384, 8388608.f));
+  };
+  uint32_t out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t pair[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      pair[j] = __byte_perm(one(__uint_as_float(w[4 * i + j] << 16)), one(__uint_as_float(w[4 * i + j] & 0xFFFF0000u)),
+                            0x5410);
+    out[i] = (pair[0] + pair[1] * 16u) + (pair[2] * 256u + pair[3] * 4096u);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 struct Kv4AppendParams {
@@ -159,48 +169,43 @@ struct Kv4AppendParams {
 
 constexpr int kKv4AppendThreads = 256;
 
-// Half a warp per row (token, kv head): 16 lanes of 8 channels, keys and
-// values together. HBM-bound: 512 bytes read and 144 written a row.
+// Four threads per row (token, kv head), a group of keys and the group of
+// values each. HBM-bound: 512 bytes read and 144 written a row.
 __global__ void __launch_bounds__(kKv4AppendThreads) kv4_append_kernel(Kv4AppendParams p) {
   grid_dependency_sync();
-  const int lane = threadIdx.x & 15;
-  const int64_t row = ((int64_t)blockIdx.x * kKv4AppendThreads + threadIdx.x) >> 4;
+  const int g = threadIdx.x & 3;
+  const int64_t row = ((int64_t)blockIdx.x * kKv4AppendThreads + threadIdx.x) >> 2;
+  if (row >= p.total * p.heads) return;
+  uint4 rk[4], rv[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) rk[i] = __ldg(reinterpret_cast<const uint4*>(p.k + row * kHeadDim + g * 32) + i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) rv[i] = __ldg(reinterpret_cast<const uint4*>(p.v + row * kHeadDim + g * 32) + i);
   const int64_t t = row / p.heads;
   const int h = (int)(row - t * p.heads);
-  int b = -1;
-  int64_t at = 0;
-  if (t < p.total) {
-    if (p.cu) {
-      b = kv4_sequence(p.cu, p.batch, t);
-      if (b >= 0) at = (int64_t)p.start[b] + (t - p.cu[b]);
-    } else {
-      const int64_t n = p.total / p.batch;
-      b = (int)(t / n);
-      at = (int64_t)p.start[b] + (t - b * n);
-    }
-    if (b >= 0 && (at < 0 || at >= p.tiles * kKv4Tile)) {  // no room: skipped and reported
-      record_status(MOBA_ERR_DEVICE_CHECK);
-      b = -1;
-    }
+  int b;
+  int64_t at;
+  if (p.cu) {
+    b = kv4_sequence(p.cu, p.batch, t);
+    if (b < 0) return;
+    at = (int64_t)p.start[b] + (t - p.cu[b]);
+  } else {
+    const int64_t n = p.total / p.batch;
+    b = (int)(t / n);
+    at = (int64_t)p.start[b] + (t - b * n);
   }
-  uint4 rk = make_uint4(0, 0, 0, 0), rv = rk;
-  if (b >= 0) {
-    rk = __ldg(reinterpret_cast<const uint4*>(p.k + row * kHeadDim) + lane);
-    rv = __ldg(reinterpret_cast<const uint4*>(p.v + row * kHeadDim) + lane);
+  if (at < 0 || at >= p.tiles * kKv4Tile) {  // no room: skipped and reported
+    record_status(MOBA_ERR_DEVICE_CHECK);
+    return;
   }
-  uint32_t pk, pv;
-  const uint32_t wk = kv4_quantise(rk, &pk);
-  const uint32_t wv = kv4_quantise(rv, &pv);
-  if (b < 0) return;
   const int tok = (int)(at % kKv4Tile);
   uint8_t* tile = p.kv4 + kv4_tile_off(p.tiles, p.heads, b, h, at / kKv4Tile);
-  *reinterpret_cast<uint32_t*>(tile + kv4_word_off(tok, lane, false)) = wk;
-  *reinterpret_cast<uint32_t*>(tile + kKv4Half + kv4_word_off(tok, lane, true)) = wv;
-  if ((lane & 3) == 0) {
-    *reinterpret_cast<uint16_t*>(tile + kKv4Params + tok * 8 + (lane >> 2) * 2) = (uint16_t)pk;
-    *reinterpret_cast<uint16_t*>(tile + kKv4Half + kKv4Params + tok * 8 + (lane >> 2) * 2) = (uint16_t)pv;
-  }
-  if (p.acc && lane == 0) p.acc[((int64_t)b * p.heads + h) * p.tiles * kKv4Tile + at] = 0.f;
+  uint32_t par;
+  *reinterpret_cast<uint4*>(tile + kv4_word_off(tok, 4 * g, false)) = kv4_quantise(rk, &par);
+  *reinterpret_cast<uint16_t*>(tile + kKv4Params + tok * 8 + g * 2) = (uint16_t)par;
+  *reinterpret_cast<uint4*>(tile + kKv4Half + kv4_word_off(tok, 4 * g, true)) = kv4_quantise(rv, &par);
+  *reinterpret_cast<uint16_t*>(tile + kKv4Half + kKv4Params + tok * 8 + g * 2) = (uint16_t)par;
+  if (p.acc && g == 0) p.acc[((int64_t)b * p.heads + h) * p.tiles * kKv4Tile + at] = 0.f;
 }
 
 // ------------------------------------------------------------------ load
@@ -213,82 +218,46 @@ struct Kv4LoadParams {
   __nv_bfloat16 *k, *v;  // [batch][n][heads][128]
 };
 
-constexpr int kKv4LoadThreads = 256;
+constexpr int kKv4LoadThreads = 256, kKv4LoadRows = 4;
 
-// Half a warp per row, 8 channels a lane: 144 bytes read, 512 written.
+// Half a warp per row, 8 channels a lane, four rows of keys and values at a
+// time: 144 bytes read, 512 written a row, HBM-bound.
 __global__ void __launch_bounds__(kKv4LoadThreads) kv4_load_kernel(Kv4LoadParams p) {
   grid_dependency_sync();
   const int lane = threadIdx.x & 15;
-  const int64_t row = ((int64_t)blockIdx.x * kKv4LoadThreads + threadIdx.x) >> 4;
-  if (row >= (int64_t)p.batch * p.n * p.heads) return;
-  const int64_t t = row / p.heads;
-  const int h = (int)(row - t * p.heads);
-  const int b = (int)(t / p.n);
-  const int64_t at = (p.first ? (int64_t)p.first[b] : 0) + (t - b * p.n);
-  const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
-  uint4 o[2] = {};
-  if (at >= 0 && at < len) {
+  const int64_t rows = (int64_t)p.batch * p.n * p.heads;
+  const int64_t row0 = (int64_t)blockIdx.x * (kKv4LoadThreads / 16 * kKv4LoadRows) + (threadIdx.x >> 4);
+  uint32_t word[kKv4LoadRows][2], par[kKv4LoadRows][2];
+#pragma unroll
+  for (int i = 0; i < kKv4LoadRows; ++i) {
+    const int64_t row = row0 + i * (kKv4LoadThreads / 16);
+    word[i][0] = word[i][1] = par[i][0] = par[i][1] = 0;
+    if (row >= rows) continue;
+    const int64_t t = row / p.heads;
+    const int h = (int)(row - t * p.heads);
+    const int b = (int)(t / p.n);
+    const int64_t at = (p.first ? (int64_t)p.first[b] : 0) + (t - b * p.n);
+    if (at < 0 || at >= kv4_length(p.lengths, b, p.tiles * kKv4Tile)) continue;
     const int tok = (int)(at % kKv4Tile);
     const uint8_t* tile = p.kv4 + kv4_tile_off(p.tiles, p.heads, b, h, at / kKv4Tile);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const uint8_t* half = tile + s * kKv4Half;
-      const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(half + kv4_word_off(tok, lane, s == 1)));
-      const uint32_t par = __ldg(reinterpret_cast<const uint16_t*>(half + kKv4Params + tok * 8 + (lane >> 2) * 2));
-      float x[8];
-      kv4_decode(word, par, x);
-      o[s] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                        pack_bf16x2(x[6], x[7]));
-    }
-  }
-  reinterpret_cast<uint4*>(p.k + row * kHeadDim)[lane] = o[0];
-  reinterpret_cast<uint4*>(p.v + row * kHeadDim)[lane] = o[1];
-}
-
-// ------------------------------------------------------------------ pool
-
-struct Kv4PoolParams {
-  const uint8_t* kv4;
-  const int32_t* lengths;
-  int64_t tiles;
-  int heads, B, blocks;  // blocks = capacity / B
-  float* kmean;          // [batch][heads][blocks][128]
-};
-
-constexpr int kKv4PoolThreads = 256;
-
-// One CTA per (block, head, sequence): thread = (code word, every 16th token),
-// fp32 sums in a fixed order. Blocks that the sequence has not completed are
-// written as zero.
-__global__ void __launch_bounds__(kKv4PoolThreads) kv4_pool_kernel(Kv4PoolParams p) {
-  grid_dependency_sync();
-  __shared__ float part[16][kHeadDim];
-  const int j = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
-  const int w = threadIdx.x & 15, lane = threadIdx.x >> 4;
-  float sum[8] = {};
-  const bool complete = (int64_t)(j + 1) * p.B <= len;
-  if (complete) {
-    const int64_t t0 = (int64_t)j * p.B;
-    for (int i = lane; i < p.B; i += 16) {
-      const int64_t t = t0 + i;
-      const int tok = (int)(t % kKv4Tile);
-      const uint8_t* tile = p.kv4 + kv4_tile_off(p.tiles, p.heads, b, h, t / kKv4Tile);
-      const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(tile + kv4_word_off(tok, w, false)));
-      const uint32_t par = __ldg(reinterpret_cast<const uint16_t*>(tile + kKv4Params + tok * 8 + (w >> 2) * 2));
-      float x[8];
-      kv4_decode(word, par, x);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) sum[c] += x[c];
+      word[i][s] = __ldg(reinterpret_cast<const uint32_t*>(half + kv4_word_off(tok, lane, s == 1)));
+      par[i][s] = __ldg(reinterpret_cast<const uint16_t*>(half + kKv4Params + tok * 8 + (lane >> 2) * 2));
     }
   }
 #pragma unroll
-  for (int c = 0; c < 8; ++c) part[lane][w * 8 + c] = sum[c];
-  __syncthreads();
-  if (threadIdx.x < kHeadDim) {
-    float s = 0.f;
-    for (int i = 0; i < 16; ++i) s += part[i][threadIdx.x];
-    p.kmean[(((int64_t)b * p.heads + h) * p.blocks + j) * kHeadDim + threadIdx.x] = complete ? s / (float)p.B : 0.f;
+  for (int i = 0; i < kKv4LoadRows; ++i) {
+    const int64_t row = row0 + i * (kKv4LoadThreads / 16);
+    if (row >= rows) continue;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float x[8];
+      kv4_decode(word[i][s], par[i][s], x);
+      reinterpret_cast<uint4*>((s ? p.v : p.k) + row * kHeadDim)[lane] =
+          make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
   }
 }
 
@@ -307,6 +276,8 @@ struct Kv4EvictParams {
 };
 
 constexpr int kKv4SelectThreads = 1024;
+constexpr int kKv4SelectItems = 16;  // neighbouring weights a thread takes at a time
+constexpr int kKv4SelectBins = 2048;
 
 // Weights as integers of the same order; a NaN below everything, -0 as 0.
 __device__ __forceinline__ uint32_t kv4_weight_key(float w) {
@@ -336,90 +307,214 @@ __device__ __forceinline__ uint32_t kv4_block_scan(uint32_t x, uint32_t* warp_su
   return before + s - x;
 }
 
-// The tokens that stay, for one (head, sequence) a CTA: the last `recent`, and
-// of the others the `budget - recent` of the largest weight, equal weights to
-// the lower index. A radix selection finds the smallest kept weight in four
-// passes of eight bits, then one pass writes the kept indexes in order.
+__device__ __forceinline__ void kv4_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A word of another CTA's shared memory, at the same place as `p` in ours.
+__device__ __forceinline__ uint32_t kv4_remote_ld(const uint32_t* p, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void kv4_remote_st(uint32_t* p, uint32_t rank, uint32_t v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// The tokens that stay, a cluster of CTAs for one (head, sequence), a
+// contiguous part of its weights each: the last `recent`, and of the others
+// the `budget - recent` of the largest weight, equal weights to the lower
+// index. A radix selection finds the smallest kept weight in three passes of
+// 11, 11 and 10 bits (counts per CTA, summed and searched by the first one
+// through distributed shared memory); a last pass writes the kept indexes,
+// each thread's neighbouring weights at its place in the order. The weights
+// are read four times, from L2 after the first.
 __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictParams p) {
   grid_dependency_sync();
-  __shared__ uint32_t hist[256];
+  __shared__ uint32_t hist[kKv4SelectBins];
   __shared__ uint32_t warp_sums[32];
-  __shared__ uint32_t s_prefix, s_need;
-  const int h = blockIdx.x, b = blockIdx.y;
+  __shared__ uint32_t s_found[2], s_count[2];  // prefix and need; this part's keys above and at the limit
+  uint32_t rank, csize;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+  const int pair = blockIdx.x / csize;  // sequence * heads + head
+  const int h = pair % p.heads, b = pair / p.heads, tid = threadIdx.x;
   const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
-  const int tid = threadIdx.x;
-  if (h == 0 && tid == 0) p.new_lengths[b] = min(len, p.budget);
-  int32_t* kept = p.kept + ((int64_t)b * p.heads + h) * p.budget;
-  if (len <= p.budget) {
-    for (int i = tid; i < p.budget; i += kKv4SelectThreads) kept[i] = i < len ? i : -1;
+  if (h == 0 && rank == 0 && tid == 0) p.new_lengths[b] = min(len, p.budget);
+  int32_t* kept = p.kept + (int64_t)pair * p.budget;
+  if (len <= p.budget) {  // the whole cluster leaves
+    for (int i = rank * kKv4SelectThreads + tid; i < p.budget; i += csize * kKv4SelectThreads) kept[i] = i < len ? i : -1;
     return;
   }
-  const float* acc = p.acc + ((int64_t)b * p.heads + h) * p.tiles * kKv4Tile;
+  const float* acc = p.acc + (int64_t)pair * p.tiles * kKv4Tile;
   const int older = len - p.recent;        // > budget - recent >= 0
   const uint32_t want = p.budget - p.recent;
-  uint32_t prefix = 0, need = want;        // of the keys that share `prefix`, `need` stay
-  if (want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kKv4SelectThreads) hist[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < older; i += kKv4SelectThreads) {
-        const uint32_t key = kv4_weight_key(acc[i]);
-        if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+  for (int i = rank * kKv4SelectThreads + tid; i < p.recent; i += csize * kKv4SelectThreads) kept[want + i] = older + i;
+  if (want == 0) return;
+  const int part = (int)(((int64_t)older + csize * kKv4SelectItems - 1) / (csize * kKv4SelectItems)) * kKv4SelectItems;
+  const int i0 = (int)min((int64_t)rank * part, (int64_t)older), i1 = (int)min((int64_t)i0 + part, (int64_t)older);
+  // a thread's neighbouring weights of a sweep over the part; those outside it come as the key 0 and do not count
+  auto keys = [&](int at, uint32_t (&k)[kKv4SelectItems]) {
+    // acc rows begin at multiples of 64 floats and parts at multiples of 16, but acc itself is 4-byte aligned
+    if (at + kKv4SelectItems <= i1 && (reinterpret_cast<uintptr_t>(acc) & 15) == 0) {
+#pragma unroll
+      for (int x = 0; x < kKv4SelectItems; x += 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(acc + at + x));
+        k[x] = kv4_weight_key(v.x);
+        k[x + 1] = kv4_weight_key(v.y);
+        k[x + 2] = kv4_weight_key(v.z);
+        k[x + 3] = kv4_weight_key(v.w);
       }
-      __syncthreads();
-      if (tid == 0) {
-        uint32_t left = need;
-        int d = 255;
-        while (d > 0 && hist[d] < left) left -= hist[d--];
-        s_prefix = prefix | (uint32_t)d << shift;
-        s_need = left;
-      }
-      __syncthreads();
-      prefix = s_prefix;
-      need = s_need;
+    } else {
+#pragma unroll
+      for (int x = 0; x < kKv4SelectItems; ++x) k[x] = at + x < i1 ? kv4_weight_key(__ldg(acc + at + x)) : 0;
     }
+  };
+  constexpr int kSweep = kKv4SelectThreads * kKv4SelectItems;
+  uint32_t prefix = 0, need = want;        // of the keys that share `prefix`, `need` stay
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 32 : pass == 1 ? 21 : 10;
+    const uint32_t mask = pass == 2 ? 1023u : 2047u;
+    for (int i = tid; i < kKv4SelectBins; i += kKv4SelectThreads) hist[i] = 0;
+    __syncthreads();
+    for (int at = i0 + tid * kKv4SelectItems; at < i1; at += kSweep) {
+      uint32_t k[kKv4SelectItems];
+      keys(at, k);
+#pragma unroll
+      for (int x = 0; x < kKv4SelectItems; ++x)
+        if (at + x < i1 && (pass == 0 || (k[x] >> above) == (prefix >> above)))
+          atomicAdd(&hist[(k[x] >> shift) & mask], 1u);
+    }
+    kv4_cluster_sync();
+    if (rank == 0) {
+      // two bins a thread, from the highest down: the bin in which the need is met
+      uint32_t c[2], total;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int bin = kKv4SelectBins - 1 - (2 * tid + x);
+        c[x] = hist[bin];
+        for (uint32_t r = 1; r < csize; ++r) c[x] += kv4_remote_ld(&hist[bin], r);
+      }
+      uint32_t before = kv4_block_scan(c[0] + c[1], warp_sums, &total);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (before < need && before + c[x] >= need) {
+          const uint32_t found = prefix | (uint32_t)(kKv4SelectBins - 1 - (2 * tid + x)) << shift;
+          for (uint32_t r = 0; r < csize; ++r) {
+            kv4_remote_st(&s_found[0], r, found);
+            kv4_remote_st(&s_found[1], r, need - before);
+          }
+        }
+        before += c[x];
+      }
+    }
+    kv4_cluster_sync();
+    prefix = s_found[0];
+    need = s_found[1];
   }
   // keys above `prefix` stay, and the first `need` equal to it
-  uint32_t kept_before = 0, equal_before = 0;
-  for (int i0 = 0; i0 < older; i0 += kKv4SelectThreads) {
-    const int i = i0 + tid;
-    const uint32_t key = i < older && want > 0 ? kv4_weight_key(acc[i]) : 0;
-    const bool in = i < older && want > 0;
-    const uint32_t eq = in && key == prefix;
-    uint32_t n_eq, n_kept;
-    const uint32_t my_eq = kv4_block_scan(eq, warp_sums, &n_eq);
-    const uint32_t stay = in && (key > prefix || (eq && equal_before + my_eq < need));
-    const uint32_t my = kv4_block_scan(stay, warp_sums, &n_kept);
-    if (stay) kept[kept_before + my] = i;
-    kept_before += n_kept;
-    equal_before += n_eq;
+  uint32_t above = 0, equal = 0;
+  for (int at = i0 + tid * kKv4SelectItems; at < i1; at += kSweep) {
+    uint32_t k[kKv4SelectItems];
+    keys(at, k);
+#pragma unroll
+    for (int x = 0; x < kKv4SelectItems; ++x) {
+      above += at + x < i1 && k[x] > prefix;
+      equal += at + x < i1 && k[x] == prefix;
+    }
   }
-  for (int i = tid; i < p.recent; i += kKv4SelectThreads) kept[want + i] = older + i;
+  uint32_t n_above, n_equal;
+  kv4_block_scan(above, warp_sums, &n_above);
+  kv4_block_scan(equal, warp_sums, &n_equal);
+  if (tid == 0) {
+    s_count[0] = n_above;
+    s_count[1] = n_equal;
+  }
+  kv4_cluster_sync();
+  uint32_t above_before = 0, equal_before = 0;
+  for (uint32_t r = 0; r < rank; ++r) {
+    above_before += kv4_remote_ld(&s_count[0], r);
+    equal_before += kv4_remote_ld(&s_count[1], r);
+  }
+  kv4_cluster_sync();  // no CTA leaves while another may still read its counts
+  for (int s0 = i0; s0 < i1; s0 += kSweep) {
+    const int at = s0 + tid * kKv4SelectItems;
+    uint32_t k[kKv4SelectItems];
+    above = equal = 0;
+    if (at < i1) {
+      keys(at, k);
+#pragma unroll
+      for (int x = 0; x < kKv4SelectItems; ++x) {
+        above += at + x < i1 && k[x] > prefix;
+        equal += at + x < i1 && k[x] == prefix;
+      }
+    }
+    uint32_t a = above_before + kv4_block_scan(above, warp_sums, &n_above);
+    uint32_t e = equal_before + kv4_block_scan(equal, warp_sums, &n_equal);
+    if (at < i1) {
+#pragma unroll
+      for (int x = 0; x < kKv4SelectItems; ++x) {
+        if (at + x >= i1) continue;
+        if (k[x] > prefix) kept[a++ + min(e, need)] = at + x;
+        else if (k[x] == prefix) {
+          if (e < need) kept[a + e] = at + x;
+          ++e;
+        }
+      }
+    }
+    above_before += n_above;
+    equal_before += n_equal;
+  }
 }
 
 constexpr int kKv4MoveThreads = 256;
 
-// Half a warp per kept token: its codes, parameters and weight.
+// Half a warp per kept token, four tokens at a time: codes, parameters and
+// weight. 148 bytes read and as many written a token; HBM-bound.
+constexpr int kKv4MoveTokens = 4;
 __global__ void __launch_bounds__(kKv4MoveThreads) kv4_move_kernel(Kv4EvictParams p) {
   grid_dependency_sync();
   const int lane = threadIdx.x & 15;
-  const int to = (int)(((int64_t)blockIdx.x * kKv4MoveThreads + threadIdx.x) >> 4);
-  if (to >= p.budget) return;
+  const int to0 = (int)(blockIdx.x * (kKv4MoveThreads / 16 * kKv4MoveTokens)) + (threadIdx.x >> 4);
   const int64_t pair = blockIdx.y;  // sequence * heads + head
-  const int from = p.kept[pair * p.budget + to];
-  if (from < 0) return;
-  const uint8_t* src = p.kv4 + (pair * p.tiles + from / kKv4Tile) * kKv4TileBytes;
-  uint8_t* dst = p.dst + (pair * p.dst_tiles + to / kKv4Tile) * kKv4TileBytes;
-  const int ft = from % kKv4Tile, tt = to % kKv4Tile;
+  const int32_t* kept = p.kept + pair * p.budget;
+  const uint8_t* src = p.kv4 + pair * p.tiles * kKv4TileBytes;
+  uint8_t* dst = p.dst + pair * p.dst_tiles * kKv4TileBytes;
+  int from[kKv4MoveTokens];
+  uint32_t word[kKv4MoveTokens][2], par[kKv4MoveTokens];
+  float weight[kKv4MoveTokens];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    *reinterpret_cast<uint32_t*>(dst + s * kKv4Half + kv4_word_off(tt, lane, s == 1)) =
-        *reinterpret_cast<const uint32_t*>(src + s * kKv4Half + kv4_word_off(ft, lane, s == 1));
-    if (lane < 2)
-      *reinterpret_cast<uint32_t*>(dst + s * kKv4Half + kKv4Params + tt * 8 + lane * 4) =
-          *reinterpret_cast<const uint32_t*>(src + s * kKv4Half + kKv4Params + ft * 8 + lane * 4);
+  for (int i = 0; i < kKv4MoveTokens; ++i) {
+    const int to = to0 + i * (kKv4MoveThreads / 16);
+    from[i] = to < p.budget ? kept[to] : -1;
   }
-  if (lane == 0) p.dst_acc[pair * p.dst_tiles * kKv4Tile + to] = p.acc[pair * p.tiles * kKv4Tile + from];
+#pragma unroll
+  for (int i = 0; i < kKv4MoveTokens; ++i) {
+    if (from[i] < 0) continue;
+    const uint8_t* t = src + (int64_t)(from[i] / kKv4Tile) * kKv4TileBytes;
+    const int ft = from[i] % kKv4Tile;
+    word[i][0] = __ldg(reinterpret_cast<const uint32_t*>(t + kv4_word_off(ft, lane, false)));
+    word[i][1] = __ldg(reinterpret_cast<const uint32_t*>(t + kKv4Half + kv4_word_off(ft, lane, true)));
+    // lanes 0, 1: the keys' parameters; 2, 3: the values'
+    if (lane < 4)
+      par[i] = __ldg(reinterpret_cast<const uint32_t*>(t + (lane >> 1) * kKv4Half + kKv4Params + ft * 8 + (lane & 1) * 4));
+    if (lane == 4) weight[i] = __ldg(p.acc + pair * p.tiles * kKv4Tile + from[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kKv4MoveTokens; ++i) {
+    if (from[i] < 0) continue;
+    const int to = to0 + i * (kKv4MoveThreads / 16);
+    uint8_t* t = dst + (int64_t)(to / kKv4Tile) * kKv4TileBytes;
+    const int tt = to % kKv4Tile;
+    *reinterpret_cast<uint32_t*>(t + kv4_word_off(tt, lane, false)) = word[i][0];
+    *reinterpret_cast<uint32_t*>(t + kKv4Half + kv4_word_off(tt, lane, true)) = word[i][1];
+    if (lane < 4)
+      *reinterpret_cast<uint32_t*>(t + (lane >> 1) * kKv4Half + kKv4Params + tt * 8 + (lane & 1) * 4) = par[i];
+    if (lane == 4) p.dst_acc[pair * p.dst_tiles * kKv4Tile + to] = weight[i];
+  }
 }
 
 }  // namespace moba

@@ -130,10 +130,6 @@ __device__ __forceinline__ bool kv4_after(double s, int j, double ps, int pj) {
   return pj < 0 || s < ps || (s == ps && j > pj);
 }
 
-__device__ __forceinline__ void kv4_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // One cluster per unit (looping over units): its CTAs score the past blocks
 // for all rows of the unit, the first CTA selects and lists. Scores are sums
 // in fp64 of products that are exact there (bf16 times fp32), so near ties
@@ -397,6 +393,11 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   return y;
 }
 
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -416,7 +417,7 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
 // bound by instructions.) t is a 64th of the scale, so that t (64 + z) stays
 // below fp16's largest number; t is a multiple of 2^-23, so all stays exact.
 struct Kv4Par {
-  uint32_t t, tz;  // t and -t (64 + z), of two tokens (or of one, twice)
+  uint32_t t, tz, z;  // t, -t (64 + z) and 1024 + z, of two tokens (or of one, twice)
 };
 // (a & mask) | top in one instruction.
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t top) {
@@ -428,14 +429,16 @@ __device__ __forceinline__ Kv4Par kv4_par(uint32_t pp) {
   Kv4Par r;
   r.t = h2_mul(pp & 0x7F807F80u, 0x24002400u);  // 2^-6
   r.tz = h2_mul(and_or(pp << 4, 0x00F000F0u, 0xD400D400u), r.t);
+  r.z = and_or(pp, 0x000F000Fu, 0x64006400u);
   return r;
 }
 // t (c - z) for nibbles 0..3 of both halves of a word.
 __device__ __forceinline__ void kv4_pairs(uint32_t w, const Kv4Par& p, uint32_t (&x)[4]) {
-  x[0] = h2_fma(and_or(w << 4, 0x00F000F0u, 0x54005400u), p.t, p.tz);
+  const uint32_t h = w >> 8;
+  x[0] = h2_mul(h2_sub(and_or(w, 0x000F000Fu, 0x64006400u), p.z), p.t);
   x[1] = h2_fma(and_or(w, 0x00F000F0u, 0x54005400u), p.t, p.tz);
-  x[2] = h2_fma(and_or(w >> 4, 0x00F000F0u, 0x54005400u), p.t, p.tz);
-  x[3] = h2_fma(and_or(w >> 8, 0x00F000F0u, 0x54005400u), p.t, p.tz);
+  x[2] = h2_mul(h2_sub(and_or(h, 0x000F000Fu, 0x64006400u), p.z), p.t);
+  x[3] = h2_fma(and_or(h, 0x00F000F0u, 0x54005400u), p.t, p.tz);
 }
 
 // A query row enters the products as fp16: times the power of two that brings
@@ -957,9 +960,12 @@ __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams
 constexpr int kKv4WeightThreads = 128;
 
 // acc[key] += sum over the rows of the kv head of 2^(score - lse): one warp per
-// 64-token tile, whose keys it widens once and holds in registers; all rows of
-// the sequence pass by, eight at a time, in order.
-__global__ void __launch_bounds__(kKv4WeightThreads, 2) kv4_weight_kernel(Kv4AttnParams p) {
+// 64-token tile; all rows of the sequence pass by, eight at a time, in order.
+// HOLD: the keys are widened once and held in registers (many rows, two CTAs
+// of four warps per SM), else widened for each eight rows (few rows: there is
+// one pass, and what counts is how many warps have loads under way).
+template <bool HOLD>
+__global__ void __launch_bounds__(kKv4WeightThreads, HOLD ? 2 : 5) kv4_weight_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
   const int lane = threadIdx.x & 31, r = lane >> 2, qd = lane & 3;
   const int64_t tile = (int64_t)blockIdx.x * (kKv4WeightThreads / 32) + (threadIdx.x >> 5);
@@ -968,43 +974,54 @@ __global__ void __launch_bounds__(kKv4WeightThreads, 2) kv4_weight_kernel(Kv4Att
   const int n = kv4_queries(p, p.cu, b, &t0);
   const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
   const int key0 = (int)(tile * kKv4Tile), pos0 = len - n, rows = n * p.G;
-  if (n == 0 || key0 >= len || tile >= p.tiles) return;
+  if (n == 0 || tile >= p.tiles || key0 >= len) return;
   const int64_t slot0 = kv4_first_slot(p, b, t0);
   const int block = key0 / p.B;
-  const uint8_t* kt = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, b, h, tile);
-  uint32_t a[4][4][8];  // [16 keys][word][pair of the first, of the second eight keys]
-  bool loaded = false;
-  float sum[4][2] = {};
   // rows before the first key's position attend nothing here
-  int r0 = key0 > pos0 ? (key0 - pos0) * p.G / 8 * 8 : 0;
-  for (; r0 < rows; r0 += 8) {
-    uint32_t picked = 0xFFu;
-    if (p.kmean) {
-      const int64_t ui = (slot0 + r0 / p.R) * p.Hkv + h;
-      picked = p.chosen[ui * p.blocks + block] >> (r0 % p.R) & 0xFFu;
-      if (!picked) continue;
-    }
-    if (!loaded) {
-      loaded = true;
+  int r0 = key0 > pos0 ? (int)((int64_t)(key0 - pos0) * p.G / 8 * 8) : 0;
+  auto picked = [&](int row) {
+    if (!p.kmean) return 0xFFu;
+    const int64_t ui = (slot0 + row / p.R) * p.Hkv + h;
+    return __ldg(p.chosen + ui * p.blocks + block) >> (row % p.R) & 0xFFu;
+  };
+  while (r0 < rows && !picked(r0)) r0 += 8;
+  if (r0 >= rows) return;
+  const uint8_t* kt = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, b, h, tile);
+  float* acc = p.acc + ((int64_t)b * p.Hkv + h) * p.tiles * kKv4Tile + key0;
+  uint4 wa[4], wb[4];
+  uint32_t pa[4], pb[4];
+  float old[4][2];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int ta = g * 16 + r, tb = ta + 8;
-        const uint4 wa = __ldg(reinterpret_cast<const uint4*>(kt + ta * kKv4Row + qd * 16));
-        const uint4 wb = __ldg(reinterpret_cast<const uint4*>(kt + tb * kKv4Row + qd * 16));
-        const uint32_t pa = __ldg(reinterpret_cast<const uint16_t*>(kt + kKv4Params + ta * 8 + qd * 2));
-        const uint32_t pb = __ldg(reinterpret_cast<const uint16_t*>(kt + kKv4Params + tb * 8 + qd * 2));
-        const Kv4Par fa = kv4_par(__byte_perm(pa, 0, 0x1010)), fb = kv4_par(__byte_perm(pb, 0, 0x1010));
-        const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xb[4] = {wb.x, wb.y, wb.z, wb.w};
+  for (int g = 0; g < 4; ++g) {
+    const int ta = g * 16 + r, tb = ta + 8;
+    wa[g] = __ldg(reinterpret_cast<const uint4*>(kt + ta * kKv4Row + qd * 16));
+    wb[g] = __ldg(reinterpret_cast<const uint4*>(kt + tb * kKv4Row + qd * 16));
+    pa[g] = __ldg(reinterpret_cast<const uint16_t*>(kt + kKv4Params + ta * 8 + qd * 2));
+    pb[g] = __ldg(reinterpret_cast<const uint16_t*>(kt + kKv4Params + tb * 8 + qd * 2));
+    old[g][0] = acc[ta];
+    old[g][1] = acc[tb];
+  }
+  auto widen = [&](int g, int w, uint32_t (&y)[4], uint32_t (&z)[4]) {
+    const uint32_t xa[4] = {wa[g].x, wa[g].y, wa[g].z, wa[g].w}, xb[4] = {wb[g].x, wb[g].y, wb[g].z, wb[g].w};
+    kv4_pairs(xa[w], kv4_par(__byte_perm(pa[g], 0, 0x1010)), y);
+    kv4_pairs(xb[w], kv4_par(__byte_perm(pb[g], 0, 0x1010)), z);
+  };
+  uint32_t a[HOLD ? 4 : 1][4][8];  // [16 keys][word][pair of the first, of the second eight keys]
+  if constexpr (HOLD) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t y[4], z[4];
-          kv4_pairs(xa[w], fa, y);
-          kv4_pairs(xb[w], fb, z);
+    for (int g = 0; g < 4; ++g)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) a[g][w][2 * j] = y[j], a[g][w][2 * j + 1] = z[j];
-        }
+      for (int w = 0; w < 4; ++w) {
+        uint32_t y[4], z[4];
+        widen(g, w, y, z);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[g][w][2 * j] = y[j], a[g][w][2 * j + 1] = z[j];
       }
-    }
+  }
+  float sum[4][2] = {};
+  for (; r0 < rows; r0 += 8) {
+    const uint32_t pick = picked(r0);
+    if (!pick) continue;
     uint32_t qf[16];
     const int rr = r0 + r;
     const __nv_bfloat16* row =
@@ -1017,17 +1034,25 @@ __global__ void __launch_bounds__(kKv4WeightThreads, 2) kv4_weight_kernel(Kv4Att
     for (int x = 0; x < 2; ++x) {
       qs[x] = __shfl_sync(0xFFFFFFFFu, s, (2 * qd + x) * 4);
       const int row2 = r0 + 2 * qd + x;
-      const bool on = row2 < rows && (picked >> (2 * qd + x) & 1u);
+      const bool on = row2 < rows && (pick >> (2 * qd + x) & 1u);
       last[x] = on ? pos0 + row2 / p.G : -1;
       le[x] = on ? p.lse[(int64_t)(h * p.G + row2 % p.G) * p.total + t0 + row2 / p.G] * 1.4426950408889634f : 0.f;
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      float sc[4] = {};
+      float sc[4];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        mma_f16(sc, a[g][w][0], a[g][w][1], a[g][w][2], a[g][w][3], qf[4 * w], qf[4 * w + 1]);
-        mma_f16(sc, a[g][w][4], a[g][w][5], a[g][w][6], a[g][w][7], qf[4 * w + 2], qf[4 * w + 3]);
+        uint32_t y[4], z[4];
+        if constexpr (HOLD) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = a[g][w][2 * j], z[j] = a[g][w][2 * j + 1];
+        } else {
+          widen(g, w, y, z);
+        }
+        if (w == 0) mma_f16_first(sc, y[0], z[0], y[1], z[1], qf[0], qf[1]);
+        else mma_f16(sc, y[0], z[0], y[1], z[1], qf[4 * w], qf[4 * w + 1]);
+        mma_f16(sc, y[2], z[2], y[3], z[3], qf[4 * w + 2], qf[4 * w + 3]);
       }
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -1037,8 +1062,6 @@ __global__ void __launch_bounds__(kKv4WeightThreads, 2) kv4_weight_kernel(Kv4Att
       }
     }
   }
-  if (!loaded) return;
-  float* acc = p.acc + ((int64_t)b * p.Hkv + h) * p.tiles * kKv4Tile + key0;
 #pragma unroll
   for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -1047,8 +1070,95 @@ __global__ void __launch_bounds__(kKv4WeightThreads, 2) kv4_weight_kernel(Kv4Att
       v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
       v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
       const int at = g * 16 + x * 8 + r;
-      if (qd == 0 && key0 + at < len) acc[at] += v;
+      if (qd == 0 && key0 + at < len) acc[at] = old[g][x] + v;
     }
+}
+
+// ------------------------------------------------------------------ pool
+
+struct Kv4PoolParams {
+  const uint8_t* kv4;
+  const int32_t* lengths;
+  int64_t tiles;
+  int heads, B, blocks;  // blocks = capacity / B
+  float* kmean;          // [batch][heads][blocks][128]
+};
+
+constexpr int kKv4PoolThreads = 256;
+
+// A cluster of CTAs per (block, head, sequence), a part of the block's tokens
+// each, 16 tokens of each warp at a time: the tensor core sums them in fp32
+// (keys as in the value product of the attention, against ones), the warps'
+// and CTAs' sums meet in a fixed order. Blocks that the sequence has not
+// completed are written as zero.
+__global__ void __launch_bounds__(kKv4PoolThreads) kv4_pool_kernel(Kv4PoolParams p) {
+  grid_dependency_sync();
+  constexpr int WARPS = kKv4PoolThreads / 32;
+  __shared__ float sums[WARPS][kHeadDim];
+  __shared__ uint32_t total[kHeadDim];  // fp32 bits
+  uint32_t rank, csize;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+  const int j = blockIdx.x / csize, h = blockIdx.y, b = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, qd = lane & 3;
+  const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
+  float* out = p.kmean + (((int64_t)b * p.heads + h) * p.blocks + j) * kHeadDim;
+  if ((int64_t)(j + 1) * p.B > len) {  // the whole cluster leaves
+    if (rank == 0 && threadIdx.x < kHeadDim) out[threadIdx.x] = 0.f;
+    return;
+  }
+  const uint8_t* kt = p.kv4 + kv4_tile_off(p.tiles, p.heads, b, h, 0);
+  const int groups = p.B / 16, g0 = (int)((int64_t)j * groups);
+  float o[8][4] = {};
+#pragma unroll 2
+  for (int g = rank * WARPS + warp; g < groups; g += csize * WARPS) {
+    const int64_t t = (int64_t)(g0 + g) * 16;
+    const uint8_t* tile = kt + t / kKv4Tile * kKv4TileBytes;
+    const int at = (int)(t % kKv4Tile) + 2 * qd;
+    uint2 w[2][2];
+    Kv4Par fp[2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      uint32_t pp[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int tok = at + 8 * f + e;
+        w[f][e] = __ldg(reinterpret_cast<const uint2*>(tile + tok * kKv4Row + r * 8));
+        pp[e] = __ldg(reinterpret_cast<const uint16_t*>(tile + kKv4Params + tok * 8 + (r >> 1) * 2));
+      }
+      fp[f] = kv4_par(__byte_perm(pp[0], pp[1], 0x5410));
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      uint32_t a[2][2][4];  // [channel parity][keys 0-7, 8-15][nibble]
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const uint32_t x0 = x ? w[f][0].y : w[f][0].x, x1 = x ? w[f][1].y : w[f][1].x;
+        kv4_pairs(__byte_perm(x0, x1, 0x5410), fp[f], a[0][f]);
+        kv4_pairs(__byte_perm(x0, x1, 0x7632), fp[f], a[1][f]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        mma_f16(o[x * 4 + i], a[0][0][i], a[1][0][i], a[0][1][i], a[1][1][i], 0x3C003C00u, 0x3C003C00u);
+    }
+  }
+  // every column holds the sums: channels 16 r + 2 mt and the next
+  if (qd == 0)
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) sums[warp][16 * r + 2 * mt] = o[mt][0], sums[warp][16 * r + 2 * mt + 1] = o[mt][2];
+  __syncthreads();
+  if (threadIdx.x < kHeadDim) {
+    float s = 0.f;
+    for (int w = 0; w < WARPS; ++w) s += sums[w][threadIdx.x];
+    total[threadIdx.x] = __float_as_uint(s);
+  }
+  kv4_cluster_sync();
+  if (rank == 0 && threadIdx.x < kHeadDim) {
+    float s = 0.f;
+    for (uint32_t c = 0; c < csize; ++c) s += __uint_as_float(kv4_remote_ld(&total[threadIdx.x], c));
+    out[threadIdx.x] = s * 64.f / (float)p.B;
+  }
+  kv4_cluster_sync();  // no CTA leaves while its sums may still be read
 }
 
 }  // namespace moba

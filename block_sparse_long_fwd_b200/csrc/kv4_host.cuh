@@ -33,6 +33,24 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// As launch_chained, with the grid in clusters of `csize` CTAs along x.
+template <typename... KArgs, typename... Args>
+void launch_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 block, int csize, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = csize;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <class C>
 constexpr size_t kv4_attn_smem() {
   return sizeof(typename C::Shared);
@@ -99,7 +117,8 @@ int moba_kv4_append(const void* k, const void* v, int64_t total, const int32_t* 
   p.heads = heads_kv;
   p.kv4 = static_cast<uint8_t*>(kv4);
   p.acc = acc;
-  const int64_t threads = total * heads_kv * 16;
+  const int64_t threads = total * heads_kv * 4;
+  if (threads / moba::kKv4AppendThreads >= INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
   launch_chained(moba::kv4_append_kernel,
                  dim3((unsigned)((threads + moba::kKv4AppendThreads - 1) / moba::kKv4AppendThreads)),
                  dim3(moba::kKv4AppendThreads), 0, stream, p);
@@ -132,7 +151,7 @@ int moba_kv4_load(const void* kv4, const int32_t* lengths, const int32_t* first,
   p.heads = heads_kv;
   p.k = static_cast<__nv_bfloat16*>(k);
   p.v = static_cast<__nv_bfloat16*>(v);
-  const int64_t ctas = (n * batch * heads_kv * 16 + moba::kKv4LoadThreads - 1) / moba::kKv4LoadThreads;
+  const int64_t per = moba::kKv4LoadThreads / 16 * moba::kKv4LoadRows, ctas = (n * batch * heads_kv + per - 1) / per;
   if (ctas > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
   launch_chained(moba::kv4_load_kernel, dim3((unsigned)ctas), dim3(moba::kKv4LoadThreads), 0, stream, p);
   MOBA_CUDA(cudaGetLastError());
@@ -161,7 +180,12 @@ int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch, int heads_
   p.blocks = (int)(capacity / block_size);
   p.kmean = kmean;
   if (p.blocks) {
-    launch_chained(moba::kv4_pool_kernel, dim3(p.blocks, heads_kv, batch), dim3(moba::kKv4PoolThreads), 0, stream, p);
+    // a CTA for every 512 tokens of a block, up to 8 of them
+    int csize = 1;
+    while (csize < 8 && block_size / csize > 512) csize *= 2;
+    if ((int64_t)p.blocks * csize > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many blocks");
+    launch_clusters(moba::kv4_pool_kernel, dim3(p.blocks * csize, heads_kv, batch), dim3(moba::kKv4PoolThreads), csize,
+                    stream, p);
     MOBA_CUDA(cudaGetLastError());
   }
   return finish_call(MOBA_OK, stream);
@@ -240,28 +264,17 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
     p.chosen = reinterpret_cast<uint32_t*>(ws + o_chosen);
     p.scores = reinterpret_cast<double*>(ws + o_scores);
     p.part = reinterpret_cast<float*>(ws + o_part);
-    if (kmean) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3((unsigned)(clusters * csize));
-      cfg.blockDim = dim3(moba::kKv4GateThreads);
-      cfg.stream = st;
-      cudaLaunchAttribute attr[2];
-      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr[0].val.programmaticStreamSerializationAllowed = 1;
-      attr[1].id = cudaLaunchAttributeClusterDimension;
-      attr[1].val.clusterDim.x = csize;
-      attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 2;
-      MOBA_CUDA(cudaLaunchKernelEx(&cfg, moba::kv4_gate_kernel, p));
-    }
+    if (kmean)
+      launch_clusters(moba::kv4_gate_kernel, dim3((unsigned)(clusters * csize)), dim3(moba::kKv4GateThreads), csize, st,
+                      p);
     if (few) launch_kv4_attn<moba::Kv4Few>(p, st);
     else launch_kv4_attn<moba::Kv4Many>(p, st);
     launch_chained(moba::kv4_join_kernel, dim3((unsigned)(nu * p.R)), dim3(moba::kKv4JoinThreads), 0, st, p);
     if (acc) {
       const int per = moba::kKv4WeightThreads / 32;
-      launch_chained(moba::kv4_weight_kernel, dim3((unsigned)((p.tiles + per - 1) / per), batch * heads_kv),
-                     dim3(moba::kKv4WeightThreads), 0, st, p);
+      launch_chained(few ? moba::kv4_weight_kernel<false> : moba::kv4_weight_kernel<true>,
+                     dim3((unsigned)((p.tiles + per - 1) / per), batch * heads_kv), dim3(moba::kKv4WeightThreads), 0,
+                     st, p);
     }
     MOBA_CUDA(cudaGetLastError());
     return MOBA_OK;
@@ -309,9 +322,12 @@ int moba_kv4_evict(const void* kv4, const float* acc, const int32_t* lengths, in
   p.dst_acc = dst_acc;
   p.kept = kept;
   p.new_lengths = new_lengths;
-  launch_chained(moba::kv4_select_kernel, dim3(heads_kv, batch), dim3(moba::kKv4SelectThreads), 0, stream, p);
-  launch_chained(moba::kv4_move_kernel,
-                 dim3((unsigned)((budget * 16 + moba::kKv4MoveThreads - 1) / moba::kKv4MoveThreads), (unsigned)pairs),
+  // up to 8 CTAs select for a kv head while there are SMs for them and 4096 weights for each
+  int csize = 1;
+  while (csize < 8 && (int64_t)pairs * csize * 2 <= 2 * dev.sms && capacity / csize > 4096) csize *= 2;
+  launch_clusters(moba::kv4_select_kernel, dim3((unsigned)pairs * csize), dim3(moba::kKv4SelectThreads), csize, stream, p);
+  const int64_t per = moba::kKv4MoveThreads / 16 * moba::kKv4MoveTokens;
+  launch_chained(moba::kv4_move_kernel, dim3((unsigned)((budget + per - 1) / per), (unsigned)pairs),
                  dim3(moba::kKv4MoveThreads), 0, stream, p);
   MOBA_CUDA(cudaGetLastError());
   return finish_call(MOBA_OK, stream);
