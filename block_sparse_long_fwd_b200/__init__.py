@@ -275,19 +275,28 @@ def kv4_cache(batch: int, heads_kv: int, capacity: int, device="cuda") -> torch.
 
 
 def _kv4(x: torch.Tensor, name: str = "kv4"):
-    if not (x.is_cuda and x.dtype == torch.uint8 and x.is_contiguous() and x.dim() == 4
-            and x.shape[3] == KV4_TILE_BYTES):
+    """(batch, heads_kv, capacity, device index) of a cache."""
+    if x.dim() != 4 or x.dtype != torch.uint8 or x.shape[3] != KV4_TILE_BYTES or not (x.is_cuda and x.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor [batch, heads_kv, tiles, {KV4_TILE_BYTES}]")
-    return x.shape[0], x.shape[1], x.shape[2] * KV4_TILE
+    return x.shape[0], x.shape[1], x.shape[2] * KV4_TILE, x.get_device()
 
 
-def _on(x, name: str, dtype, shape, device):
+def _on(x, name: str, dtype, shape, device: int):
     """Address of a contiguous tensor of this type, shape and device (None stays None)."""
     if x is None:
         return None
-    if x.dtype != dtype or tuple(x.shape) != tuple(shape) or x.device != device or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+    if x.dtype != dtype or x.shape != shape or x.get_device() != device or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{device}")
     return x.data_ptr()
+
+
+def _call(device: int, stream, fn, *args) -> None:
+    """fn(*args, stream) with `device` current (a switch only when another one is)."""
+    if torch.cuda.current_device() == device:
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream))
+        return
+    with torch.cuda.device(device):
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream))
 
 
 def kv4_append(k: torch.Tensor, v: torch.Tensor, kv4: torch.Tensor, start: torch.Tensor, cu=None, acc=None,
@@ -300,19 +309,16 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, kv4: torch.Tensor, start: torch
     ``start[b]`` (int32 [batch], on the GPU). ``acc`` (fp32 [batch, Hkv,
     capacity]) is set to zero there.
     """
-    batch, hkv, cap = _kv4(kv4)
-    dev = kv4.device
-    _dev_bf16(k, "k"), _dev_bf16(v, "v")
+    batch, hkv, cap, dev = _kv4(kv4)
     T = k.shape[0]
-    kp, vp = (_on(x, n, torch.bfloat16, (T, hkv, HEAD_DIM), dev) for x, n in ((k, "k"), (v, "v")))
+    kp = _on(k, "k", torch.bfloat16, (T, hkv, HEAD_DIM), dev)
+    vp = _on(v, "v", torch.bfloat16, (T, hkv, HEAD_DIM), dev)
     cp = _on(cu, "cu", torch.int32, (batch + 1,), dev)
     sp = _on(start, "start", torch.int32, (batch,), dev)
     ap = _on(acc, "acc", torch.float32, (batch, hkv, cap), dev)
     if T == 0:
         return
-    with torch.cuda.device(dev):
-        _check(lib().moba_kv4_append(kp, vp, T, cp, sp, batch, hkv, HEAD_DIM, cap, kv4.data_ptr(), ap,
-                                     _stream(stream)))
+    _call(dev, stream, lib().moba_kv4_append, kp, vp, T, cp, sp, batch, hkv, HEAD_DIM, cap, kv4.data_ptr(), ap)
 
 
 def kv4_load(kv4: torch.Tensor, lengths: torch.Tensor, n: int, first=None, stream=None):
@@ -320,18 +326,16 @@ def kv4_load(kv4: torch.Tensor, lengths: torch.Tensor, n: int, first=None, strea
     [batch] on the GPU; None: from token 0) as bf16: (k, v), each
     [batch, n, Hkv, 128], exact, zero from ``lengths[b]`` on.
     """
-    batch, hkv, cap = _kv4(kv4)
-    dev = kv4.device
+    batch, hkv, cap, dev = _kv4(kv4)
     lp = _on(lengths, "lengths", torch.int32, (batch,), dev)
     fp = _on(first, "first", torch.int32, (batch,), dev)
     if not 0 <= n <= cap:
         raise ValueError("n must be in [0, capacity]")
-    k, v = (torch.empty((batch, n, hkv, HEAD_DIM), dtype=torch.bfloat16, device=dev) for _ in "kv")
-    if n == 0:
-        return k, v
-    with torch.cuda.device(dev):
-        _check(lib().moba_kv4_load(kv4.data_ptr(), lp, fp, batch, hkv, HEAD_DIM, cap, n, k.data_ptr(), v.data_ptr(),
-                                   _stream(stream)))
+    k = torch.empty((batch, n, hkv, HEAD_DIM), dtype=torch.bfloat16, device=kv4.device)
+    v = torch.empty_like(k)
+    if n:
+        _call(dev, stream, lib().moba_kv4_load, kv4.data_ptr(), lp, fp, batch, hkv, HEAD_DIM, cap, n, k.data_ptr(),
+              v.data_ptr())
     return k, v
 
 
@@ -339,18 +343,16 @@ def kv4_pool(kv4: torch.Tensor, lengths: torch.Tensor, block_size: int, kmean=No
     """Mean keys of a 4-bit cache's complete blocks: fp32
     [batch, Hkv, capacity // block_size, 128], zero for the other blocks.
     """
-    batch, hkv, cap = _kv4(kv4)
-    dev = kv4.device
+    batch, hkv, cap, dev = _kv4(kv4)
     lp = _on(lengths, "lengths", torch.int32, (batch,), dev)
     if block_size < 1:
         raise ValueError("block_size must be positive")
     shape = (batch, hkv, cap // block_size, HEAD_DIM)
     if kmean is None:
-        kmean = torch.empty(shape, dtype=torch.float32, device=dev)
+        kmean = torch.empty(shape, dtype=torch.float32, device=kv4.device)
     mp = _on(kmean, "kmean", torch.float32, shape, dev)
     if shape[2]:
-        with torch.cuda.device(dev):
-            _check(lib().moba_kv4_pool(kv4.data_ptr(), lp, batch, hkv, HEAD_DIM, cap, block_size, mp, _stream(stream)))
+        _call(dev, stream, lib().moba_kv4_pool, kv4.data_ptr(), lp, batch, hkv, HEAD_DIM, cap, block_size, mp)
     return kmean
 
 
@@ -366,12 +368,10 @@ def kv4_attend(q: torch.Tensor, kv4: torch.Tensor, lengths: torch.Tensor, cu=Non
     ``acc`` (fp32 [batch, Hkv, capacity]) grows by the tokens' attention
     weights. Returns (out [T, Hq, 128] bf16, lse [Hq, T] fp32).
     """
-    batch, hkv, cap = _kv4(kv4)
-    dev = kv4.device
-    _dev_bf16(q, "q")
+    batch, hkv, cap, dev = _kv4(kv4)
     if q.dim() != 3:
         raise ValueError("q must be [T, heads_q, head_dim]")
-    T, hq, d = q.shape
+    T, hq, _ = q.shape
     qp = _on(q, "q", torch.bfloat16, (T, hq, HEAD_DIM), dev)
     cp = _on(cu, "cu", torch.int32, (batch + 1,), dev)
     lp = _on(lengths, "lengths", torch.int32, (batch,), dev)
@@ -385,14 +385,12 @@ def kv4_attend(q: torch.Tensor, kv4: torch.Tensor, lengths: torch.Tensor, cu=Non
     elif block_size or topk:
         raise ValueError("block_size and topk need kmean")
     out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((hq, T), dtype=torch.float32, device=dev) if lse is None else lse
+    lse = torch.empty((hq, T), dtype=torch.float32, device=kv4.device) if lse is None else lse
     op = _on(out, "out", torch.bfloat16, (T, hq, HEAD_DIM), dev)
     ep = _on(lse, "lse", torch.float32, (hq, T), dev)
-    if T == 0:
-        return out, lse
-    with torch.cuda.device(dev):
-        _check(lib().moba_kv4_attend(qp, T, cp, kv4.data_ptr(), lp, mp, batch, hq, hkv, HEAD_DIM, cap, block_size,
-                                     topk, ap, op, ep, _stream(stream)))
+    if T:
+        _call(dev, stream, lib().moba_kv4_attend, qp, T, cp, kv4.data_ptr(), lp, mp, batch, hq, hkv, HEAD_DIM, cap,
+              block_size, topk, ap, op, ep)
     return out, lse
 
 
@@ -406,10 +404,9 @@ def kv4_evict(kv4: torch.Tensor, acc: torch.Tensor, lengths: torch.Tensor, budge
     Returns (lengths int32 [batch] of the new cache, kept int32
     [batch, Hkv, budget]: the old index of every kept token, padded with -1).
     """
-    batch, hkv, cap = _kv4(kv4)
-    dev = kv4.device
-    db, dh, dcap = _kv4(dst, "dst")
-    if (db, dh) != (batch, hkv) or dst.device != dev:
+    batch, hkv, cap, dev = _kv4(kv4)
+    db, dh, dcap, ddev = _kv4(dst, "dst")
+    if (db, dh, ddev) != (batch, hkv, dev):
         raise ValueError("dst must be a cache of the same sequences and heads on the same device")
     if acc is None or dst_acc is None:
         raise ValueError("acc and dst_acc are required")
@@ -419,10 +416,9 @@ def kv4_evict(kv4: torch.Tensor, acc: torch.Tensor, lengths: torch.Tensor, budge
     if not 1 <= budget <= dcap or not 0 <= recent <= budget:
         raise ValueError("budget must be in [1, dst's capacity] and recent in [0, budget]")
     new = torch.empty_like(lengths)
-    kept = torch.empty((batch, hkv, budget), dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().moba_kv4_evict(kv4.data_ptr(), ap, lp, batch, hkv, HEAD_DIM, cap, budget, recent, dst.data_ptr(),
-                                    dp, dcap, kept.data_ptr(), new.data_ptr(), _stream(stream)))
+    kept = torch.empty((batch, hkv, budget), dtype=torch.int32, device=kv4.device)
+    _call(dev, stream, lib().moba_kv4_evict, kv4.data_ptr(), ap, lp, batch, hkv, HEAD_DIM, cap, budget, recent,
+          dst.data_ptr(), dp, dcap, kept.data_ptr(), new.data_ptr())
     return new, kept
 
 
