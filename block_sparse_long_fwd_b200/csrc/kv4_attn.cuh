@@ -44,12 +44,16 @@ struct Kv4AttnParams {
   float* lse;                   // [Hq][total]
   // scratch
   Kv4Unit* units;               // [slots * Hkv]
-  int64_t* before;              // [slots * Hkv + 1]: half tiles of the units before
+  int64_t* before;              // [slots * Hkv + 1]: items of the units before
   uint2* list;                  // [slots * Hkv][list_cap]: (block, rows that chose it), ascending
   uint32_t* chosen;             // [slots * Hkv][blocks]: rows of the unit that chose the block
   double* scores;               // [clusters][R][means]
   float* part;                  // [2 * ctas][R * 130]: O, then m and l
-  int list_cap, ctas, warps;    // warps of a CTA
+  int list_cap, ctas;
+  int parts;                    // ranges of a CTA
+  int steps;                    // ranges are dealt out in steps of 128 keys (else in half tiles)
+  uint8_t* qtiles;              // [slots * Hkv][2][32768]: query tiles as fp16 operands
+  float* qscale;                // [slots * Hkv][256]: their rows' scales
 };
 
 // Queries of sequence b: packed index of the first and their number. Offsets
@@ -105,6 +109,11 @@ __device__ __forceinline__ Kv4Unit kv4_unit_of(const Kv4AttnParams& p, const int
 // Position of the unit's last row: the last key that any of its rows attends.
 __device__ __forceinline__ int kv4_last_pos(const Kv4AttnParams& p, const Kv4Unit& u) {
   return u.pos0 + (u.row0 + u.rows - 1) / p.G;
+}
+
+// What is dealt out of a unit: half tiles, or steps of two tiles.
+__device__ __forceinline__ int kv4_items(const Kv4AttnParams& p, const Kv4Unit& u) {
+  return p.steps ? (u.tiles + 1) / 2 : 2 * u.tiles;
 }
 
 // ------------------------------------------------------------------ gate
@@ -259,29 +268,29 @@ __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams
 
 // ------------------------------------------------------------------ plan
 
-// CTAs that get a range of `all` half tiles: as many as leave no warp idle.
+// CTAs that get a range of `all` items: as many as leave no part of one idle.
 __device__ __forceinline__ int kv4_ctas(const Kv4AttnParams& p, int64_t all) {
-  return (int)min((int64_t)p.ctas, (all + p.warps - 1) / p.warps);
+  return (int)min((int64_t)p.ctas, (all + p.parts - 1) / p.parts);
 }
 
-// Where each warp's range begins: every CTA scans all units' tiles for itself
+// Where each part's range begins (a part is a warp, or the CTA): every CTA scans all units' tiles for itself
 // (they follow from the lengths alone, or the gate has left them), which is
 // a round trip to L2 where a kernel of its own was 6 to 9 us with its launch.
-// The units that the CTA's range touches, and the half tiles before them, are
+// The units that the CTA's range touches, and the items before them, are
 // left in scratch for the rest of the CTA and for the join (units of several
 // CTAs get the same values from each); CTA 0 leaves those without tiles.
 // `copy`: shared memory for the offsets and lengths, `room` words.
 struct Kv4Range {
-  int n;          // half tiles of this warp
-  int unit, off;  // its first unit, half tiles of it that lie before the range
+  int n;          // items of this part
+  int unit, off;  // its first unit, items of it that lie before the range
   bool any;       // the CTA has some
 };
 
-template <int WARPS>
+template <int THREADS, int PARTS>
 __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* copy, int room) {
-  constexpr int THREADS = 32 * WARPS;
-  __shared__ int64_t warp_sums[WARPS], bound[WARPS + 1];
-  __shared__ int2 s_start[WARPS];
+  constexpr int WARPS = THREADS / 32;
+  __shared__ int64_t warp_sums[WARPS], bound[PARTS + 1];
+  __shared__ int2 s_start[PARTS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
   const int nu = p.slots * p.Hkv;
   const int32_t *cu = p.cu, *lengths = p.lengths;
@@ -323,32 +332,32 @@ __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* co
     return sum;
   };
   Kv4Unit u = unit(tid);
-  int64_t before, all = scan(2 * u.tiles, &before);
+  int64_t before, all = scan(kv4_items(p, u), &before);
   const bool once = nu <= THREADS;
   for (int u0 = THREADS; u0 < nu; u0 += THREADS) {
     int64_t unused;
-    all += scan(2 * unit(u0 + tid).tiles, &unused);
+    all += scan(kv4_items(p, unit(u0 + tid)), &unused);
   }
   const int ctas = kv4_ctas(p, all);
-  if (tid <= WARPS) bound[tid] = cta < ctas ? all * (cta * WARPS + tid) / (ctas * WARPS) : all;  // start of warp tid
+  if (tid <= PARTS) bound[tid] = cta < ctas ? all * (cta * PARTS + tid) / (ctas * PARTS) : all;  // start of part tid
   __syncthreads();
-  const int64_t lo = bound[0], hi = bound[WARPS];
+  const int64_t lo = bound[0], hi = bound[PARTS];
   if (cta == 0 && tid == 0) p.before[nu] = all;
   int64_t done = 0;
   for (int u0 = 0; u0 < nu; u0 += THREADS) {
     const int ui = u0 + tid;
     if (!once) {
       u = unit(ui);
-      const int64_t sum = scan(2 * u.tiles, &before);
+      const int64_t sum = scan(kv4_items(p, u), &before);
       before += done;
       done += sum;
     }
     if (ui < nu) {
-      const int64_t end = before + 2 * u.tiles;
+      const int64_t end = before + kv4_items(p, u);
       const bool mine = u.tiles > 0 && before < hi && end > lo;
       if (mine) {
         p.before[ui] = before;
-        for (int w = 0; w < WARPS; ++w) {
+        for (int w = 0; w < PARTS; ++w) {
           const int64_t x = bound[w];
           if (x >= before && x < end) s_start[w] = make_int2(ui, (int)(x - before));
         }
@@ -359,9 +368,10 @@ __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* co
   __syncthreads();
   Kv4Range g;
   g.any = hi > lo;
-  g.n = (int)(bound[warp + 1] - bound[warp]);
-  g.unit = g.n ? s_start[warp].x : 0;
-  g.off = g.n ? s_start[warp].y : 0;
+  const int part = PARTS == 1 ? 0 : warp;
+  g.n = (int)(bound[part + 1] - bound[part]);
+  g.unit = g.n ? s_start[part].x : 0;
+  g.off = g.n ? s_start[part].y : 0;
   return g;
 }
 
@@ -441,6 +451,18 @@ __device__ __forceinline__ void kv4_pairs(uint32_t w, const Kv4Par& p, uint32_t 
   x[3] = h2_fma(and_or(h, 0x00F000F0u, 0x54005400u), p.t, p.tz);
 }
 
+// The factors that bring a row with the largest magnitude `top` (bf16 bits) to
+// fp16, and the one that turns its products into log2 scores.
+__device__ __forceinline__ float kv4_query_scale(uint32_t top, float scale_log2, float& f1, float& f2) {
+  const int e = (int)(top >> 7);  // biased exponent; 0: zero or subnormal, 255: not finite
+  // 2^k with e - 127 + k = 14, in two factors that are normal numbers
+  const int k = (e == 0 || e == 255) ? 0 : 141 - e;
+  const int k1 = k / 2, k2 = k - k1;
+  f1 = __int_as_float((127 + k1) << 23);
+  f2 = __int_as_float((127 + k2) << 23);
+  return 64.f * scale_log2 * __int_as_float((127 - k1) << 23) * __int_as_float((127 - k2) << 23);
+}
+
 // A query row enters the products as fp16: times the power of two that brings
 // its largest channel to [2^14, 2^15). bf16's eight bits then stay exact but
 // for channels 2^28 times smaller than the largest, whose error is 2^-40 of it.
@@ -458,15 +480,12 @@ __device__ __forceinline__ float kv4_query_fragment(const __nv_bfloat16* row, fl
   for (int i = 0; i < 16; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
   top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
   top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-  const int e = (int)(top >> 7);  // biased exponent; 0: zero or subnormal, 255: not finite
-  // 2^k with e - 127 + k = 14, in two factors that are normal numbers
-  const int k = (e == 0 || e == 255) ? 0 : 141 - e;
-  const int k1 = k / 2, k2 = k - k1;
-  const float f1 = __int_as_float((127 + k1) << 23), f2 = __int_as_float((127 + k2) << 23);
+  float f1, f2;
+  const float scale = kv4_query_scale(top, scale_log2, f1, f2);
 #pragma unroll
   for (int i = 0; i < 16; ++i)
     f[i] = pack_half2(__uint_as_float(w[i] << 16) * f1 * f2, __uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2);
-  return 64.f * scale_log2 * __int_as_float((127 - k1) << 23) * __int_as_float((127 - k2) << 23);
+  return scale;
 }
 
 // Token (of 16) that row r of the score product holds: neighbours, swapped
@@ -537,7 +556,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
     fence_barrier_init();
   }
   if (threadIdx.x < 2 * C::WARPS) sh->unit[threadIdx.x] = -1;
-  const Kv4Range range = kv4_plan<C::WARPS>(p, reinterpret_cast<int32_t*>(&sh->piece), sizeof(sh->piece) / 4);
+  const Kv4Range range = kv4_plan<C::THREADS, C::WARPS>(p, reinterpret_cast<int32_t*>(&sh->piece), sizeof(sh->piece) / 4);
   if (!range.any) return;
   const int n = range.n;
 
@@ -893,7 +912,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
 
 constexpr int kKv4JoinThreads = 128;
 
-// The CTA whose range holds half tile x of `all`: the last one that begins at
+// The CTA whose range holds item x of `all`: the last one that begins at
 // or before it.
 __device__ __forceinline__ int kv4_cta_of(int64_t x, int64_t all, int ctas) {
   return (int)(((x + 1) * ctas + all - 1) / all) - 1;
@@ -917,7 +936,7 @@ __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams
     const int64_t all = p.before[p.slots * p.Hkv], x = p.before[ui];
     const int ctas = kv4_ctas(p, all);
     c0 = kv4_cta_of(x, all, ctas);
-    c1 = kv4_cta_of(x + 2 * u.tiles - 1, all, ctas);
+    c1 = kv4_cta_of(x + kv4_items(p, u) - 1, all, ctas);
     if (c0 == c1) return;  // written by the CTA itself
   }
   const int64_t per = p.R * 130;

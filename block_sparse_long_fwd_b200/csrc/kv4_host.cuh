@@ -5,6 +5,7 @@
 
 #include "kv4.cuh"
 #include "kv4_attn.cuh"
+#include "kv4_chunk.cuh"
 
 namespace {
 
@@ -67,6 +68,13 @@ cudaError_t set_kv4_attn_smem() {
                               (int)kv4_attn_smem<C>());
 }
 
+// Rows of a sequence and kv head, on average, above which the tcgen05 kernel
+// takes over.
+int64_t kv4_chunk_rows() {
+  const char* e = getenv("KV4_CHUNK_ROWS");
+  return e ? atoll(e) : 64;
+}
+
 bool g_kv4_ready[64] = {};
 
 // The device, and an error that an earlier call's kernels left behind.
@@ -80,6 +88,10 @@ int kv4_begin(DeviceInfo* dev, cudaStream_t st) {
     if (!g_kv4_ready[d]) {
       MOBA_CUDA(set_kv4_attn_smem<moba::Kv4Few>());
       MOBA_CUDA(set_kv4_attn_smem<moba::Kv4Many>());
+      MOBA_CUDA(cudaFuncSetAttribute(moba::kv4_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     moba::kKv4ChunkSmemBytes));
+      MOBA_CUDA(cudaFuncSetAttribute(moba::kv4_chunk_weight_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     moba::kKv4ColSmemBytes));
       g_kv4_ready[d] = true;
     }
   }
@@ -239,12 +251,14 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   p.means = kmean ? (int)(capacity / block_size) : 0;
   p.blocks = kmean ? (int)((capacity + block_size - 1) / block_size) : 0;
   const bool few = total * p.G <= (int64_t)moba::Kv4Few::R * batch;
-  p.R = few ? moba::Kv4Few::R : moba::Kv4Many::R;
+  const bool chunk = !kmean && total * p.G > kv4_chunk_rows() * batch;
+  p.R = few ? moba::Kv4Few::R : chunk ? moba::kKv4ChunkRows : moba::Kv4Many::R;
   const int64_t slots = total * p.G / p.R + batch;
   if (slots * heads_kv * p.R > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
   p.slots = (int)slots;
   p.ctas = dev.sms;
-  p.warps = few ? moba::Kv4Few::WARPS : moba::Kv4Many::WARPS;
+  p.parts = few ? moba::Kv4Few::WARPS : chunk ? 1 : moba::Kv4Many::WARPS;
+  p.steps = chunk ? 1 : 0;
   const int64_t nu = slots * heads_kv;
   p.list_cap = kmean ? (int)std::min<int64_t>(p.blocks, (int64_t)p.R * topk) : 0;
   // the gate: up to 8 CTAs share a unit's scores while there are few units
@@ -257,7 +271,11 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   const size_t o_chosen = c.take((size_t)nu * p.blocks * 4);
   const size_t o_scores = c.take((size_t)clusters * p.R * p.means * 8);
   const size_t o_part = c.take((size_t)2 * p.ctas * p.R * 130 * 4);
+  const size_t o_qtiles = c.take(chunk ? (size_t)nu * 2 * moba::kKv4TileOp : 0);
+  const size_t o_qscale = c.take(chunk ? (size_t)nu * moba::kKv4ChunkRows * 4 : 0);
   const Runner run = [&](uint8_t* ws, cudaStream_t st) -> int {
+    p.qtiles = ws + o_qtiles;
+    p.qscale = reinterpret_cast<float*>(ws + o_qscale);
     p.units = reinterpret_cast<moba::Kv4Unit*>(ws + o_units);
     p.before = reinterpret_cast<int64_t*>(ws + o_before);
     p.list = reinterpret_cast<uint2*>(ws + o_list);
@@ -267,10 +285,21 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
     if (kmean)
       launch_clusters(moba::kv4_gate_kernel, dim3((unsigned)(clusters * csize)), dim3(moba::kKv4GateThreads), csize, st,
                       p);
-    if (few) launch_kv4_attn<moba::Kv4Few>(p, st);
-    else launch_kv4_attn<moba::Kv4Many>(p, st);
+    if (few) {
+      launch_kv4_attn<moba::Kv4Few>(p, st);
+    } else if (chunk) {
+      launch_chained(moba::kv4_prep_kernel, dim3((unsigned)nu, moba::kKv4ChunkRows * 16 / moba::kKv4PrepThreads),
+                     dim3(moba::kKv4PrepThreads), 0, st, p);
+      launch_chained(moba::kv4_chunk_kernel, dim3(p.ctas), dim3(moba::kKv4ChunkThreads), moba::kKv4ChunkSmemBytes, st,
+                     p);
+    } else {
+      launch_kv4_attn<moba::Kv4Many>(p, st);
+    }
     launch_chained(moba::kv4_join_kernel, dim3((unsigned)(nu * p.R)), dim3(moba::kKv4JoinThreads), 0, st, p);
-    if (acc) {
+    if (acc && chunk) {
+      launch_chained(moba::kv4_chunk_weight_kernel, dim3((unsigned)((capacity + 255) / 256), batch * heads_kv),
+                     dim3(moba::kKv4ColThreads), moba::kKv4ColSmemBytes, st, p);
+    } else if (acc) {
       const int per = moba::kKv4WeightThreads / 32;
       launch_chained(few ? moba::kv4_weight_kernel<false> : moba::kv4_weight_kernel<true>,
                      dim3((unsigned)((p.tiles + per - 1) / per), batch * heads_kv), dim3(moba::kKv4WeightThreads), 0,

@@ -258,6 +258,12 @@ DENSE = [
     (1, 1, [2000], [300]),
     (2, 4, [700], [129]),
     (1, 40, [200], [9]),
+    (2, 4, [1500, 900], [200, 77]),             # many rows: units of 256, the last of them short
+    (1, 8, [128], [128]),                       # a whole prompt
+    (1, 1, [5000], [257]),                      # a single row in the second tile
+    (1, 1, [4100], [128]),
+    (1, 3, [77, 300, 0, 64], [90, 100, 70, 64]),  # more queries than tokens
+    (1, 70, [1000, 130], [1, 1]),               # one token, many heads of a kv head
 ]
 
 
