@@ -330,8 +330,7 @@ __device__ __forceinline__ void kv4_remote_st(uint32_t* p, uint32_t rank, uint32
 // index. A radix selection finds the smallest kept weight in three passes of
 // 11, 11 and 10 bits (counts per CTA, summed and searched by the first one
 // through distributed shared memory); a last pass writes the kept indexes,
-// each thread's neighbouring weights at its place in the order. The weights
-// are read four times, from L2 after the first.
+// each thread's neighbouring weights at its place in the order.
 __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictParams p) {
   grid_dependency_sync();
   __shared__ uint32_t hist[kKv4SelectBins];
@@ -374,6 +373,10 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
     }
   };
   constexpr int kSweep = kKv4SelectThreads * kKv4SelectItems;
+  // a part that is one sweep stays in registers, a longer one is read again in each pass
+  const bool once = i1 - i0 <= kSweep;
+  uint32_t k[kKv4SelectItems];
+  if (once) keys(i0 + tid * kKv4SelectItems, k);
   uint32_t prefix = 0, need = want;        // of the keys that share `prefix`, `need` stay
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 32 : pass == 1 ? 21 : 10;
@@ -381,8 +384,7 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
     for (int i = tid; i < kKv4SelectBins; i += kKv4SelectThreads) hist[i] = 0;
     __syncthreads();
     for (int at = i0 + tid * kKv4SelectItems; at < i1; at += kSweep) {
-      uint32_t k[kKv4SelectItems];
-      keys(at, k);
+      if (!once) keys(at, k);
 #pragma unroll
       for (int x = 0; x < kKv4SelectItems; ++x)
         if (at + x < i1 && (pass == 0 || (k[x] >> above) == (prefix >> above)))
@@ -418,8 +420,7 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
   // keys above `prefix` stay, and the first `need` equal to it
   uint32_t above = 0, equal = 0;
   for (int at = i0 + tid * kKv4SelectItems; at < i1; at += kSweep) {
-    uint32_t k[kKv4SelectItems];
-    keys(at, k);
+    if (!once) keys(at, k);
 #pragma unroll
     for (int x = 0; x < kKv4SelectItems; ++x) {
       above += at + x < i1 && k[x] > prefix;
@@ -442,10 +443,9 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
   kv4_cluster_sync();  // no CTA leaves while another may still read its counts
   for (int s0 = i0; s0 < i1; s0 += kSweep) {
     const int at = s0 + tid * kKv4SelectItems;
-    uint32_t k[kKv4SelectItems];
     above = equal = 0;
     if (at < i1) {
-      keys(at, k);
+      if (!once) keys(at, k);
 #pragma unroll
       for (int x = 0; x < kKv4SelectItems; ++x) {
         above += at + x < i1 && k[x] > prefix;

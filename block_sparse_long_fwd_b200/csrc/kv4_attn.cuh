@@ -146,6 +146,7 @@ __device__ __forceinline__ bool kv4_after(double s, int j, double ps, int pj) {
 // attention itself (one mean per block of at least 128 keys).
 __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
+  extern __shared__ uint32_t picked[];  // [blocks]: rows of the unit that chose the block
   __shared__ float q[32][kHeadDim];
   __shared__ Kv4Unit s_unit;
   __shared__ uint32_t warp_sums[32];
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
   const int cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int WARPS = kKv4GateThreads / 32;
   double* scores = p.scores + (int64_t)cluster * p.R * p.means;
   const int nu = p.slots * p.Hkv;
   for (int ui = cluster; ui < nu; ui += clusters) {
@@ -162,102 +164,120 @@ __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams
     Kv4Unit u = s_unit;
     const int last = u.rows ? kv4_last_pos(p, u) : -1;
     const int own = last < 0 ? 0 : last / p.B;  // past blocks of the last row
-    uint32_t* chosen = p.chosen + (int64_t)ui * p.blocks;
+    const int n = min(own, p.means);
     if (last >= 0) {
-      for (int i = tid; i < u.rows * kHeadDim; i += kKv4GateThreads) {
-        const int r = i / kHeadDim, c = i % kHeadDim, rr = u.row0 + r;
-        q[r][c] = __bfloat162float(
-            p.q[((int64_t)(u.t0 + rr / p.G) * p.Hq + u.h * p.G + rr % p.G) * kHeadDim + c]);
-      }
-      for (int j = rank * kKv4GateThreads + tid; j < p.blocks; j += csize * kKv4GateThreads) chosen[j] = 0;
-    }
-    __syncthreads();
-    if (last >= 0) {
+      // this warp's first means are on their way while the rows come
       const float* means = p.kmean + ((int64_t)u.b * p.Hkv + u.h) * p.means * kHeadDim;
-      const int n = min(own, p.means);
-      for (int j = rank * (kKv4GateThreads / 32) + warp; j < n; j += csize * (kKv4GateThreads / 32)) {
-        const float4 m = __ldg(reinterpret_cast<const float4*>(means + (int64_t)j * kHeadDim) + lane);
+      const int j0 = rank * WARPS + warp, step = csize * WARPS;
+      float4 m[4];
+      auto fetch = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          m[i] = j + i * step < n ? __ldg(reinterpret_cast<const float4*>(means + (int64_t)(j + i * step) * kHeadDim) + lane)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+      };
+      fetch(j0);
+      for (int i = tid; i < u.rows * 16; i += kKv4GateThreads) {
+        const int r = i >> 4, c = i & 15, rr = u.row0 + r;
+        const uint4 raw = __ldg(reinterpret_cast<const uint4*>(
+            p.q + ((int64_t)(u.t0 + rr / p.G) * p.Hq + u.h * p.G + rr % p.G) * kHeadDim) + c);
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          q[r][8 * c + 2 * k] = __uint_as_float(w[k] << 16);
+          q[r][8 * c + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        }
+      }
+      if (rank == 0)
+        for (int j = tid; j < p.blocks; j += kKv4GateThreads) picked[j] = 0;
+      __syncthreads();
+      for (int j = j0; j < n; j += 4 * step) {
+        if (j != j0) fetch(j);
         for (int r = 0; r < u.rows; ++r) {
           const float4 x = *reinterpret_cast<const float4*>(&q[r][lane * 4]);
-          double s = (double)x.x * m.x;
-          s = fma((double)x.y, (double)m.y, s);
-          s = fma((double)x.z, (double)m.z, s);
-          s = fma((double)x.w, (double)m.w, s);
+          double s[4];
 #pragma unroll
-          for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-          if (lane == 0) scores[(int64_t)r * p.means + j] = s;
+          for (int i = 0; i < 4; ++i) {
+            s[i] = (double)x.x * m[i].x;
+            s[i] = fma((double)x.y, (double)m[i].y, s[i]);
+            s[i] = fma((double)x.z, (double)m[i].z, s[i]);
+            s[i] = fma((double)x.w, (double)m[i].w, s[i]);
+          }
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], d);
+          if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (j + i * step < n) scores[(int64_t)r * p.means + j + i * step] = s[i];
         }
       }
     }
     kv4_cluster_sync();
     if (rank == 0) {
       if (last >= 0) {
-        for (int r = warp; r < u.rows; r += kKv4GateThreads / 32) {
+        for (int r = warp; r < u.rows; r += WARPS) {
           const int pos = u.pos0 + (u.row0 + r) / p.G;
           if (pos < 0) continue;
           const int mine = pos / p.B, picks = min(p.topk - 1, mine);
           const uint32_t bit = 1u << r;
-          if (lane == 0) atomicOr(&chosen[mine], bit);
+          if (lane == 0) atomicOr(&picked[mine], bit);
           if (picks == mine) {
-            for (int j = lane; j < mine; j += 32) atomicOr(&chosen[j], bit);
+            for (int j = lane; j < mine; j += 32) atomicOr(&picked[j], bit);
             continue;
           }
           const double* sc = scores + (int64_t)r * p.means;
           double ps = 0.0;
           int pj = -1;
-          if (mine <= 32 * kKv4GateRegs) {
-            double mv[kKv4GateRegs];
+          const bool few = mine <= 32 * kKv4GateRegs;
+          double mv[kKv4GateRegs];
+          if (few)
 #pragma unroll
             for (int i = 0; i < kKv4GateRegs; ++i) mv[i] = i * 32 + lane < mine ? __ldcg(sc + i * 32 + lane) : 0.0;
-            for (int k = 0; k < picks; ++k) {
-              double s = 0.0;
-              int j = -1;
+          for (int k = 0; k < picks; ++k) {
+            double s = 0.0;
+            int j = -1;
+            if (few) {
 #pragma unroll
               for (int i = 0; i < kKv4GateRegs; ++i) {
                 const int jj = i * 32 + lane;
                 if (jj < mine && kv4_after(mv[i], jj, ps, pj) && (j < 0 || mv[i] > s)) s = mv[i], j = jj;
               }
-              kv4_warp_best(s, j);
-              if (j < 0) break;  // only NaN scores are left
-              if (lane == 0) atomicOr(&chosen[j], bit);
-              ps = s;
-              pj = j;
-            }
-          } else {
-            for (int k = 0; k < picks; ++k) {
-              double s = 0.0;
-              int j = -1;
+            } else {
               for (int jj = lane; jj < mine; jj += 32) {
                 const double v = __ldcg(sc + jj);
                 if (kv4_after(v, jj, ps, pj) && (j < 0 || v > s)) s = v, j = jj;
               }
-              kv4_warp_best(s, j);
-              if (j < 0) break;
-              if (lane == 0) atomicOr(&chosen[j], bit);
-              ps = s;
-              pj = j;
             }
+            kv4_warp_best(s, j);
+            if (j < 0) break;  // only NaN scores are left
+            if (lane == 0) atomicOr(&picked[j], bit);
+            ps = s;
+            pj = j;
           }
         }
       }
       __syncthreads();
       // the chosen blocks in order; the last one (the last row's own) may be partial
       uint2* list = p.list + (int64_t)ui * p.list_cap;
-      uint32_t n = 0;
+      uint32_t count = 0;
       if (last >= 0) {
-        for (int j0 = 0; j0 <= own; j0 += kKv4GateThreads) {
-          const int j = j0 + tid;
-          const uint32_t rows = j <= own ? __ldcg(chosen + j) : 0;
+        for (int k0 = 0; k0 <= own; k0 += kKv4GateThreads) {
+          const int j = k0 + tid;
+          const uint32_t rows = j <= own ? picked[j] : 0;
           uint32_t total;
-          const uint32_t at = n + kv4_block_scan(rows != 0, warp_sums, &total);
+          const uint32_t at = count + kv4_block_scan(rows != 0, warp_sums, &total);
           if (rows && at < (uint32_t)p.list_cap) list[at] = make_uint2(j, rows);
-          n += total;
+          count += total;
         }
-        n = min(n, (uint32_t)p.list_cap);
+        count = min(count, (uint32_t)p.list_cap);
+        if (p.acc)
+          for (int j = tid; j < p.blocks; j += kKv4GateThreads) p.chosen[(int64_t)ui * p.blocks + j] = picked[j];
       }
       if (tid == 0) {
-        u.blocks = n;
-        u.tiles = n ? (int)(n - 1) * (p.B / kKv4Tile) + (last - own * p.B) / kKv4Tile + 1 : 0;
+        u.blocks = count;
+        u.tiles = count ? (int)(count - 1) * (p.B / kKv4Tile) + (last - own * p.B) / kKv4Tile + 1 : 0;
         p.units[ui] = u;
       }
     }
@@ -280,7 +300,14 @@ __device__ __forceinline__ int kv4_ctas(const Kv4AttnParams& p, int64_t all) {
 // left in scratch for the rest of the CTA and for the join (units of several
 // CTAs get the same values from each); CTA 0 leaves those without tiles.
 // `copy`: shared memory for the offsets and lengths, `room` words.
+// The first units of the range stay in shared memory, where every role walks
+// them without a trip to L2.
+constexpr int kKv4Kept = 16;
 struct Kv4Range {
+  const Kv4Unit* kept;
+  const Kv4Unit* units;
+  int first;      // unit of kept[0]
+  __device__ __forceinline__ Kv4Unit at(int ui) const { return ui - first < kKv4Kept ? kept[ui - first] : units[ui]; }
   int n;          // items of this part
   int unit, off;  // its first unit, items of it that lie before the range
   bool any;       // the CTA has some
@@ -291,9 +318,12 @@ __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* co
   constexpr int WARPS = THREADS / 32;
   __shared__ int64_t warp_sums[WARPS], bound[PARTS + 1];
   __shared__ int2 s_start[PARTS];
+  __shared__ Kv4Unit s_kept[kKv4Kept];
+  __shared__ int s_first;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
   const int nu = p.slots * p.Hkv;
   const int32_t *cu = p.cu, *lengths = p.lengths;
+  for (int i = tid; i < kKv4Kept; i += THREADS) s_kept[i].tiles = 0;  // units without tiles are not kept
   if (!p.kmean && 2 * p.batch + 1 <= room) {
     for (int i = tid; i < p.batch; i += THREADS) copy[i] = p.lengths[i];
     lengths = copy;
@@ -352,10 +382,13 @@ __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* co
       before += done;
       done += sum;
     }
+    const int64_t end = before + kv4_items(p, u);
+    const bool mine = ui < nu && u.tiles > 0 && before < hi && end > lo;
+    if (mine && before <= lo) s_first = ui;
+    __syncthreads();
     if (ui < nu) {
-      const int64_t end = before + kv4_items(p, u);
-      const bool mine = u.tiles > 0 && before < hi && end > lo;
       if (mine) {
+        if (ui - s_first < kKv4Kept) s_kept[ui - s_first] = u;
         p.before[ui] = before;
         for (int w = 0; w < PARTS; ++w) {
           const int64_t x = bound[w];
@@ -367,6 +400,9 @@ __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* co
   }
   __syncthreads();
   Kv4Range g;
+  g.kept = s_kept;
+  g.units = p.units;
+  g.first = s_first;
   g.any = hi > lo;
   const int part = PARTS == 1 ? 0 : warp;
   g.n = (int)(bound[part + 1] - bound[part]);
@@ -576,9 +612,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
     if (c_left <= 0) return;
     if (c_off >= c_end) {  // on to the next unit that has tiles
       c_off -= c_end;
-      do c_end = 2 * p.units[++c_ui].tiles;
+      do c_end = 2 * range.at(++c_ui).tiles;
       while (c_end == 0);
-      const Kv4Unit u = p.units[c_ui];
+      const Kv4Unit u = range.at(c_ui);
       c_src = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, u.b, u.h, 0) + piece;
       if (p.kmean) {
         c_at = (c_off >> 1) / tpb;
@@ -620,7 +656,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
   int death = 0;  // the half tile that never came
   int k = 0;      // half tiles of this warp behind us
   for (int ui = range.unit, off = range.off; k < n; ++ui, off = 0) {
-    const Kv4Unit u = p.units[ui];
+    const Kv4Unit u = range.at(ui);
     const int stop = k + min(n - k, 2 * u.tiles - off);
     if (stop == k) continue;
     // the rows' fragments, scales, and last keys (of this lane's two rows of each group of eight)
@@ -876,10 +912,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
       if (sh->unit[e] == ui) fin = e;
       ++e;
     }
-    const int rows = p.units[ui].rows;
+    const Kv4Unit u = range.at(ui);
+    const int rows = u.rows;
     for (int row = 0; row < rows; ++row, ++item) {
       if (item % C::WARPS != warp) continue;
-      const Kv4Unit u = p.units[ui];
       float mm = kKv4Low, ll = 0.f;
       for (int i = s; i <= fin; ++i)
         if (sh->unit[i] == ui) mm = fmaxf(mm, sh->ml[i >> 1][i & 1][row].x);

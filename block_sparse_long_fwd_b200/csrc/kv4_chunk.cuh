@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kKv4ChunkThreads, 1) kv4_chunk_kernel(Kv4AttnP
     uint32_t sx = 0;  // steps done by tile X
     int done = 0;
     for (int ui = range.unit, s0 = range.off; done < range.n; ++ui, s0 = 0) {
-      const Kv4Unit u = p.units[ui];
+      const Kv4Unit u = range.at(ui);
       const int steps = kv4_items(p, u), s1 = min(steps, s0 + range.n - done);
       if (s1 <= s0) continue;
       done += s1 - s0;
@@ -331,9 +331,9 @@ __global__ void __launch_bounds__(kKv4ChunkThreads, 1) kv4_chunk_kernel(Kv4AttnP
       if (c_left <= 0) return;
       if (c_s >= c_end) {
         c_s -= c_end;
-        do c_end = kv4_items(p, p.units[++c_ui]);
+        do c_end = kv4_items(p, range.at(++c_ui));
         while (c_end == 0);
-        const Kv4Unit u = p.units[c_ui];
+        const Kv4Unit u = range.at(c_ui);
         c_src = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, u.b, u.h, 0);
         c_keys = kv4_last_pos(p, u) + 1;
       }
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kKv4ChunkThreads, 1) kv4_chunk_kernel(Kv4AttnP
     uint32_t ux[2] = {0, 0};   // units per tile
     int done = 0;
     for (int ui = range.unit, s0 = range.off; done < range.n; ++ui, s0 = 0) {
-      const Kv4Unit u = p.units[ui];
+      const Kv4Unit u = range.at(ui);
       const int s1 = min(kv4_items(p, u), s0 + range.n - done);
       if (s1 <= s0) continue;
       done += s1 - s0;
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kKv4ChunkThreads, 1) kv4_chunk_kernel(Kv4AttnP
     uint32_t ux[2] = {0, 0};
     int done = 0;
     for (int ui = range.unit, s0 = range.off; done < range.n; ++ui, s0 = 0) {
-      const Kv4Unit u = p.units[ui];
+      const Kv4Unit u = range.at(ui);
       const int s1 = min(kv4_items(p, u), s0 + range.n - done);
       if (s1 <= s0) continue;
       done += s1 - s0;

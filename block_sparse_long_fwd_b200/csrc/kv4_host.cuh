@@ -36,10 +36,12 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 
 // As launch_chained, with the grid in clusters of `csize` CTAs along x.
 template <typename... KArgs, typename... Args>
-void launch_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 block, int csize, cudaStream_t st, Args... args) {
+void launch_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int csize, cudaStream_t st,
+                     Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -69,11 +71,11 @@ cudaError_t set_kv4_attn_smem() {
 }
 
 // Rows of a sequence and kv head, on average, above which the tcgen05 kernel
-// takes over.
-int64_t kv4_chunk_rows() {
-  const char* e = getenv("KV4_CHUNK_ROWS");
-  return e ? atoll(e) : 64;
-}
+// (256 rows a unit) takes over from mma.sync (16 rows a unit, every key widened
+// for each of them). At 32K tokens, 32 / 8 heads, one sequence: 32 rows 43
+// against 44 us, 64 rows 45 against 65, 2048 rows 293 against 1430; 16
+// sequences of 8K: 16 rows 162 against 70, 64 rows 173 against 219.
+constexpr int kKv4ManyRows = 48;
 
 bool g_kv4_ready[64] = {};
 
@@ -92,6 +94,8 @@ int kv4_begin(DeviceInfo* dev, cudaStream_t st) {
                                      moba::kKv4ChunkSmemBytes));
       MOBA_CUDA(cudaFuncSetAttribute(moba::kv4_chunk_weight_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      moba::kKv4ColSmemBytes));
+      MOBA_CUDA(cudaFuncSetAttribute(moba::kv4_gate_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     MOBA_KV4_MAX_BLOCKS * 4 + 4));
       g_kv4_ready[d] = true;
     }
   }
@@ -192,12 +196,12 @@ int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch, int heads_
   p.blocks = (int)(capacity / block_size);
   p.kmean = kmean;
   if (p.blocks) {
-    // a CTA for every 512 tokens of a block, up to 8 of them
+    // up to 8 CTAs share a block while there are too few blocks for two CTAs an SM
     int csize = 1;
-    while (csize < 8 && block_size / csize > 512) csize *= 2;
+    while (csize < 8 && (int64_t)p.blocks * heads_kv * batch * csize < 2 * dev.sms && block_size / csize > 256) csize *= 2;
     if ((int64_t)p.blocks * csize > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many blocks");
-    launch_clusters(moba::kv4_pool_kernel, dim3(p.blocks * csize, heads_kv, batch), dim3(moba::kKv4PoolThreads), csize,
-                    stream, p);
+    launch_clusters(moba::kv4_pool_kernel, dim3(p.blocks * csize, heads_kv, batch), dim3(moba::kKv4PoolThreads), 0,
+                    csize, stream, p);
     MOBA_CUDA(cudaGetLastError());
   }
   return finish_call(MOBA_OK, stream);
@@ -251,7 +255,7 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   p.means = kmean ? (int)(capacity / block_size) : 0;
   p.blocks = kmean ? (int)((capacity + block_size - 1) / block_size) : 0;
   const bool few = total * p.G <= (int64_t)moba::Kv4Few::R * batch;
-  const bool chunk = !kmean && total * p.G > kv4_chunk_rows() * batch;
+  const bool chunk = !kmean && total * p.G > (int64_t)kKv4ManyRows * batch;
   p.R = few ? moba::Kv4Few::R : chunk ? moba::kKv4ChunkRows : moba::Kv4Many::R;
   const int64_t slots = total * p.G / p.R + batch;
   if (slots * heads_kv * p.R > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
@@ -268,7 +272,7 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   Carve c;
   const size_t o_units = c.take((size_t)nu * sizeof(moba::Kv4Unit)), o_before = c.take((size_t)(nu + 1) * 8);
   const size_t o_list = c.take((size_t)nu * p.list_cap * 8);
-  const size_t o_chosen = c.take((size_t)nu * p.blocks * 4);
+  const size_t o_chosen = c.take(acc ? (size_t)nu * p.blocks * 4 : 0);
   const size_t o_scores = c.take((size_t)clusters * p.R * p.means * 8);
   const size_t o_part = c.take((size_t)2 * p.ctas * p.R * 130 * 4);
   const size_t o_qtiles = c.take(chunk ? (size_t)nu * 2 * moba::kKv4TileOp : 0);
@@ -283,8 +287,8 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
     p.scores = reinterpret_cast<double*>(ws + o_scores);
     p.part = reinterpret_cast<float*>(ws + o_part);
     if (kmean)
-      launch_clusters(moba::kv4_gate_kernel, dim3((unsigned)(clusters * csize)), dim3(moba::kKv4GateThreads), csize, st,
-                      p);
+      launch_clusters(moba::kv4_gate_kernel, dim3((unsigned)(clusters * csize)), dim3(moba::kKv4GateThreads),
+                      (size_t)p.blocks * 4, csize, st, p);
     if (few) {
       launch_kv4_attn<moba::Kv4Few>(p, st);
     } else if (chunk) {
@@ -354,7 +358,8 @@ int moba_kv4_evict(const void* kv4, const float* acc, const int32_t* lengths, in
   // up to 8 CTAs select for a kv head while there are SMs for them and 4096 weights for each
   int csize = 1;
   while (csize < 8 && (int64_t)pairs * csize * 2 <= 2 * dev.sms && capacity / csize > 4096) csize *= 2;
-  launch_clusters(moba::kv4_select_kernel, dim3((unsigned)pairs * csize), dim3(moba::kKv4SelectThreads), csize, stream, p);
+  launch_clusters(moba::kv4_select_kernel, dim3((unsigned)pairs * csize), dim3(moba::kKv4SelectThreads), 0, csize, stream,
+                  p);
   const int64_t per = moba::kKv4MoveThreads / 16 * moba::kKv4MoveTokens;
   launch_chained(moba::kv4_move_kernel, dim3((unsigned)((budget + per - 1) / per), (unsigned)pairs),
                  dim3(moba::kKv4MoveThreads), 0, stream, p);
