@@ -37,7 +37,8 @@ struct Kv4AttnParams {
   int batch, Hq, Hkv, G;
   int B, topk, means;           // with kmean: block size, means = capacity / B
   int blocks;                   // blocks of the capacity, the last one partial
-  int R, slots;                 // rows of a unit; unit slots per kv head
+  int R, rshift, slots;         // rows of a unit, 2^rshift; unit slots per kv head
+  int each;                     // without cu, queries of a sequence
   float scale_log2;             // log2(e) / sqrt(128)
   float* acc;                   // [batch][Hkv][tiles * 64], or null
   __nv_bfloat16* out;           // [total][Hq][128]
@@ -60,9 +61,8 @@ struct Kv4AttnParams {
 // outside the rows are a caller's error, recorded and read as no query.
 __device__ __forceinline__ int kv4_queries(const Kv4AttnParams& p, const int32_t* cu, int b, int* t0) {
   if (!cu) {
-    const int n = (int)(p.total / p.batch);
-    *t0 = b * n;
-    return n;
+    *t0 = b * p.each;
+    return p.each;
   }
   const int c0 = cu[b], c1 = cu[b + 1];
   *t0 = c0;
@@ -76,8 +76,8 @@ __device__ __forceinline__ int kv4_queries(const Kv4AttnParams& p, const int32_t
 // First unit slot of sequence b, whose rows start at row t0 * G of a kv head:
 // each sequence has room for its rows / R, rounded up, without a scan over the
 // sequences before it (floor(x / R) grows by at least ceil(n / R) - 1).
-__device__ __forceinline__ int64_t kv4_first_slot(const Kv4AttnParams& p, int b, int t0) {
-  return (int64_t)t0 * p.G / p.R + b;
+__device__ __forceinline__ int kv4_first_slot(const Kv4AttnParams& p, int b, int t0) {
+  return (int)((uint32_t)t0 * (uint32_t)p.G >> p.rshift) + b;
 }
 
 // The unit of slot `slot` of kv head h; rows = 0 for an unused slot. cu and
@@ -89,14 +89,13 @@ __device__ __forceinline__ Kv4Unit kv4_unit_of(const Kv4AttnParams& p, const int
   int lo = 0, hi = p.batch;  // first_slot(lo) <= slot < first_slot(hi)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    const int t = cu ? cu[mid] : (int)(mid * (p.total / p.batch));
+    const int t = cu ? cu[mid] : mid * p.each;
     if (kv4_first_slot(p, mid, t) <= slot) lo = mid;
     else hi = mid;
   }
   int t0;
   const int n = kv4_queries(p, cu, lo, &t0);
-  const int64_t first = kv4_first_slot(p, lo, t0);
-  const int64_t row0 = (slot - first) * p.R;
+  const int64_t row0 = ((int64_t)slot - kv4_first_slot(p, lo, t0)) << p.rshift;
   if (row0 < 0 || row0 >= (int64_t)n * p.G) return u;
   u.b = lo;
   u.row0 = (int)row0;
@@ -288,9 +287,11 @@ __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams
 
 // ------------------------------------------------------------------ plan
 
-// CTAs that get a range of `all` items: as many as leave no part of one idle.
-__device__ __forceinline__ int kv4_ctas(const Kv4AttnParams& p, int64_t all) {
-  return (int)min((int64_t)p.ctas, (all + p.parts - 1) / p.parts);
+// Items of a part's range: the same for all but the last that has any.
+__device__ __forceinline__ int64_t kv4_quota(const Kv4AttnParams& p, int64_t all) {
+  const int n = p.ctas * p.parts;
+  if (all < (1ll << 31) - n) return ((uint32_t)all + n - 1) / n;  // a 64-bit division costs several times more
+  return (all + n - 1) / n;
 }
 
 // Where each part's range begins (a part is a warp, or the CTA): every CTA scans all units' tiles for itself
@@ -316,7 +317,7 @@ struct Kv4Range {
 template <int THREADS, int PARTS>
 __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* copy, int room) {
   constexpr int WARPS = THREADS / 32;
-  __shared__ int64_t warp_sums[WARPS], bound[PARTS + 1];
+  __shared__ int64_t warp_sums[WARPS];
   __shared__ int2 s_start[PARTS];
   __shared__ Kv4Unit s_kept[kKv4Kept];
   __shared__ int s_first;
@@ -342,70 +343,67 @@ __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* co
     u.tiles = last < 0 ? 0 : last / kKv4Tile + 1;
     return u;
   };
-  // sum over the block; `before` of the own thread
-  auto scan = [&](int64_t x, int64_t* before) {
-    int64_t s = x;
+  // neighbouring units for each thread, found again below where there are several
+  const int mine = (nu + THREADS - 1) / THREADS, u0 = tid * mine;
+  Kv4Unit u = unit(u0);
+  int64_t x = kv4_items(p, u);
+  for (int i = 1; i < mine; ++i) x += kv4_items(p, unit(u0 + i));
+  int64_t s = x;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, d);
-      if (lane >= d) s += y;
-    }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = s;
-    __syncthreads();
-    int64_t base = 0, sum = 0;
-    for (int i = 0; i < WARPS; ++i) {
-      if (i < warp) base += warp_sums[i];
-      sum += warp_sums[i];
-    }
-    *before = base + s - x;
-    return sum;
-  };
-  Kv4Unit u = unit(tid);
-  int64_t before, all = scan(kv4_items(p, u), &before);
-  const bool once = nu <= THREADS;
-  for (int u0 = THREADS; u0 < nu; u0 += THREADS) {
-    int64_t unused;
-    all += scan(kv4_items(p, unit(u0 + tid)), &unused);
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, d);
+    if (lane >= d) s += y;
   }
-  const int ctas = kv4_ctas(p, all);
-  if (tid <= PARTS) bound[tid] = cta < ctas ? all * (cta * PARTS + tid) / (ctas * PARTS) : all;  // start of part tid
+  if (lane == 31) warp_sums[warp] = s;
   __syncthreads();
-  const int64_t lo = bound[0], hi = bound[PARTS];
+  int64_t before = s - x, all = 0;
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) {
+    const int64_t y = warp_sums[i];
+    if (i < warp) before += y;
+    all += y;
+  }
+  const int64_t quota = kv4_quota(p, all);
+  const int64_t lo = min(cta * PARTS * quota, all), hi = min(lo + PARTS * quota, all);
   if (cta == 0 && tid == 0) p.before[nu] = all;
-  int64_t done = 0;
-  for (int u0 = 0; u0 < nu; u0 += THREADS) {
-    const int ui = u0 + tid;
-    if (!once) {
-      u = unit(ui);
-      const int64_t sum = scan(kv4_items(p, u), &before);
-      before += done;
-      done += sum;
+  const bool touches = before < hi && before + x > lo;
+  if (touches && before <= lo) {
+    int64_t at = before;
+    for (int i = 0; i < mine; ++i) {
+      const int n = kv4_items(p, mine == 1 ? u : unit(u0 + i));
+      if (at <= lo && lo < at + n) s_first = u0 + i;
+      at += n;
     }
-    const int64_t end = before + kv4_items(p, u);
-    const bool mine = ui < nu && u.tiles > 0 && before < hi && end > lo;
-    if (mine && before <= lo) s_first = ui;
-    __syncthreads();
-    if (ui < nu) {
-      if (mine) {
+  }
+  __syncthreads();
+  if (touches || cta == 0) {
+    int64_t at = before;
+    for (int i = 0; i < mine && u0 + i < nu; ++i) {
+      const int ui = u0 + i;
+      if (mine > 1) u = unit(ui);
+      const int n = kv4_items(p, u);
+      if (n > 0 && at < hi && at + n > lo) {
         if (ui - s_first < kKv4Kept) s_kept[ui - s_first] = u;
-        p.before[ui] = before;
+        p.before[ui] = at;
         for (int w = 0; w < PARTS; ++w) {
-          const int64_t x = bound[w];
-          if (x >= before && x < end) s_start[w] = make_int2(ui, (int)(x - before));
+          const int64_t y = lo + w * quota;
+          if (y >= at && y < at + n) s_start[w] = make_int2(ui, (int)(y - at));
         }
+        if (!p.kmean) p.units[ui] = u;
+      } else if (!p.kmean && cta == 0 && n == 0) {
+        p.units[ui] = u;
       }
-      if (!p.kmean && (mine || (cta == 0 && u.tiles == 0))) p.units[ui] = u;
+      at += n;
     }
   }
   __syncthreads();
   Kv4Range g;
+  const int part = PARTS == 1 ? 0 : warp;
   g.kept = s_kept;
   g.units = p.units;
   g.first = s_first;
   g.any = hi > lo;
-  const int part = PARTS == 1 ? 0 : warp;
-  g.n = (int)(bound[part + 1] - bound[part]);
+  g.n = (int)max((int64_t)0, min(quota, hi - lo - part * quota));
   g.unit = g.n ? s_start[part].x : 0;
   g.off = g.n ? s_start[part].y : 0;
   return g;
@@ -899,60 +897,55 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
   }
   __syncthreads();
 
-  // ---- join the CTA's pieces: those of a unit follow one another. One warp per (unit, row)
+  // ---- join the CTA's pieces: a lane for each, those of a unit follow one another; one warp per (unit, row)
+  static_assert(2 * C::WARPS <= 32, "a lane for each piece");
+  const int my_unit = lane < 2 * C::WARPS ? sh->unit[lane] : -1;
+  const uint32_t used = __ballot_sync(0xFFFFFFFFu, my_unit >= 0);
   int item = 0;
-  for (int s = 0; s < 2 * C::WARPS;) {
-    const int ui = sh->unit[s];
-    if (ui < 0) {
-      ++s;
-      continue;
-    }
-    int e = s + 1, fin = s;  // the pieces s .. fin
-    while (e < 2 * C::WARPS && (sh->unit[e] < 0 || sh->unit[e] == ui)) {
-      if (sh->unit[e] == ui) fin = e;
-      ++e;
-    }
+  for (uint32_t left = used; left;) {
+    const int first = __ffs(left) - 1, ui = __shfl_sync(0xFFFFFFFFu, my_unit, first);
+    const uint32_t of = __ballot_sync(0xFFFFFFFFu, my_unit == ui) & used;
+    left &= ~of;
+    const int fin = 31 - __clz(of);
     const Kv4Unit u = range.at(ui);
-    const int rows = u.rows;
-    for (int row = 0; row < rows; ++row, ++item) {
+    const bool begins = sh->begins[first], whole = begins && sh->ends[fin];
+    for (int row = 0; row < u.rows; ++row, ++item) {
       if (item % C::WARPS != warp) continue;
-      float mm = kKv4Low, ll = 0.f;
-      for (int i = s; i <= fin; ++i)
-        if (sh->unit[i] == ui) mm = fmaxf(mm, sh->ml[i >> 1][i & 1][row].x);
+      const bool on = of >> lane & 1u;
+      const float2 x = on ? sh->ml[lane >> 1][lane & 1][row] : make_float2(kKv4Low, 0.f);
+      float mm = x.x;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, d));
+      const float a = ex2_approx(x.x - mm);
+      float ll = x.y * a;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, d);
       float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = s; i <= fin; ++i) {
-        if (sh->unit[i] != ui) continue;
-        const float2 x = sh->ml[i >> 1][i & 1][row];
-        const float a = ex2_approx(x.x - mm);
+#pragma unroll 4
+      for (int i = first; i <= fin; ++i) {
+        if (!(of >> i & 1u)) continue;
+        const float f = __shfl_sync(0xFFFFFFFFu, a, i);
         const float* from = reinterpret_cast<const float*>(i & 1 ? &sh->ring[i >> 1][0][0] : sh->piece[i >> 1]);
         const float4 v = reinterpret_cast<const float4*>(from + row * kHeadDim)[lane ^ (lane >> 2 & 3)];
-        ll = fmaf(x.y, a, ll);
-        oo.x = fmaf(v.x, a, oo.x);
-        oo.y = fmaf(v.y, a, oo.y);
-        oo.z = fmaf(v.z, a, oo.z);
-        oo.w = fmaf(v.w, a, oo.w);
+        oo.x = fmaf(v.x, f, oo.x);
+        oo.y = fmaf(v.y, f, oo.y);
+        oo.z = fmaf(v.z, f, oo.z);
+        oo.w = fmaf(v.w, f, oo.w);
       }
-      if (sh->begins[s] && sh->ends[fin]) {
+      if (whole) {
         kv4_write_row(p, u, row, lane, mm, ll, oo);
       } else {
-        float* part = p.part + (int64_t)(2 * cta + (sh->begins[s] ? 1 : 0)) * (R * 130);
+        float* part = p.part + (int64_t)(2 * cta + (begins ? 1 : 0)) * (R * 130);
         reinterpret_cast<float4*>(part + row * kHeadDim)[lane] = oo;
         if (lane == 0) *reinterpret_cast<float2*>(part + R * kHeadDim + 2 * row) = make_float2(mm, ll);
       }
     }
-    s = e;
   }
 }
 
 // ------------------------------------------------------------------ join
 
 constexpr int kKv4JoinThreads = 128;
-
-// The CTA whose range holds item x of `all`: the last one that begins at
-// or before it.
-__device__ __forceinline__ int kv4_cta_of(int64_t x, int64_t all, int ctas) {
-  return (int)(((x + 1) * ctas + all - 1) / all) - 1;
-}
 
 // One CTA per (unit, row) whose tiles lie in more than one CTA's range: each
 // of its warps takes every fourth partial result, all at once (a loop that
@@ -970,9 +963,9 @@ __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams
   int c0 = 0, c1 = -1;
   if (u.tiles) {
     const int64_t all = p.before[p.slots * p.Hkv], x = p.before[ui];
-    const int ctas = kv4_ctas(p, all);
-    c0 = kv4_cta_of(x, all, ctas);
-    c1 = kv4_cta_of(x + kv4_items(p, u) - 1, all, ctas);
+    const int64_t per_cta = kv4_quota(p, all) * p.parts;
+    c0 = (int)(x / per_cta);
+    c1 = (int)((x + kv4_items(p, u) - 1) / per_cta);
     if (c0 == c1) return;  // written by the CTA itself
   }
   const int64_t per = p.R * 130;
@@ -1030,14 +1023,14 @@ __global__ void __launch_bounds__(kKv4WeightThreads, HOLD ? 2 : 5) kv4_weight_ke
   const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
   const int key0 = (int)(tile * kKv4Tile), pos0 = len - n, rows = n * p.G;
   if (n == 0 || tile >= p.tiles || key0 >= len) return;
-  const int64_t slot0 = kv4_first_slot(p, b, t0);
+  const int slot0 = kv4_first_slot(p, b, t0);
   const int block = key0 / p.B;
   // rows before the first key's position attend nothing here
   int r0 = key0 > pos0 ? (int)((int64_t)(key0 - pos0) * p.G / 8 * 8) : 0;
   auto picked = [&](int row) {
     if (!p.kmean) return 0xFFu;
-    const int64_t ui = (slot0 + row / p.R) * p.Hkv + h;
-    return __ldg(p.chosen + ui * p.blocks + block) >> (row % p.R) & 0xFFu;
+    const int64_t ui = (int64_t)(slot0 + (row >> p.rshift)) * p.Hkv + h;
+    return __ldg(p.chosen + ui * p.blocks + block) >> (row & (p.R - 1)) & 0xFFu;
   };
   while (r0 < rows && !picked(r0)) r0 += 8;
   if (r0 >= rows) return;

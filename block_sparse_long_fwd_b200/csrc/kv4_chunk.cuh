@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kKv4ColThreads, 2) kv4_chunk_weight_kernel(Kv4
   const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
   const int key0 = blockIdx.x * 2 * kTile, pos0 = len - n, rows = n * p.G;
   if (n == 0 || key0 >= len) return;
-  const int64_t slot0 = kv4_first_slot(p, b, t0);
+  const int slot0 = kv4_first_slot(p, b, t0);
   // tiles of 128 rows; rows before the first key's position attend nothing here
   const int tile0 = key0 > pos0 ? (int)((int64_t)(key0 - pos0) * p.G / kTile) : 0, tiles = (rows + kTile - 1) / kTile;
 
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kKv4ColThreads, 2) kv4_chunk_weight_kernel(Kv4
     for (int i = tile0; i < tiles; ++i, ++k) {
       // the rows' numbers of two tiles ago have been read once the products of the last one could start
       if (k > 0 && !mbar_wait(&sh->q_empty, (k - 1) & 1, abort_flag)) break;
-      const int64_t ui = (slot0 + i / 2) * p.Hkv + h;
+      const int64_t ui = (int64_t)(slot0 + i / 2) * p.Hkv + h;
       if (lane == 0) {
         mbar_arrive_expect_tx(&sh->q_full, kKv4TileOp);
         bulk_load(sQ, p.qtiles + (ui * 2 + (i & 1)) * kKv4TileOp, kKv4TileOp, &sh->q_full);

@@ -234,7 +234,7 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   rc = kv4_begin(&dev, stream);
   if (rc) return rc;
   if (total == 0) return finish_call(MOBA_OK, stream);
-  moba::Kv4AttnParams p;
+  moba::Kv4AttnParams p = {};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.kv4 = static_cast<const uint8_t*>(kv4);
   p.lengths = lengths;
@@ -257,6 +257,8 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   const bool few = total * p.G <= (int64_t)moba::Kv4Few::R * batch;
   const bool chunk = !kmean && total * p.G > (int64_t)kKv4ManyRows * batch;
   p.R = few ? moba::Kv4Few::R : chunk ? moba::kKv4ChunkRows : moba::Kv4Many::R;
+  while (1 << p.rshift < p.R) ++p.rshift;
+  p.each = cu ? 0 : (int)(total / batch);
   const int64_t slots = total * p.G / p.R + batch;
   if (slots * heads_kv * p.R > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
   p.slots = (int)slots;
