@@ -170,19 +170,21 @@ struct Kv4AppendParams {
 constexpr int kKv4AppendThreads = 256;
 
 // Four threads per row (token, kv head), a group of keys and the group of
-// values each. HBM-bound: 512 bytes read and 144 written a row.
+// values each; a CTA takes 64 tokens of one head, whose places in the cache
+// lie side by side (rows of all heads in turn scatter the stores: 133 against
+// 1.. us for 128K tokens of 8 heads). HBM-bound: 512 bytes read and 144 written
+// a row.
 __global__ void __launch_bounds__(kKv4AppendThreads) kv4_append_kernel(Kv4AppendParams p) {
   grid_dependency_sync();
-  const int g = threadIdx.x & 3;
-  const int64_t row = ((int64_t)blockIdx.x * kKv4AppendThreads + threadIdx.x) >> 2;
-  if (row >= p.total * p.heads) return;
+  const int g = threadIdx.x & 3, h = blockIdx.y;
+  const int64_t t = (int64_t)blockIdx.x * (kKv4AppendThreads / 4) + (threadIdx.x >> 2);
+  if (t >= p.total) return;
+  const int64_t row = t * p.heads + h;
   uint4 rk[4], rv[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) rk[i] = __ldg(reinterpret_cast<const uint4*>(p.k + row * kHeadDim + g * 32) + i);
 #pragma unroll
   for (int i = 0; i < 4; ++i) rv[i] = __ldg(reinterpret_cast<const uint4*>(p.v + row * kHeadDim + g * 32) + i);
-  const int64_t t = row / p.heads;
-  const int h = (int)(row - t * p.heads);
   int b;
   int64_t at;
   if (p.cu) {
@@ -220,26 +222,24 @@ struct Kv4LoadParams {
 
 constexpr int kKv4LoadThreads = 256, kKv4LoadRows = 4;
 
-// Half a warp per row, 8 channels a lane, four rows of keys and values at a
-// time: 144 bytes read, 512 written a row, HBM-bound.
+// A CTA per 64 tokens of a kv head, half a warp per row, 8 channels a lane,
+// four rows of keys and values at a time: 144 bytes read, 512 written a row,
+// HBM-bound.
 __global__ void __launch_bounds__(kKv4LoadThreads) kv4_load_kernel(Kv4LoadParams p) {
   grid_dependency_sync();
-  const int lane = threadIdx.x & 15;
-  const int64_t rows = (int64_t)p.batch * p.n * p.heads;
-  const int64_t row0 = (int64_t)blockIdx.x * (kKv4LoadThreads / 16 * kKv4LoadRows) + (threadIdx.x >> 4);
+  const int lane = threadIdx.x & 15, h = blockIdx.y, b = blockIdx.z;
+  const int64_t i0 = (int64_t)blockIdx.x * (kKv4LoadThreads / 16 * kKv4LoadRows) + (threadIdx.x >> 4);
+  const int64_t first = p.first ? p.first[b] : 0;
+  const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
+  const uint8_t* src = p.kv4 + kv4_tile_off(p.tiles, p.heads, b, h, 0);
   uint32_t word[kKv4LoadRows][2], par[kKv4LoadRows][2];
 #pragma unroll
   for (int i = 0; i < kKv4LoadRows; ++i) {
-    const int64_t row = row0 + i * (kKv4LoadThreads / 16);
+    const int64_t at = first + i0 + i * (kKv4LoadThreads / 16);
     word[i][0] = word[i][1] = par[i][0] = par[i][1] = 0;
-    if (row >= rows) continue;
-    const int64_t t = row / p.heads;
-    const int h = (int)(row - t * p.heads);
-    const int b = (int)(t / p.n);
-    const int64_t at = (p.first ? (int64_t)p.first[b] : 0) + (t - b * p.n);
-    if (at < 0 || at >= kv4_length(p.lengths, b, p.tiles * kKv4Tile)) continue;
+    if (i0 + i * (kKv4LoadThreads / 16) >= p.n || at < 0 || at >= len) continue;
     const int tok = (int)(at % kKv4Tile);
-    const uint8_t* tile = p.kv4 + kv4_tile_off(p.tiles, p.heads, b, h, at / kKv4Tile);
+    const uint8_t* tile = src + at / kKv4Tile * kKv4TileBytes;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const uint8_t* half = tile + s * kKv4Half;
@@ -249,8 +249,9 @@ __global__ void __launch_bounds__(kKv4LoadThreads) kv4_load_kernel(Kv4LoadParams
   }
 #pragma unroll
   for (int i = 0; i < kKv4LoadRows; ++i) {
-    const int64_t row = row0 + i * (kKv4LoadThreads / 16);
-    if (row >= rows) continue;
+    const int64_t at = i0 + i * (kKv4LoadThreads / 16);
+    if (at >= p.n) continue;
+    const int64_t row = ((int64_t)b * p.n + at) * p.heads + h;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       float x[8];
@@ -315,7 +316,7 @@ __device__ __forceinline__ void kv4_cluster_sync() {
 __device__ __forceinline__ uint32_t kv4_remote_ld(const uint32_t* p, uint32_t rank) {
   uint32_t a, v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ void kv4_remote_st(uint32_t* p, uint32_t rank, uint32_t v) {
@@ -397,8 +398,10 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int bin = kKv4SelectBins - 1 - (2 * tid + x);
-        c[x] = hist[bin];
-        for (uint32_t r = 1; r < csize; ++r) c[x] += kv4_remote_ld(&hist[bin], r);
+        uint32_t y[8];  // all under way at once
+#pragma unroll
+        for (uint32_t r = 0; r < 8; ++r) y[r] = r < csize ? kv4_remote_ld(&hist[bin], r) : 0;
+        c[x] = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
       }
       uint32_t before = kv4_block_scan(c[0] + c[1], warp_sums, &total);
 #pragma unroll

@@ -1005,121 +1005,148 @@ __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams
 
 // ------------------------------------------------------------------ accumulated weights
 
-constexpr int kKv4WeightThreads = 128;
+constexpr int kKv4WeightThreads = 128, kKv4WeightTiles = 8;
 
-// acc[key] += sum over the rows of the kv head of 2^(score - lse): one warp per
+// acc[key] += sum over the rows of the kv head of 2^(score - lse), one warp per
 // 64-token tile; all rows of the sequence pass by, eight at a time, in order.
 // HOLD: the keys are widened once and held in registers (many rows, two CTAs
-// of four warps per SM), else widened for each eight rows (few rows: there is
-// one pass, and what counts is how many warps have loads under way).
+// of four warps per SM), else widened for each eight rows, and a warp goes
+// through kKv4WeightTiles tiles, with the rows' fragments kept where there are
+// at most eight rows (few rows: what counts is how many warps have loads under
+// way, and what a tile costs beside them).
 template <bool HOLD>
 __global__ void __launch_bounds__(kKv4WeightThreads, HOLD ? 2 : 5) kv4_weight_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
+  constexpr int TILES = HOLD ? 1 : kKv4WeightTiles, WARPS = kKv4WeightThreads / 32;
   const int lane = threadIdx.x & 31, r = lane >> 2, qd = lane & 3;
-  const int64_t tile = (int64_t)blockIdx.x * (kKv4WeightThreads / 32) + (threadIdx.x >> 5);
   const int b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
   int t0;
   const int n = kv4_queries(p, p.cu, b, &t0);
   const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
-  const int key0 = (int)(tile * kKv4Tile), pos0 = len - n, rows = n * p.G;
-  if (n == 0 || tile >= p.tiles || key0 >= len) return;
+  const int pos0 = len - n, rows = n * p.G;
+  const int64_t tile0 = (int64_t)blockIdx.x * (WARPS * TILES) + (threadIdx.x >> 5);
+  if (n == 0 || tile0 * kKv4Tile >= len) return;
   const int slot0 = kv4_first_slot(p, b, t0);
-  const int block = key0 / p.B;
-  // rows before the first key's position attend nothing here
-  int r0 = key0 > pos0 ? (int)((int64_t)(key0 - pos0) * p.G / 8 * 8) : 0;
-  auto picked = [&](int row) {
-    if (!p.kmean) return 0xFFu;
-    const int64_t ui = (int64_t)(slot0 + (row >> p.rshift)) * p.Hkv + h;
-    return __ldg(p.chosen + ui * p.blocks + block) >> (row & (p.R - 1)) & 0xFFu;
-  };
-  while (r0 < rows && !picked(r0)) r0 += 8;
-  if (r0 >= rows) return;
-  const uint8_t* kt = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, b, h, tile);
-  float* acc = p.acc + ((int64_t)b * p.Hkv + h) * p.tiles * kKv4Tile + key0;
-  uint4 wa[4], wb[4];
-  uint32_t pa[4], pb[4];
-  float old[4][2];
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int ta = g * 16 + r, tb = ta + 8;
-    wa[g] = __ldg(reinterpret_cast<const uint4*>(kt + ta * kKv4Row + qd * 16));
-    wb[g] = __ldg(reinterpret_cast<const uint4*>(kt + tb * kKv4Row + qd * 16));
-    pa[g] = __ldg(reinterpret_cast<const uint16_t*>(kt + kKv4Params + ta * 8 + qd * 2));
-    pb[g] = __ldg(reinterpret_cast<const uint16_t*>(kt + kKv4Params + tb * 8 + qd * 2));
-    old[g][0] = acc[ta];
-    old[g][1] = acc[tb];
-  }
-  auto widen = [&](int g, int w, uint32_t (&y)[4], uint32_t (&z)[4]) {
-    const uint32_t xa[4] = {wa[g].x, wa[g].y, wa[g].z, wa[g].w}, xb[4] = {wb[g].x, wb[g].y, wb[g].z, wb[g].w};
-    kv4_pairs(xa[w], kv4_par(__byte_perm(pa[g], 0, 0x1010)), y);
-    kv4_pairs(xb[w], kv4_par(__byte_perm(pb[g], 0, 0x1010)), z);
-  };
-  uint32_t a[HOLD ? 4 : 1][4][8];  // [16 keys][word][pair of the first, of the second eight keys]
-  if constexpr (HOLD) {
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t y[4], z[4];
-        widen(g, w, y, z);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[g][w][2 * j] = y[j], a[g][w][2 * j + 1] = z[j];
-      }
-  }
-  float sum[4][2] = {};
-  for (; r0 < rows; r0 += 8) {
-    const uint32_t pick = picked(r0);
-    if (!pick) continue;
-    uint32_t qf[16];
+  const uint8_t* kt0 = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, b, h, 0);
+  float* acc0 = p.acc + ((int64_t)b * p.Hkv + h) * p.tiles * kKv4Tile;
+
+  // eight rows: fragments, and of this lane's two scale, log2 of the sum and position
+  uint32_t qf[16];
+  float qs[2], le[2];
+  int pos[2];
+  auto rows8 = [&](int r0) {
     const int rr = r0 + r;
     const __nv_bfloat16* row =
         rr < rows ? p.q + ((int64_t)(t0 + rr / p.G) * p.Hq + h * p.G + rr % p.G) * kHeadDim + qd * 32 : nullptr;
     const float s = kv4_query_fragment(row, p.scale_log2, qf);
-    // this lane's two rows: scale, log2 of the sum, last key
-    float qs[2], le[2];
-    int last[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       qs[x] = __shfl_sync(0xFFFFFFFFu, s, (2 * qd + x) * 4);
       const int row2 = r0 + 2 * qd + x;
-      const bool on = row2 < rows && (pick >> (2 * qd + x) & 1u);
-      last[x] = on ? pos0 + row2 / p.G : -1;
+      const bool on = row2 < rows;
+      pos[x] = on ? pos0 + row2 / p.G : -1;
       le[x] = on ? p.lse[(int64_t)(h * p.G + row2 % p.G) * p.total + t0 + row2 / p.G] * 1.4426950408889634f : 0.f;
     }
+  };
+  const bool one = rows <= 8;
+  if (one) rows8(0);
+
+#pragma unroll 1
+  for (int i = 0; i < TILES; ++i) {
+    const int64_t tile = tile0 + i * WARPS;
+    const int key0 = (int)(tile * kKv4Tile);
+    if (key0 >= len) break;
+    const int block = key0 / p.B;
+    auto picked = [&](int row) {
+      if (!p.kmean) return 0xFFu;
+      const int64_t ui = (int64_t)(slot0 + (row >> p.rshift)) * p.Hkv + h;
+      return __ldg(p.chosen + ui * p.blocks + block) >> (row & (p.R - 1)) & 0xFFu;
+    };
+    // rows before the first key's position attend nothing here
+    int r0 = key0 > pos0 ? (int)((int64_t)(key0 - pos0) * p.G / 8 * 8) : 0;
+    while (r0 < rows && !picked(r0)) r0 += 8;
+    if (r0 >= rows) continue;
+    const uint8_t* kt = kt0 + tile * kKv4TileBytes;
+    float* acc = acc0 + key0;
+    uint4 wa[4], wb[4];
+    uint32_t pa[4], pb[4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      float sc[4];
+      const int ta = g * 16 + r, tb = ta + 8;
+      wa[g] = __ldg(reinterpret_cast<const uint4*>(kt + ta * kKv4Row + qd * 16));
+      wb[g] = __ldg(reinterpret_cast<const uint4*>(kt + tb * kKv4Row + qd * 16));
+      pa[g] = __ldg(reinterpret_cast<const uint16_t*>(kt + kKv4Params + ta * 8 + qd * 2));
+      pb[g] = __ldg(reinterpret_cast<const uint16_t*>(kt + kKv4Params + tb * 8 + qd * 2));
+    }
+    // lane 4 r + x: the keys r + 16 x and r + 16 x + 8
+    const float old0 = acc[16 * qd + r], old1 = acc[16 * qd + r + 8];
+    auto widen = [&](int g, int w, const Kv4Par& fa, const Kv4Par& fb, uint32_t (&y)[4], uint32_t (&z)[4]) {
+      const uint32_t xa[4] = {wa[g].x, wa[g].y, wa[g].z, wa[g].w}, xb[4] = {wb[g].x, wb[g].y, wb[g].z, wb[g].w};
+      kv4_pairs(xa[w], fa, y);
+      kv4_pairs(xb[w], fb, z);
+    };
+    uint32_t a[HOLD ? 4 : 1][4][8];  // [16 keys][word][pair of the first, of the second eight keys]
+    if constexpr (HOLD) {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t y[4], z[4];
-        if constexpr (HOLD) {
+      for (int g = 0; g < 4; ++g) {
+        const Kv4Par fa = kv4_par(__byte_perm(pa[g], 0, 0x1010)), fb = kv4_par(__byte_perm(pb[g], 0, 0x1010));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = a[g][w][2 * j], z[j] = a[g][w][2 * j + 1];
-        } else {
-          widen(g, w, y, z);
+        for (int w = 0; w < 4; ++w) {
+          uint32_t y[4], z[4];
+          widen(g, w, fa, fb, y, z);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a[g][w][2 * j] = y[j], a[g][w][2 * j + 1] = z[j];
         }
-        if (w == 0) mma_f16_first(sc, y[0], z[0], y[1], z[1], qf[0], qf[1]);
-        else mma_f16(sc, y[0], z[0], y[1], z[1], qf[4 * w], qf[4 * w + 1]);
-        mma_f16(sc, y[2], z[2], y[3], z[3], qf[4 * w + 2], qf[4 * w + 3]);
-      }
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int key = key0 + g * 16 + r + (x >> 1) * 8;
-        const float e = ex2_approx(fmaf(sc[x], qs[x & 1], -le[x & 1]));
-        if (key <= last[x & 1]) sum[g][x >> 1] += e;
       }
     }
+    float sum[4][2] = {};
+    for (; r0 < rows; r0 += 8) {
+      const uint32_t pick = picked(r0);
+      if (!pick) continue;
+      if (!one) rows8(r0);
+      int last[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) last[x] = pick >> (2 * qd + x) & 1u ? pos[x] : -1;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float sc[4];
+        const Kv4Par fa = kv4_par(__byte_perm(pa[g], 0, 0x1010)), fb = kv4_par(__byte_perm(pb[g], 0, 0x1010));
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t y[4], z[4];
+          if constexpr (HOLD) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = a[g][w][2 * j], z[j] = a[g][w][2 * j + 1];
+          } else {
+            widen(g, w, fa, fb, y, z);
+          }
+          if (w == 0) mma_f16_first(sc, y[0], z[0], y[1], z[1], qf[0], qf[1]);
+          else mma_f16(sc, y[0], z[0], y[1], z[1], qf[4 * w], qf[4 * w + 1]);
+          mma_f16(sc, y[2], z[2], y[3], z[3], qf[4 * w + 2], qf[4 * w + 3]);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int key = key0 + g * 16 + r + (x >> 1) * 8;
+          const float e = ex2_approx(fmaf(sc[x], qs[x & 1], -le[x & 1]));
+          if (key <= last[x & 1]) sum[g][x >> 1] += e;
+        }
+      }
+    }
+    // the four lanes of a key add up; lane qd keeps the keys of 16 qd
+    float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float v = sum[g][x];
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+        if (g == qd) (x ? v1 : v0) = v;
+      }
+    const int at = 16 * qd + r;
+    if (key0 + at < len) acc[at] = old0 + v0;
+    if (key0 + at + 8 < len) acc[at + 8] = old1 + v1;
   }
-#pragma unroll
-  for (int g = 0; g < 4; ++g)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      float v = sum[g][x];
-      v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-      v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
-      const int at = g * 16 + x * 8 + r;
-      if (qd == 0 && key0 + at < len) acc[at] = old[g][x] + v;
-    }
 }
 
 // ------------------------------------------------------------------ pool
@@ -1139,7 +1166,7 @@ constexpr int kKv4PoolThreads = 256;
 // (keys as in the value product of the attention, against ones), the warps'
 // and CTAs' sums meet in a fixed order. Blocks that the sequence has not
 // completed are written as zero.
-__global__ void __launch_bounds__(kKv4PoolThreads) kv4_pool_kernel(Kv4PoolParams p) {
+__global__ void __launch_bounds__(kKv4PoolThreads, 2) kv4_pool_kernel(Kv4PoolParams p) {
   grid_dependency_sync();
   constexpr int WARPS = kKv4PoolThreads / 32;
   __shared__ float sums[WARPS][kHeadDim];
@@ -1158,7 +1185,7 @@ __global__ void __launch_bounds__(kKv4PoolThreads) kv4_pool_kernel(Kv4PoolParams
   const uint8_t* kt = p.kv4 + kv4_tile_off(p.tiles, p.heads, b, h, 0);
   const int groups = p.B / 16, g0 = (int)((int64_t)j * groups);
   float o[8][4] = {};
-#pragma unroll 2
+#pragma unroll 4
   for (int g = rank * WARPS + warp; g < groups; g += csize * WARPS) {
     const int64_t t = (int64_t)(g0 + g) * 16;
     const uint8_t* tile = kt + t / kKv4Tile * kKv4TileBytes;

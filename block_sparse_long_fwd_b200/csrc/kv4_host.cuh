@@ -133,10 +133,8 @@ int moba_kv4_append(const void* k, const void* v, int64_t total, const int32_t* 
   p.heads = heads_kv;
   p.kv4 = static_cast<uint8_t*>(kv4);
   p.acc = acc;
-  const int64_t threads = total * heads_kv * 4;
-  if (threads / moba::kKv4AppendThreads >= INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
-  launch_chained(moba::kv4_append_kernel,
-                 dim3((unsigned)((threads + moba::kKv4AppendThreads - 1) / moba::kKv4AppendThreads)),
+  const int per = moba::kKv4AppendThreads / 4;
+  launch_chained(moba::kv4_append_kernel, dim3((unsigned)((total + per - 1) / per), heads_kv),
                  dim3(moba::kKv4AppendThreads), 0, stream, p);
   MOBA_CUDA(cudaGetLastError());
   return finish_call(MOBA_OK, stream);
@@ -167,9 +165,9 @@ int moba_kv4_load(const void* kv4, const int32_t* lengths, const int32_t* first,
   p.heads = heads_kv;
   p.k = static_cast<__nv_bfloat16*>(k);
   p.v = static_cast<__nv_bfloat16*>(v);
-  const int64_t per = moba::kKv4LoadThreads / 16 * moba::kKv4LoadRows, ctas = (n * batch * heads_kv + per - 1) / per;
-  if (ctas > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
-  launch_chained(moba::kv4_load_kernel, dim3((unsigned)ctas), dim3(moba::kKv4LoadThreads), 0, stream, p);
+  const int per = moba::kKv4LoadThreads / 16 * moba::kKv4LoadRows;
+  launch_chained(moba::kv4_load_kernel, dim3((unsigned)((n + per - 1) / per), heads_kv, batch),
+                 dim3(moba::kKv4LoadThreads), 0, stream, p);
   MOBA_CUDA(cudaGetLastError());
   return finish_call(MOBA_OK, stream);
 }
@@ -306,7 +304,7 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
       launch_chained(moba::kv4_chunk_weight_kernel, dim3((unsigned)((capacity + 255) / 256), batch * heads_kv),
                      dim3(moba::kKv4ColThreads), moba::kKv4ColSmemBytes, st, p);
     } else if (acc) {
-      const int per = moba::kKv4WeightThreads / 32;
+      const int per = moba::kKv4WeightThreads / 32 * (few ? moba::kKv4WeightTiles : 1);
       launch_chained(few ? moba::kv4_weight_kernel<false> : moba::kv4_weight_kernel<true>,
                      dim3((unsigned)((p.tiles + per - 1) / per), batch * heads_kv), dim3(moba::kKv4WeightThreads), 0,
                      st, p);
