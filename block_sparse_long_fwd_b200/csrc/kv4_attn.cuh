@@ -45,7 +45,7 @@ struct Kv4AttnParams {
   float* lse;                   // [Hq][total]
   // scratch
   Kv4Unit* units;               // [slots * Hkv]
-  int64_t* before;              // [slots * Hkv + 1]: items of the units before
+  int* before;                  // [slots * Hkv + 1]: items of the units before
   uint2* list;                  // [slots * Hkv][list_cap]: (block, rows that chose it), ascending
   uint32_t* chosen;             // [slots * Hkv][blocks]: rows of the unit that chose the block
   double* scores;               // [clusters][R][means]
@@ -287,11 +287,11 @@ __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams
 
 // ------------------------------------------------------------------ plan
 
-// Items of a part's range: the same for all but the last that has any.
-__device__ __forceinline__ int64_t kv4_quota(const Kv4AttnParams& p, int64_t all) {
-  const int n = p.ctas * p.parts;
-  if (all < (1ll << 31) - n) return ((uint32_t)all + n - 1) / n;  // a 64-bit division costs several times more
-  return (all + n - 1) / n;
+// Items of a part's range: the same for all but the last that has any. (Items
+// fit 31 bits: the host sees to it.)
+__device__ __forceinline__ int kv4_quota(const Kv4AttnParams& p, int all) {
+  const uint32_t n = p.ctas * p.parts;
+  return (int)(((uint32_t)all + n - 1) / n);
 }
 
 // Where each part's range begins (a part is a warp, or the CTA): every CTA scans all units' tiles for itself
@@ -317,14 +317,14 @@ struct Kv4Range {
 template <int THREADS, int PARTS>
 __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* copy, int room) {
   constexpr int WARPS = THREADS / 32;
-  __shared__ int64_t warp_sums[WARPS];
+  __shared__ int warp_sums[WARPS];
   __shared__ int2 s_start[PARTS];
   __shared__ Kv4Unit s_kept[kKv4Kept];
   __shared__ int s_first;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
   const int nu = p.slots * p.Hkv;
   const int32_t *cu = p.cu, *lengths = p.lengths;
-  for (int i = tid; i < kKv4Kept; i += THREADS) s_kept[i].tiles = 0;  // units without tiles are not kept
+  if (tid < kKv4Kept) s_kept[tid].tiles = 0;  // units without tiles are not kept
   if (!p.kmean && 2 * p.batch + 1 <= room) {
     for (int i = tid; i < p.batch; i += THREADS) copy[i] = p.lengths[i];
     lengths = copy;
@@ -334,76 +334,72 @@ __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* co
     }
     __syncthreads();
   }
-  auto unit = [&](int ui) {
-    Kv4Unit u = {};
-    if (ui >= nu) return u;
-    if (p.kmean) return p.units[ui];
-    u = kv4_unit_of(p, cu, lengths, ui / p.Hkv, ui % p.Hkv);
-    const int last = u.rows ? kv4_last_pos(p, u) : -1;
-    u.tiles = last < 0 ? 0 : last / kKv4Tile + 1;
-    return u;
-  };
-  // neighbouring units for each thread, found again below where there are several
+  // Neighbouring units for each thread, in three sweeps: their items; the unit in which the CTA's range begins; what
+  // the range touches. (One piece of code: this runs once, and what it costs is fetching its instructions.)
   const int mine = (nu + THREADS - 1) / THREADS, u0 = tid * mine;
-  Kv4Unit u = unit(u0);
-  int64_t x = kv4_items(p, u);
-  for (int i = 1; i < mine; ++i) x += kv4_items(p, unit(u0 + i));
-  int64_t s = x;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, d);
-    if (lane >= d) s += y;
-  }
-  if (lane == 31) warp_sums[warp] = s;
-  __syncthreads();
-  int64_t before = s - x, all = 0;
-#pragma unroll
-  for (int i = 0; i < WARPS; ++i) {
-    const int64_t y = warp_sums[i];
-    if (i < warp) before += y;
-    all += y;
-  }
-  const int64_t quota = kv4_quota(p, all);
-  const int64_t lo = min(cta * PARTS * quota, all), hi = min(lo + PARTS * quota, all);
-  if (cta == 0 && tid == 0) p.before[nu] = all;
-  const bool touches = before < hi && before + x > lo;
-  if (touches && before <= lo) {
-    int64_t at = before;
+  Kv4Unit u = {};
+  int x = 0, before = 0, all = 0, quota = 0, lo = 0, hi = 0;
+#pragma unroll 1
+  for (int sweep = 0; sweep < 3; ++sweep) {
+    int at = before;
+#pragma unroll 1
     for (int i = 0; i < mine; ++i) {
-      const int n = kv4_items(p, mine == 1 ? u : unit(u0 + i));
-      if (at <= lo && lo < at + n) s_first = u0 + i;
-      at += n;
-    }
-  }
-  __syncthreads();
-  if (touches || cta == 0) {
-    int64_t at = before;
-    for (int i = 0; i < mine && u0 + i < nu; ++i) {
       const int ui = u0 + i;
-      if (mine > 1) u = unit(ui);
-      const int n = kv4_items(p, u);
-      if (n > 0 && at < hi && at + n > lo) {
-        if (ui - s_first < kKv4Kept) s_kept[ui - s_first] = u;
-        p.before[ui] = at;
-        for (int w = 0; w < PARTS; ++w) {
-          const int64_t y = lo + w * quota;
-          if (y >= at && y < at + n) s_start[w] = make_int2(ui, (int)(y - at));
+      if (ui >= nu) break;
+      if (sweep == 0 || mine > 1) {
+        if (p.kmean) {
+          u = p.units[ui];
+        } else {
+          u = kv4_unit_of(p, cu, lengths, ui / p.Hkv, ui % p.Hkv);
+          const int last = u.rows ? kv4_last_pos(p, u) : -1;
+          u.tiles = last < 0 ? 0 : last / kKv4Tile + 1;
         }
-        if (!p.kmean) p.units[ui] = u;
-      } else if (!p.kmean && cta == 0 && n == 0) {
-        p.units[ui] = u;
+      }
+      const int n = kv4_items(p, u);
+      if (sweep == 1 && at <= lo && lo < at + n) s_first = ui;
+      if (sweep == 2) {
+        const bool touches = n > 0 && at < hi && at + n > lo;
+        if (touches) {
+          if (ui - s_first < kKv4Kept) s_kept[ui - s_first] = u;
+          p.before[ui] = at;
+#pragma unroll 1
+          for (int w = 0; w < PARTS; ++w) {
+            const int y = lo + w * quota;
+            if (y >= at && y < at + n) s_start[w] = make_int2(ui, y - at);
+          }
+        }
+        if (!p.kmean && (touches || (cta == 0 && n == 0))) p.units[ui] = u;
       }
       at += n;
     }
+    if (sweep == 0) {
+      x = at;
+      int s = x;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, s, d);
+        if (lane >= d) s += y;
+      }
+      if (lane == 31) warp_sums[warp] = s;
+      __syncthreads();
+      const int y = lane < WARPS ? warp_sums[lane] : 0;
+      before = s - x + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? y : 0);
+      all = __reduce_add_sync(0xFFFFFFFFu, y);
+      quota = kv4_quota(p, all);
+      lo = (int)min((int64_t)cta * PARTS * quota, (int64_t)all);
+      hi = min(lo + PARTS * quota, all);
+      if (cta == 0 && tid == 0) p.before[nu] = all;
+    } else {
+      __syncthreads();
+    }
   }
-  __syncthreads();
   Kv4Range g;
   const int part = PARTS == 1 ? 0 : warp;
   g.kept = s_kept;
   g.units = p.units;
   g.first = s_first;
   g.any = hi > lo;
-  g.n = (int)max((int64_t)0, min(quota, hi - lo - part * quota));
+  g.n = max(0, min(quota, hi - lo - part * quota));
   g.unit = g.n ? s_start[part].x : 0;
   g.off = g.n ? s_start[part].y : 0;
   return g;
@@ -962,10 +958,10 @@ __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams
   if (row >= u.rows) return;
   int c0 = 0, c1 = -1;
   if (u.tiles) {
-    const int64_t all = p.before[p.slots * p.Hkv], x = p.before[ui];
-    const int64_t per_cta = kv4_quota(p, all) * p.parts;
-    c0 = (int)(x / per_cta);
-    c1 = (int)((x + kv4_items(p, u) - 1) / per_cta);
+    const int all = p.before[p.slots * p.Hkv], x = p.before[ui];
+    const int per_cta = kv4_quota(p, all) * p.parts;
+    c0 = x / per_cta;
+    c1 = (x + kv4_items(p, u) - 1) / per_cta;
     if (c0 == c1) return;  // written by the CTA itself
   }
   const int64_t per = p.R * 130;
@@ -1162,11 +1158,15 @@ struct Kv4PoolParams {
 constexpr int kKv4PoolThreads = 256;
 
 // A cluster of CTAs per (block, head, sequence), a part of the block's tokens
-// each, 16 tokens of each warp at a time: the tensor core sums them in fp32
-// (keys as in the value product of the attention, against ones), the warps'
-// and CTAs' sums meet in a fixed order. Blocks that the sequence has not
-// completed are written as zero.
-__global__ void __launch_bounds__(kKv4PoolThreads, 2) kv4_pool_kernel(Kv4PoolParams p) {
+// each, 16 tokens of each warp at a time. The tensor core sums in fp32: codes,
+// as they stand in a word, are fp16 subnormals (a nibble at bit 0 is c 2^-24,
+// at bit 4 c 2^-20), so a mask is all that they need; they meet the scales of
+// the four groups in four columns, of which the channel's own is kept, and the
+// scales times zero points are summed by one product more and taken off at the
+// end. (Widened to s (c - z) first, as the attention needs them, 128K tokens
+// of 8 heads took 35 us.) The warps' and CTAs' sums meet in a fixed order.
+// Blocks that the sequence has not completed are written as zero.
+__global__ void __launch_bounds__(kKv4PoolThreads, 3) kv4_pool_kernel(Kv4PoolParams p) {
   grid_dependency_sync();
   constexpr int WARPS = kKv4PoolThreads / 32;
   __shared__ float sums[WARPS][kHeadDim];
@@ -1184,14 +1184,14 @@ __global__ void __launch_bounds__(kKv4PoolThreads, 2) kv4_pool_kernel(Kv4PoolPar
   }
   const uint8_t* kt = p.kv4 + kv4_tile_off(p.tiles, p.heads, b, h, 0);
   const int groups = p.B / 16, g0 = (int)((int64_t)j * groups);
-  float o[8][4] = {};
+  float o[8][4] = {}, oz[4] = {};
 #pragma unroll 4
   for (int g = rank * WARPS + warp; g < groups; g += csize * WARPS) {
     const int64_t t = (int64_t)(g0 + g) * 16;
     const uint8_t* tile = kt + t / kKv4Tile * kKv4TileBytes;
     const int at = (int)(t % kKv4Tile) + 2 * qd;
     uint2 w[2][2];
-    Kv4Par fp[2];
+    uint32_t s[2], sz[2];  // scales, and scales times zero points, of group r % 4 for the lane's tokens
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
       uint32_t pp[2];
@@ -1199,28 +1199,43 @@ __global__ void __launch_bounds__(kKv4PoolThreads, 2) kv4_pool_kernel(Kv4PoolPar
       for (int e = 0; e < 2; ++e) {
         const int tok = at + 8 * f + e;
         w[f][e] = __ldg(reinterpret_cast<const uint2*>(tile + tok * kKv4Row + r * 8));
-        pp[e] = __ldg(reinterpret_cast<const uint16_t*>(tile + kKv4Params + tok * 8 + (r >> 1) * 2));
+        pp[e] = __ldg(reinterpret_cast<const uint16_t*>(tile + kKv4Params + tok * 8 + (r & 3) * 2));
       }
-      fp[f] = kv4_par(__byte_perm(pp[0], pp[1], 0x5410));
+      const uint32_t par = __byte_perm(pp[0], pp[1], 0x5410);
+      s[f] = par & 0x7F807F80u;
+      sz[f] = h2_mul(h2_sub(and_or(par, 0x000F000Fu, 0x64006400u), 0x64006400u), s[f]);
     }
+    mma_f16(oz, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, sz[0], sz[1]);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      uint32_t a[2][2][4];  // [channel parity][keys 0-7, 8-15][nibble]
+      uint32_t a[2][2][4];  // [channel parity][tokens 0-7, 8-15][nibble]
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
         const uint32_t x0 = x ? w[f][0].y : w[f][0].x, x1 = x ? w[f][1].y : w[f][1].x;
-        kv4_pairs(__byte_perm(x0, x1, 0x5410), fp[f], a[0][f]);
-        kv4_pairs(__byte_perm(x0, x1, 0x7632), fp[f], a[1][f]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t u = __byte_perm(x0, x1, c ? 0x7632 : 0x5410), v = u >> 8;
+          a[c][f][0] = u & 0x000F000Fu;
+          a[c][f][1] = u & 0x00F000F0u;
+          a[c][f][2] = v & 0x000F000Fu;
+          a[c][f][3] = v & 0x00F000F0u;
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        mma_f16(o[x * 4 + i], a[0][0][i], a[1][0][i], a[0][1][i], a[1][1][i], 0x3C003C00u, 0x3C003C00u);
+      for (int i = 0; i < 4; ++i) mma_f16(o[x * 4 + i], a[0][0][i], a[1][0][i], a[0][1][i], a[1][1][i], s[0], s[1]);
     }
   }
-  // every column holds the sums: channels 16 r + 2 mt and the next
-  if (qd == 0)
+  // channels 16 r .. are of group r / 2: the lane that holds this column has their sums
+  if (qd == r >> 2) {
+    const int c = r >> 1 & 1;
+    const float z = c ? oz[1] : oz[0];
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) sums[warp][16 * r + 2 * mt] = o[mt][0], sums[warp][16 * r + 2 * mt + 1] = o[mt][2];
+    for (int mt = 0; mt < 8; ++mt) {
+      const float unit = mt & 1 ? 1048576.f : 16777216.f;  // 2^20, 2^24
+      sums[warp][16 * r + 2 * mt] = fmaf(c ? o[mt][1] : o[mt][0], unit, -z);
+      sums[warp][16 * r + 2 * mt + 1] = fmaf(c ? o[mt][3] : o[mt][2], unit, -z);
+    }
+  }
   __syncthreads();
   if (threadIdx.x < kHeadDim) {
     float s = 0.f;
@@ -1231,7 +1246,7 @@ __global__ void __launch_bounds__(kKv4PoolThreads, 2) kv4_pool_kernel(Kv4PoolPar
   if (rank == 0 && threadIdx.x < kHeadDim) {
     float s = 0.f;
     for (uint32_t c = 0; c < csize; ++c) s += __uint_as_float(kv4_remote_ld(&total[threadIdx.x], c));
-    out[threadIdx.x] = s * 64.f / (float)p.B;
+    out[threadIdx.x] = s / (float)p.B;
   }
   kv4_cluster_sync();  // no CTA leaves while its sums may still be read
 }

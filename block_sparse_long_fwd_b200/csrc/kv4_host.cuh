@@ -194,9 +194,9 @@ int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch, int heads_
   p.blocks = (int)(capacity / block_size);
   p.kmean = kmean;
   if (p.blocks) {
-    // up to 8 CTAs share a block while there are too few blocks for two CTAs an SM
+    // up to 8 CTAs share a block while there are too few blocks for four CTAs an SM
     int csize = 1;
-    while (csize < 8 && (int64_t)p.blocks * heads_kv * batch * csize < 2 * dev.sms && block_size / csize > 256) csize *= 2;
+    while (csize < 8 && (int64_t)p.blocks * heads_kv * batch * csize < 4 * dev.sms && block_size / csize > 256) csize *= 2;
     if ((int64_t)p.blocks * csize > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many blocks");
     launch_clusters(moba::kv4_pool_kernel, dim3(p.blocks * csize, heads_kv, batch), dim3(moba::kKv4PoolThreads), 0,
                     csize, stream, p);
@@ -264,13 +264,16 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   p.parts = few ? moba::Kv4Few::WARPS : chunk ? 1 : moba::Kv4Many::WARPS;
   p.steps = chunk ? 1 : 0;
   const int64_t nu = slots * heads_kv;
+  // items (half tiles, or steps of two tiles) are counted in 31 bits, and so are the starts of all ranges
+  const int64_t items = chunk ? (p.tiles + 1) / 2 : 2 * p.tiles;
+  if (nu * items > INT32_MAX - 4096) return fail(MOBA_ERR_UNSUPPORTED, "too many (row, key) tiles");
   p.list_cap = kmean ? (int)std::min<int64_t>(p.blocks, (int64_t)p.R * topk) : 0;
   // the gate: up to 8 CTAs share a unit's scores while there are few units
   int csize = 1;
   while (csize < 8 && nu * csize * 2 <= dev.sms) csize *= 2;
   const int64_t clusters = std::min<int64_t>(nu, 4 * dev.sms / csize);
   Carve c;
-  const size_t o_units = c.take((size_t)nu * sizeof(moba::Kv4Unit)), o_before = c.take((size_t)(nu + 1) * 8);
+  const size_t o_units = c.take((size_t)nu * sizeof(moba::Kv4Unit)), o_before = c.take((size_t)(nu + 1) * 4);
   const size_t o_list = c.take((size_t)nu * p.list_cap * 8);
   const size_t o_chosen = c.take(acc ? (size_t)nu * p.blocks * 4 : 0);
   const size_t o_scores = c.take((size_t)clusters * p.R * p.means * 8);
@@ -281,7 +284,7 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
     p.qtiles = ws + o_qtiles;
     p.qscale = reinterpret_cast<float*>(ws + o_qscale);
     p.units = reinterpret_cast<moba::Kv4Unit*>(ws + o_units);
-    p.before = reinterpret_cast<int64_t*>(ws + o_before);
+    p.before = reinterpret_cast<int*>(ws + o_before);
     p.list = reinterpret_cast<uint2*>(ws + o_list);
     p.chosen = reinterpret_cast<uint32_t*>(ws + o_chosen);
     p.scores = reinterpret_cast<double*>(ws + o_scores);
