@@ -318,11 +318,13 @@ template <int THREADS, int PARTS>
 __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* copy, int room) {
   constexpr int WARPS = THREADS / 32;
   __shared__ int warp_sums[WARPS];
-  __shared__ int2 s_start[PARTS];
   __shared__ Kv4Unit s_kept[kKv4Kept];
+  __shared__ int s_at[kKv4Kept];  // items before a kept unit
   __shared__ int s_first;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
   const int nu = p.slots * p.Hkv;
+  // without a gate the units of a slot differ in their head alone
+  const int heads = p.kmean ? 1 : p.Hkv, entries = nu / heads;
   const int32_t *cu = p.cu, *lengths = p.lengths;
   if (tid < kKv4Kept) s_kept[tid].tiles = 0;  // units without tiles are not kept
   if (!p.kmean && 2 * p.batch + 1 <= room) {
@@ -334,43 +336,52 @@ __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* co
     }
     __syncthreads();
   }
-  // Neighbouring units for each thread, in three sweeps: their items; the unit in which the CTA's range begins; what
-  // the range touches. (One piece of code: this runs once, and what it costs is fetching its instructions.)
-  const int mine = (nu + THREADS - 1) / THREADS, u0 = tid * mine;
+  // Neighbouring entries for each thread, in three sweeps: their items; the unit in which the CTA's range begins; what
+  // the range touches. (One piece of code: this runs once, and much of what it costs is fetching its instructions.)
+  const int mine = (entries + THREADS - 1) / THREADS, e0 = tid * mine;
   Kv4Unit u = {};
   int x = 0, before = 0, all = 0, quota = 0, lo = 0, hi = 0;
 #pragma unroll 1
   for (int sweep = 0; sweep < 3; ++sweep) {
     int at = before;
+    const bool here = sweep == 0 || (before <= hi && before + x >= lo);
 #pragma unroll 1
-    for (int i = 0; i < mine; ++i) {
-      const int ui = u0 + i;
-      if (ui >= nu) break;
+    for (int i = 0; here && i < mine; ++i) {
+      const int e = e0 + i;
+      if (e >= entries) break;
       if (sweep == 0 || mine > 1) {
         if (p.kmean) {
-          u = p.units[ui];
+          u = p.units[e];
         } else {
-          u = kv4_unit_of(p, cu, lengths, ui / p.Hkv, ui % p.Hkv);
+          u = kv4_unit_of(p, cu, lengths, e, 0);
           const int last = u.rows ? kv4_last_pos(p, u) : -1;
           u.tiles = last < 0 ? 0 : last / kKv4Tile + 1;
         }
       }
       const int n = kv4_items(p, u);
-      if (sweep == 1 && at <= lo && lo < at + n) s_first = ui;
-      if (sweep == 2) {
-        const bool touches = n > 0 && at < hi && at + n > lo;
-        if (touches) {
-          if (ui - s_first < kKv4Kept) s_kept[ui - s_first] = u;
-          p.before[ui] = at;
+      if (sweep == 0 && n == 0 && cta == 0 && !p.kmean)
+        for (int h = 0; h < heads; ++h) u.h = h, p.units[e * heads + h] = u;
+      if (sweep > 0) {
+        int y = at;
 #pragma unroll 1
-          for (int w = 0; w < PARTS; ++w) {
-            const int y = lo + w * quota;
-            if (y >= at && y < at + n) s_start[w] = make_int2(ui, y - at);
+        for (int h = 0; h < heads; ++h, y += n) {
+          if (y >= hi || (n == 0 ? y < lo : y + n <= lo)) continue;
+          const int ui = e * heads + h;
+          if (n == 0) {  // the walk through the range passes it
+            if (!p.kmean && sweep == 2) u.h = h, p.units[ui] = u;
+            continue;
           }
+          if (sweep == 1) {
+            if (y <= lo) s_first = ui;
+            continue;
+          }
+          if (!p.kmean) u.h = h, p.units[ui] = u;
+          p.before[ui] = y;
+          const int k = ui - s_first;
+          if (k < kKv4Kept) s_kept[k] = u, s_at[k] = y;
         }
-        if (!p.kmean && (touches || (cta == 0 && n == 0))) p.units[ui] = u;
       }
-      at += n;
+      at += n * heads;
     }
     if (sweep == 0) {
       x = at;
@@ -400,8 +411,26 @@ __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* co
   g.first = s_first;
   g.any = hi > lo;
   g.n = max(0, min(quota, hi - lo - part * quota));
-  g.unit = g.n ? s_start[part].x : 0;
-  g.off = g.n ? s_start[part].y : 0;
+  g.unit = g.off = 0;
+  if (g.n) {
+    // the unit that this part begins in: among the kept ones, a lane each, or further on
+    const int start = lo + part * quota;
+    const bool in = lane < kKv4Kept && s_kept[lane].tiles && s_at[lane] <= start &&
+                    start < s_at[lane] + kv4_items(p, s_kept[lane]);
+    const uint32_t found = __ballot_sync(0xFFFFFFFFu, in);
+    if (found) {
+      g.unit = g.first + __ffs(found) - 1;
+      g.off = start - s_at[__ffs(found) - 1];
+    } else {
+      int ui = g.first + kKv4Kept;
+      for (;; ++ui) {  // the range reaches this unit: it ends there
+        const int n = kv4_items(p, p.units[ui]);
+        if (n && p.before[ui] <= start && start < p.before[ui] + n) break;
+      }
+      g.unit = ui;
+      g.off = start - p.before[ui];
+    }
+  }
   return g;
 }
 
@@ -1155,7 +1184,7 @@ struct Kv4PoolParams {
   float* kmean;          // [batch][heads][blocks][128]
 };
 
-constexpr int kKv4PoolThreads = 256;
+constexpr int kKv4PoolThreads = 512;  // at most
 
 // A cluster of CTAs per (block, head, sequence), a part of the block's tokens
 // each, 16 tokens of each warp at a time. The tensor core sums in fp32: codes,
@@ -1166,10 +1195,10 @@ constexpr int kKv4PoolThreads = 256;
 // end. (Widened to s (c - z) first, as the attention needs them, 128K tokens
 // of 8 heads took 35 us.) The warps' and CTAs' sums meet in a fixed order.
 // Blocks that the sequence has not completed are written as zero.
-__global__ void __launch_bounds__(kKv4PoolThreads, 3) kv4_pool_kernel(Kv4PoolParams p) {
+__global__ void __launch_bounds__(kKv4PoolThreads, 2) kv4_pool_kernel(Kv4PoolParams p) {
   grid_dependency_sync();
-  constexpr int WARPS = kKv4PoolThreads / 32;
-  __shared__ float sums[WARPS][kHeadDim];
+  const int WARPS = blockDim.x / 32;
+  __shared__ float sums[kKv4PoolThreads / 32][kHeadDim];
   __shared__ uint32_t total[kHeadDim];  // fp32 bits
   uint32_t rank, csize;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -1185,7 +1214,7 @@ __global__ void __launch_bounds__(kKv4PoolThreads, 3) kv4_pool_kernel(Kv4PoolPar
   const uint8_t* kt = p.kv4 + kv4_tile_off(p.tiles, p.heads, b, h, 0);
   const int groups = p.B / 16, g0 = (int)((int64_t)j * groups);
   float o[8][4] = {}, oz[4] = {};
-#pragma unroll 4
+#pragma unroll 2
   for (int g = rank * WARPS + warp; g < groups; g += csize * WARPS) {
     const int64_t t = (int64_t)(g0 + g) * 16;
     const uint8_t* tile = kt + t / kKv4Tile * kKv4TileBytes;

@@ -194,12 +194,13 @@ int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch, int heads_
   p.blocks = (int)(capacity / block_size);
   p.kmean = kmean;
   if (p.blocks) {
-    // up to 8 CTAs share a block while there are too few blocks for four CTAs an SM
+    // a warp for 64 tokens, 4 to 16 of them; up to 8 CTAs share a large block while there are SMs for them
+    const int threads = std::min(moba::kKv4PoolThreads, std::max(moba::kHeadDim, block_size / 64 * 32));
     int csize = 1;
-    while (csize < 8 && (int64_t)p.blocks * heads_kv * batch * csize < 4 * dev.sms && block_size / csize > 256) csize *= 2;
+    while (csize < 8 && (int64_t)p.blocks * heads_kv * batch * csize * 2 <= dev.sms && block_size / csize > 2048) csize *= 2;
     if ((int64_t)p.blocks * csize > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many blocks");
-    launch_clusters(moba::kv4_pool_kernel, dim3(p.blocks * csize, heads_kv, batch), dim3(moba::kKv4PoolThreads), 0,
-                    csize, stream, p);
+    launch_clusters(moba::kv4_pool_kernel, dim3(p.blocks * csize, heads_kv, batch), dim3(threads), 0, csize,
+                    stream, p);
     MOBA_CUDA(cudaGetLastError());
   }
   return finish_call(MOBA_OK, stream);

@@ -273,6 +273,14 @@ def test_attention_over_every_key(hkv, G, lengths, news, acc):
     attend_case(hkv, G, lengths, news, acc=acc, seed=len(lengths) + G)
 
 
+def test_many_short_sequences_with_empty_ones_between():
+    # far more units than CTAs, most of them without tiles: every range walks over several, and past the kept ones
+    rng = np.random.default_rng(2)
+    lengths = [int(x) for x in np.where(rng.random(700) < 0.3, rng.integers(1, 90, 700), 0)]
+    attend_case(1, 2, lengths, [1 if L else 0 for L in lengths], acc=False, seed=1, cap=128)
+    attend_case(1, 2, lengths, [1] * 700, acc=False, seed=1, cap=128)  # a query without keys for each empty one
+
+
 SPARSE = [
     # hkv, G, lengths, new tokens, block, topk
     (1, 1, [1], [1], 128, 2),
