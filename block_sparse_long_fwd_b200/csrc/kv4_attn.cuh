@@ -772,6 +772,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
               if (key > last[nt][x & 1] || !(rows_a >> row & 1u)) sc[g][nt][x] = -INFINITY;
             }
       }
+      // the first values' codes are on their way while the weights are found
+      auto values = [&](int g, uint2 (&w)[2][2], uint32_t (&pp)[2]) {
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int t0 = ve0 + g * 16 + f * 8, t1 = ve1 + g * 16 + f * 8;
+          w[f][0] = *reinterpret_cast<const uint2*>(vt + t0 * kKv4Row + vchunk);
+          w[f][1] = *reinterpret_cast<const uint2*>(vt + t1 * kKv4Row + vchunk);
+          const uint32_t p0 = *reinterpret_cast<const uint16_t*>(vt + kKv4HalfParams + t0 * 8 + (r >> 1) * 2);
+          const uint32_t p1 = *reinterpret_cast<const uint16_t*>(vt + kKv4HalfParams + t1 * 8 + (r >> 1) * 2);
+          pp[f] = __byte_perm(p0, p1, 0x5410);
+        }
+      };
+      uint2 w[2][2];
+      uint32_t vp[2];
+      values(0, w, vp);
       // weights 2^(score - m). The reference m moves when a score exceeds it by more than 15, to 12 below
       // the largest: weights then lie under 2^15, which fp16 holds, and end 2^-37 below the largest
       uint32_t pf[NT][2][2];
@@ -821,18 +836,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
       // O^T += V^T P^T: channels x rows
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        uint2 w[2][2];
         Kv4Par fp[2];
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const int t0 = ve0 + g * 16 + f * 8, t1 = ve1 + g * 16 + f * 8;
-          w[f][0] = *reinterpret_cast<const uint2*>(vt + t0 * kKv4Row + vchunk);
-          w[f][1] = *reinterpret_cast<const uint2*>(vt + t1 * kKv4Row + vchunk);
-          const uint32_t p0 = *reinterpret_cast<const uint16_t*>(vt + kKv4HalfParams + t0 * 8 + (r >> 1) * 2);
-          const uint32_t p1 = *reinterpret_cast<const uint16_t*>(vt + kKv4HalfParams + t1 * 8 + (r >> 1) * 2);
-          fp[f] = kv4_par(__byte_perm(p0, p1, 0x5410));
-        }
-        if (g == 1) __syncwarp();  // the half tile is in registers: the next but one may take its place
+        for (int f = 0; f < 2; ++f) fp[f] = kv4_par(vp[f]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t a[2][2][4];  // [channel parity][keys 0-7, 8-15][nibble]
@@ -848,7 +854,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
             for (int nt = 0; nt < NT; ++nt)
               mma_f16(o[nt][h * 4 + j], a[0][0][j], a[1][0][j], a[0][1][j], a[1][1][j], pf[nt][g][0], pf[nt][g][1]);
         }
+        if (g == 0) values(1, w, vp);
       }
+      __syncwarp();  // the half tile is in registers: the next but one may take its place
       issue(d);
     }
 
