@@ -49,6 +49,7 @@ struct Kv4AttnParams {
   uint2* list;                  // [slots * Hkv][list_cap]: (block, rows that chose it), ascending
   uint32_t* chosen;             // [slots * Hkv][blocks]: rows of the unit that chose the block
   double* scores;               // [clusters][R][means]
+  float* seen;                  // or null: [items][4][32][2] log2 scores, of each half tile's keys and two rows
   float* part;                  // [2 * ctas][R * 130]: O, then m and l
   int list_cap, ctas;
   int parts;                    // ranges of a CTA
@@ -310,6 +311,7 @@ struct Kv4Range {
   int first;      // unit of kept[0]
   __device__ __forceinline__ Kv4Unit at(int ui) const { return ui - first < kKv4Kept ? kept[ui - first] : units[ui]; }
   int n;          // items of this part
+  int item;       // the first of them, of all
   int unit, off;  // its first unit, items of it that lie before the range
   bool any;       // the CTA has some
 };
@@ -411,6 +413,7 @@ __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* co
   g.first = s_first;
   g.any = hi > lo;
   g.n = max(0, min(quota, hi - lo - part * quota));
+  g.item = lo + part * quota;
   g.unit = g.off = 0;
   if (g.n) {
     // the unit that this part begins in: among the kept ones, a lane each, or further on
@@ -771,6 +774,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
               const uint32_t row = nt * 8 + 2 * qd + (x & 1);
               if (key > last[nt][x & 1] || !(rows_a >> row & 1u)) sc[g][nt][x] = -INFINITY;
             }
+      }
+      if constexpr (NT == 1) {
+        if (p.seen && 2 * qd < u.rows) {  // for the accumulated weights: the lane's two rows of its keys
+          float2* to = reinterpret_cast<float2*>(p.seen) + ((int64_t)(range.item + k) * 4 + qd) * kKv4HalfTok + tok0;
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint64_t y = f2_fma(f2_pack(sc[g][0][2 * x], sc[g][0][2 * x + 1]), qs[0], 0);
+              to[g * 16 + x * 8] = make_float2(f2_lo(y), f2_hi(y));
+            }
+        }
       }
       // the first values' codes are on their way while the weights are found
       auto values = [&](int g, uint2 (&w)[2][2], uint32_t (&pp)[2]) {
@@ -1180,6 +1195,71 @@ __global__ void __launch_bounds__(kKv4WeightThreads, HOLD ? 2 : 5) kv4_weight_ke
     if (key0 + at < len) acc[at] = old0 + v0;
     if (key0 + at + 8 < len) acc[at + 8] = old1 + v1;
   }
+}
+
+constexpr int kKv4SeenThreads = 128, kKv4SeenKeys = 1024;
+
+// The same from the scores that the attention has left: 4 bytes written and
+// read a row and key, against 72 read again and widened a key (at 128K tokens of
+// 8 heads, 4 rows each: 8 against 28 us, and 1 us more in the attention). A warp takes 256 keys
+// of a kv head, a lane a key, over the units of the sequence in order.
+__global__ void __launch_bounds__(kKv4SeenThreads) kv4_seen_kernel(Kv4AttnParams p) {
+  grid_dependency_sync();
+  const int lane = threadIdx.x & 31, b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
+  const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
+  const int first = blockIdx.x * kKv4SeenKeys + (threadIdx.x >> 5) * (kKv4SeenKeys / (kKv4SeenThreads / 32));
+  int t0;
+  const int n = kv4_queries(p, p.cu, b, &t0);
+  if (n == 0 || first >= len) return;
+  constexpr int PARTS = kKv4SeenKeys / (kKv4SeenThreads / 32) / kKv4HalfTok;
+  float sum[PARTS] = {};
+  const int slot0 = kv4_first_slot(p, b, t0), tpb = p.B / kKv4Tile;
+  for (int row0 = 0; row0 < n * p.G; row0 += p.R) {
+    const int ui = (slot0 + (row0 >> p.rshift)) * p.Hkv + h;
+    const Kv4Unit u = p.units[ui];
+    if (u.tiles == 0) continue;
+    const int before = p.before[ui];
+    // log2 of the rows' sums; a row without keys has scores of minus infinity alone
+    float le[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int rr = u.row0 + r;
+      const float e = r < u.rows ? p.lse[(int64_t)(h * p.G + rr % p.G) * p.total + u.t0 + rr / p.G] : 0.f;
+      le[r] = e > -INFINITY ? e * 1.4426950408889634f : 0.f;
+    }
+    int block = -1, at = -1;  // the block that was looked up, and its place in the list
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+      const int key0 = first + i * kKv4HalfTok;
+      int tile = key0 / kKv4Tile;
+      if (key0 >= len) break;
+      if (p.kmean) {
+        if (tile / tpb != block) {
+          block = tile / tpb;
+          at = -1;
+          for (int e = lane; e < u.blocks; e += 32)
+            if ((int)p.list[(int64_t)ui * p.list_cap + e].x == block) at = e;
+          at = __reduce_max_sync(0xFFFFFFFFu, at);
+        }
+        if (at < 0) continue;
+        tile = at * tpb + tile % tpb;
+      }
+      if (tile >= u.tiles) continue;
+      const int64_t item = before + 2 * tile + (key0 / kKv4HalfTok & 1);
+      const float2* from = reinterpret_cast<const float2*>(p.seen) + item * 4 * kKv4HalfTok + lane;
+#pragma unroll
+      for (int r = 0; r < 8; r += 2) {
+        if (r >= u.rows) break;
+        const float2 s = __ldcs(from + r / 2 * kKv4HalfTok);
+        sum[i] += ex2_approx(s.x - le[r]);
+        if (r + 1 < u.rows) sum[i] += ex2_approx(s.y - le[r + 1]);
+      }
+    }
+  }
+  float* acc = p.acc + ((int64_t)b * p.Hkv + h) * p.tiles * kKv4Tile + first + lane;
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i)
+    if (first + i * kKv4HalfTok + lane < len) acc[i * kKv4HalfTok] += sum[i];
 }
 
 // ------------------------------------------------------------------ pool

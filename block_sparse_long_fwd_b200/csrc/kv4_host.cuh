@@ -279,9 +279,15 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   const size_t o_chosen = c.take(acc ? (size_t)nu * p.blocks * 4 : 0);
   const size_t o_scores = c.take((size_t)clusters * p.R * p.means * 8);
   const size_t o_part = c.take((size_t)2 * p.ctas * p.R * 130 * 4);
+  // the scores of few rows are kept for their weights, up to a GiB of them
+  const int64_t most = kmean ? std::min<int64_t>(items, (int64_t)2 * p.list_cap * (block_size / moba::kKv4Tile)) : items;
+  const size_t seen = few && acc ? (size_t)nu * most * 4 * moba::kKv4HalfTok * 8 : 0;
+  const bool keep = seen > 0 && seen <= ((size_t)1 << 30);
+  const size_t o_seen = c.take(keep ? seen : 0);
   const size_t o_qtiles = c.take(chunk ? (size_t)nu * 2 * moba::kKv4TileOp : 0);
   const size_t o_qscale = c.take(chunk ? (size_t)nu * moba::kKv4ChunkRows * 4 : 0);
   const Runner run = [&](uint8_t* ws, cudaStream_t st) -> int {
+    p.seen = keep ? reinterpret_cast<float*>(ws + o_seen) : nullptr;
     p.qtiles = ws + o_qtiles;
     p.qscale = reinterpret_cast<float*>(ws + o_qscale);
     p.units = reinterpret_cast<moba::Kv4Unit*>(ws + o_units);
@@ -307,6 +313,10 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
     if (acc && chunk) {
       launch_chained(moba::kv4_chunk_weight_kernel, dim3((unsigned)((capacity + 255) / 256), batch * heads_kv),
                      dim3(moba::kKv4ColThreads), moba::kKv4ColSmemBytes, st, p);
+    } else if (keep) {
+      launch_chained(moba::kv4_seen_kernel,
+                     dim3((unsigned)((capacity + moba::kKv4SeenKeys - 1) / moba::kKv4SeenKeys), batch * heads_kv),
+                     dim3(moba::kKv4SeenThreads), 0, st, p);
     } else if (acc) {
       const int per = moba::kKv4WeightThreads / 32 * (few ? moba::kKv4WeightTiles : 1);
       launch_chained(few ? moba::kv4_weight_kernel<false> : moba::kv4_weight_kernel<true>,
