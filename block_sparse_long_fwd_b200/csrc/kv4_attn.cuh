@@ -568,10 +568,10 @@ __device__ __forceinline__ void kv4_write_row(const Kv4AttnParams& p, const Kv4U
   const int rr = u.row0 + row;
   const int64_t t = u.t0 + rr / p.G;
   const int hq = u.h * p.G + rr % p.G;
-  const float inv = l > 0.f ? 64.f / l : 0.f;
+  const float inv = l != 0.f ? 64.f / l : 0.f;  // a NaN stays one
   reinterpret_cast<uint2*>(p.out + (t * p.Hq + hq) * kHeadDim)[lane] =
       make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (lane == 0) p.lse[(int64_t)hq * p.total + t] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  if (lane == 0) p.lse[(int64_t)hq * p.total + t] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 template <int NT_, int WARPS_, bool QREG_>
@@ -900,7 +900,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
           const int rr = u.row0 + row;
           const int64_t t = u.t0 + rr / p.G;
           const int hq = u.h * p.G + rr % p.G;
-          const float inv = l[nt][x] > 0.f ? 64.f / l[nt][x] : 0.f;
+          const float inv = l[nt][x] != 0.f ? 64.f / l[nt][x] : 0.f;
           uint32_t y[8];
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt) y[mt] = pack_bf16x2(o[nt][mt][x] * inv, o[nt][mt][x + 2] * inv);
@@ -909,7 +909,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
           out[1] = make_uint4(y[4], y[5], y[6], y[7]);
           if (r == 0)
             p.lse[(int64_t)hq * p.total + t] =
-                l[nt][x] > 0.f ? (m[nt][x] + log2f(l[nt][x])) * 0.6931471805599453f : -INFINITY;
+                l[nt][x] != 0.f ? (m[nt][x] + log2f(l[nt][x])) * 0.6931471805599453f : -INFINITY;
         }
     } else {
       const int which = begins ? 1 : 0;
@@ -1225,7 +1225,7 @@ __global__ void __launch_bounds__(kKv4SeenThreads) kv4_seen_kernel(Kv4AttnParams
     for (int r = 0; r < 8; ++r) {
       const int rr = u.row0 + r;
       const float e = r < u.rows ? p.lse[(int64_t)(h * p.G + rr % p.G) * p.total + u.t0 + rr / p.G] : 0.f;
-      le[r] = e > -INFINITY ? e * 1.4426950408889634f : 0.f;
+      le[r] = e != -INFINITY ? e * 1.4426950408889634f : 0.f;
     }
     int block = -1, at = -1;  // the block that was looked up, and its place in the list
 #pragma unroll

@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kKv4ChunkThreads, 1) kv4_chunk_kernel(Kv4AttnP
       const int rr = u.row0 + row;
       const int64_t t = u.t0 + rr / p.G;
       const int hq = u.h * p.G + rr % p.G;
-      const float inv = l > 0.f ? 64.f / l : 0.f;
+      const float inv = l != 0.f ? 64.f / l : 0.f;  // a NaN stays one
       float* part = p.part + (int64_t)(2 * cta + (s0 == 0 ? 1 : 0)) * (kKv4ChunkRows * 130);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kKv4ChunkThreads, 1) kv4_chunk_kernel(Kv4AttnP
         }
       }
       if (write && whole) {
-        p.lse[(int64_t)hq * p.total + t] = l > 0.f ? (ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        p.lse[(int64_t)hq * p.total + t] = l != 0.f ? (ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
       } else if (write) {
         *reinterpret_cast<float2*>(part + kKv4ChunkRows * kHeadDim + 2 * row) = make_float2(ref, l);
       }

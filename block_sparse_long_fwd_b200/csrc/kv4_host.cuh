@@ -265,9 +265,9 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   p.parts = few ? moba::Kv4Few::WARPS : chunk ? 1 : moba::Kv4Many::WARPS;
   p.steps = chunk ? 1 : 0;
   const int64_t nu = slots * heads_kv;
-  // items (half tiles, or steps of two tiles) are counted in 31 bits, and so are the starts of all ranges
+  // items (half tiles, or steps of two tiles) and the ends of all ranges are counted in 31 bits
   const int64_t items = chunk ? (p.tiles + 1) / 2 : 2 * p.tiles;
-  if (nu * items > INT32_MAX - 4096) return fail(MOBA_ERR_UNSUPPORTED, "too many (row, key) tiles");
+  if (nu * items > ((int64_t)1 << 30)) return fail(MOBA_ERR_UNSUPPORTED, "too many (row, key) tiles");
   p.list_cap = kmean ? (int)std::min<int64_t>(p.blocks, (int64_t)p.R * topk) : 0;
   // the gate: up to 8 CTAs share a unit's scores while there are few units
   int csize = 1;

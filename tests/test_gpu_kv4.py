@@ -365,6 +365,52 @@ def test_garbage_behind_the_last_token_is_not_read_into_results():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(a, b)
 
 
+@pytest.mark.parametrize("n", [1, 9, 100])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_query_that_is_not_finite_spoils_its_own_row_alone(n, bad):
+    hkv, L = 2, 700
+    kv4, _ = random_cache([L], hkv, 704, 5)
+    q = bf16(np.random.default_rng(1).standard_normal((n, 4, 128))).cuda()
+    want = moba.kv4_attend(q, kv4, ints([L]))
+    dirty = q.clone()
+    dirty[n // 2, 1, 5] = bad
+    got = moba.kv4_attend(dirty, kv4, ints([L]))
+    ok()
+    other = torch.ones(n, 4, dtype=torch.bool, device="cuda")
+    other[n // 2, 1] = False
+    assert torch.equal(got[0][other], want[0][other]) and torch.equal(got[1].T[other], want[1].T[other])
+    assert got[0][~other].isnan().all() and got[1].T[~other].isnan().all()
+
+
+def test_tensors_of_another_kind_are_refused():
+    kv4, _ = random_cache([64], 2, 128, 5)
+    q, acc, L = torch.zeros(1, 4, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 2, 128, device="cuda"), ints([64])
+    k = torch.zeros(1, 2, 128, dtype=torch.bfloat16, device="cuda")
+    moba.kv4_attend(q, kv4, L, acc=acc)
+    for call in (
+        lambda: moba.kv4_attend(q.half(), kv4, L), lambda: moba.kv4_attend(q.transpose(0, 1), kv4, L),
+        lambda: moba.kv4_attend(q[..., :64], kv4, L), lambda: moba.kv4_attend(q, kv4[:, :, ::2], L),
+        lambda: moba.kv4_attend(q, kv4, L.long()), lambda: moba.kv4_attend(q, kv4, L.cpu()),
+        lambda: moba.kv4_attend(q, kv4, L, acc=acc[..., :64]), lambda: moba.kv4_attend(q, kv4, L, acc=acc.double()),
+        lambda: moba.kv4_attend(q, kv4, L, cu=ints([0, 1, 1])), lambda: moba.kv4_attend(q, kv4, L, topk=3),
+        lambda: moba.kv4_attend(q, kv4, L, kmean=torch.zeros(1, 2, 1, 128, device="cuda")),
+        lambda: moba.kv4_attend(q, kv4, L, kmean=torch.zeros(1, 1, 1, 128, device="cuda"), block_size=128, topk=2),
+        lambda: moba.kv4_append(k, k[:, :1], kv4, L), lambda: moba.kv4_append(k.float(), k.float(), kv4, L),
+        lambda: moba.kv4_append(k, k, kv4, ints([0, 0])), lambda: moba.kv4_load(kv4, L, 129), lambda: moba.kv4_load(kv4, L, -1),
+        lambda: moba.kv4_pool(kv4, L, 0), lambda: moba.kv4_pool(kv4.view(torch.int8), L, 128),
+        lambda: moba.kv4_evict(kv4, acc, L, 200, 0, moba.kv4_cache(1, 2, 128), acc.clone()),
+        lambda: moba.kv4_evict(kv4, acc, L, 64, 65, moba.kv4_cache(1, 2, 128), acc.clone()),
+        lambda: moba.kv4_evict(kv4, acc, L, 64, 0, moba.kv4_cache(1, 1, 128), acc.clone()),
+    ):
+        with pytest.raises((ValueError, moba.MobaError)):
+            call()
+    with pytest.raises(moba.MobaError):
+        moba.kv4_pool(kv4, L, 100)
+    with pytest.raises(moba.MobaError):
+        moba.kv4_evict(kv4, acc, L, 64, 0, kv4, acc.clone())
+    ok()
+
+
 def test_a_length_beyond_the_capacity_is_cut_and_reported():
     kv4, vals = random_cache([128], 1, 128, 5)
     q = bf16(np.random.default_rng(1).standard_normal((1, 2, 128))).cuda()
