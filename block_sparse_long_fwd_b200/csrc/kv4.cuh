@@ -278,7 +278,7 @@ struct Kv4EvictParams {
 
 constexpr int kKv4SelectThreads = 1024;
 constexpr int kKv4SelectItems = 16;  // neighbouring weights a thread takes at a time
-constexpr int kKv4SelectBins = 2048;
+constexpr int kKv4SelectBins = 2048, kKv4SelectCopies = 4;
 
 // Weights as integers of the same order; a NaN below everything, -0 as 0.
 __device__ __forceinline__ uint32_t kv4_weight_key(float w) {
@@ -334,7 +334,8 @@ __device__ __forceinline__ void kv4_remote_st(uint32_t* p, uint32_t rank, uint32
 // each thread's neighbouring weights at its place in the order.
 __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictParams p) {
   grid_dependency_sync();
-  __shared__ uint32_t hist[kKv4SelectBins];
+  // neighbouring lanes count in copies of their own: weights crowd into few bins
+  __shared__ uint32_t hist[kKv4SelectCopies][kKv4SelectBins];
   __shared__ uint32_t warp_sums[32];
   __shared__ uint32_t s_found[2], s_count[2];  // prefix and need; this part's keys above and at the limit
   uint32_t rank, csize;
@@ -382,15 +383,18 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 32 : pass == 1 ? 21 : 10;
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
-    for (int i = tid; i < kKv4SelectBins; i += kKv4SelectThreads) hist[i] = 0;
+    for (int i = tid; i < kKv4SelectCopies * kKv4SelectBins; i += kKv4SelectThreads) (&hist[0][0])[i] = 0;
     __syncthreads();
     for (int at = i0 + tid * kKv4SelectItems; at < i1; at += kSweep) {
       if (!once) keys(at, k);
 #pragma unroll
       for (int x = 0; x < kKv4SelectItems; ++x)
         if (at + x < i1 && (pass == 0 || (k[x] >> above) == (prefix >> above)))
-          atomicAdd(&hist[(k[x] >> shift) & mask], 1u);
+          atomicAdd(&hist[tid % kKv4SelectCopies][(k[x] >> shift) & mask], 1u);
     }
+    __syncthreads();
+    for (int i = tid; i < kKv4SelectBins; i += kKv4SelectThreads)
+      hist[0][i] += (hist[1][i] + hist[2][i]) + hist[3][i];
     kv4_cluster_sync();
     if (rank == 0) {
       // two bins a thread, from the highest down: the bin in which the need is met
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
         const int bin = kKv4SelectBins - 1 - (2 * tid + x);
         uint32_t y[8];  // all under way at once
 #pragma unroll
-        for (uint32_t r = 0; r < 8; ++r) y[r] = r < csize ? kv4_remote_ld(&hist[bin], r) : 0;
+        for (uint32_t r = 0; r < 8; ++r) y[r] = r < csize ? kv4_remote_ld(&hist[0][bin], r) : 0;
         c[x] = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
       }
       uint32_t before = kv4_block_scan(c[0] + c[1], warp_sums, &total);
@@ -420,19 +424,40 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
     prefix = s_found[0];
     need = s_found[1];
   }
-  // keys above `prefix` stay, and the first `need` equal to it
-  uint32_t above = 0, equal = 0;
-  for (int at = i0 + tid * kKv4SelectItems; at < i1; at += kSweep) {
-    if (!once) keys(at, k);
+  // keys above `prefix` stay, and the first `need` equal to it: their numbers before each thread's
+  auto count = [&](int at, uint32_t& above, uint32_t& equal) {
+    above = equal = 0;
 #pragma unroll
     for (int x = 0; x < kKv4SelectItems; ++x) {
       above += at + x < i1 && k[x] > prefix;
       equal += at + x < i1 && k[x] == prefix;
     }
+  };
+  auto place = [&](int at, uint32_t a, uint32_t e) {
+#pragma unroll
+    for (int x = 0; x < kKv4SelectItems; ++x) {
+      if (at + x >= i1) continue;
+      if (k[x] > prefix) kept[a++ + min(e, need)] = at + x;
+      else if (k[x] == prefix) {
+        if (e < need) kept[a + e] = at + x;
+        ++e;
+      }
+    }
+  };
+  uint32_t above = 0, equal = 0, n_above, n_equal, a, e;
+  if (once) {
+    count(i0 + tid * kKv4SelectItems, above, equal);
+  } else {
+    for (int at = i0 + tid * kKv4SelectItems; at < i1; at += kSweep) {
+      uint32_t x, y;
+      keys(at, k);
+      count(at, x, y);
+      above += x;
+      equal += y;
+    }
   }
-  uint32_t n_above, n_equal;
-  kv4_block_scan(above, warp_sums, &n_above);
-  kv4_block_scan(equal, warp_sums, &n_equal);
+  a = kv4_block_scan(above, warp_sums, &n_above);
+  e = kv4_block_scan(equal, warp_sums, &n_equal);
   if (tid == 0) {
     s_count[0] = n_above;
     s_count[1] = n_equal;
@@ -444,30 +469,17 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
     equal_before += kv4_remote_ld(&s_count[1], r);
   }
   kv4_cluster_sync();  // no CTA leaves while another may still read its counts
+  if (once) {
+    place(i0 + tid * kKv4SelectItems, above_before + a, equal_before + e);
+    return;
+  }
   for (int s0 = i0; s0 < i1; s0 += kSweep) {
     const int at = s0 + tid * kKv4SelectItems;
-    above = equal = 0;
-    if (at < i1) {
-      if (!once) keys(at, k);
-#pragma unroll
-      for (int x = 0; x < kKv4SelectItems; ++x) {
-        above += at + x < i1 && k[x] > prefix;
-        equal += at + x < i1 && k[x] == prefix;
-      }
-    }
-    uint32_t a = above_before + kv4_block_scan(above, warp_sums, &n_above);
-    uint32_t e = equal_before + kv4_block_scan(equal, warp_sums, &n_equal);
-    if (at < i1) {
-#pragma unroll
-      for (int x = 0; x < kKv4SelectItems; ++x) {
-        if (at + x >= i1) continue;
-        if (k[x] > prefix) kept[a++ + min(e, need)] = at + x;
-        else if (k[x] == prefix) {
-          if (e < need) kept[a + e] = at + x;
-          ++e;
-        }
-      }
-    }
+    keys(at, k);
+    count(at, above, equal);
+    a = above_before + kv4_block_scan(above, warp_sums, &n_above);
+    e = equal_before + kv4_block_scan(equal, warp_sums, &n_equal);
+    place(at, a, e);
     above_before += n_above;
     equal_before += n_equal;
   }

@@ -1272,22 +1272,28 @@ struct Kv4PoolParams {
   float* kmean;          // [batch][heads][blocks][128]
 };
 
-constexpr int kKv4PoolThreads = 512;  // at most
+constexpr int kKv4PoolThreads = 256, kKv4PoolStages = 3;
 
-// A cluster of CTAs per (block, head, sequence), a part of the block's tokens
-// each, 16 tokens of each warp at a time. The tensor core sums in fp32: codes,
-// as they stand in a word, are fp16 subnormals (a nibble at bit 0 is c 2^-24,
-// at bit 4 c 2^-20), so a mask is all that they need; they meet the scales of
-// the four groups in four columns, of which the channel's own is kept, and the
-// scales times zero points are summed by one product more and taken off at the
-// end. (Widened to s (c - z) first, as the attention needs them, 128K tokens
-// of 8 heads took 35 us.) The warps' and CTAs' sums meet in a fixed order.
-// Blocks that the sequence has not completed are written as zero.
+// A cluster of CTAs per (block, head, sequence), a part of the block's tiles
+// each; each warp brings its tiles of keys into a ring of its own, one bulk
+// copy each, two ahead (with loads into registers instead, 16 warps of two
+// groups of tokens at a time, 128K tokens of 8 heads took 27 us).
+// The tensor core sums in fp32: codes, as they stand in a word, are fp16
+// subnormals (a nibble at bit 0 is c 2^-24, at bit 4 c 2^-20), so a mask is all
+// that they need; they meet the scales of the four groups in four columns, of
+// which the channel's own is kept, and the scales times zero points are summed
+// by one product more and taken off at the end. The warps' and CTAs' sums meet
+// in a fixed order. Blocks that the sequence has not completed are written as
+// zero.
 __global__ void __launch_bounds__(kKv4PoolThreads, 2) kv4_pool_kernel(Kv4PoolParams p) {
   grid_dependency_sync();
+  constexpr int MOST = kKv4PoolThreads / 32;
   const int WARPS = blockDim.x / 32;
-  __shared__ float sums[kKv4PoolThreads / 32][kHeadDim];
+  extern __shared__ __align__(16) uint8_t pool_ring[];  // [WARPS][kKv4PoolStages][kKv4Half]
+  __shared__ float sums[MOST][kHeadDim];
   __shared__ uint32_t total[kHeadDim];  // fp32 bits
+  __shared__ uint64_t full[MOST][kKv4PoolStages];
+  __shared__ int abort_flag;
   uint32_t rank, csize;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
@@ -1299,48 +1305,71 @@ __global__ void __launch_bounds__(kKv4PoolThreads, 2) kv4_pool_kernel(Kv4PoolPar
     if (rank == 0 && threadIdx.x < kHeadDim) out[threadIdx.x] = 0.f;
     return;
   }
-  const uint8_t* kt = p.kv4 + kv4_tile_off(p.tiles, p.heads, b, h, 0);
-  const int groups = p.B / 16, g0 = (int)((int64_t)j * groups);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < MOST * kKv4PoolStages; ++i) mbar_init(&full[0][0] + i, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const int tiles = p.B / kKv4Tile, step = csize * WARPS, t0 = rank * WARPS + warp;
+  const int n = t0 < tiles ? (tiles - t0 + step - 1) / step : 0;  // tiles of this warp
+  const uint8_t* src = p.kv4 + kv4_tile_off(p.tiles, p.heads, b, h, (int64_t)j * tiles + t0);
+  uint8_t* ring = pool_ring + warp * kKv4PoolStages * kKv4Half;
+  auto issue = [&](int k) {
+    if (k >= n || lane != 0) return;
+    const int d = k % kKv4PoolStages;
+    mbar_arrive_expect_tx(&full[warp][d], kKv4Half);
+    bulk_load(ring + d * kKv4Half, src + (int64_t)k * step * kKv4TileBytes, kKv4Half, &full[warp][d]);
+  };
+  issue(0);
+  issue(1);
   float o[8][4] = {}, oz[4] = {};
-#pragma unroll 2
-  for (int g = rank * WARPS + warp; g < groups; g += csize * WARPS) {
-    const int64_t t = (int64_t)(g0 + g) * 16;
-    const uint8_t* tile = kt + t / kKv4Tile * kKv4TileBytes;
-    const int at = (int)(t % kKv4Tile) + 2 * qd;
-    uint2 w[2][2];
-    uint32_t s[2], sz[2];  // scales, and scales times zero points, of group r % 4 for the lane's tokens
+  bool dead = false;
+  for (int k = 0; k < n; ++k) {
+    issue(k + 2);
+    const int d = k % kKv4PoolStages;
+    // a wait that ran out is followed by those for the copies under way, so that none outlives the block
+    if (!mbar_wait(&full[warp][d], (k / kKv4PoolStages) & 1, &abort_flag)) dead = true;
+    if (dead) continue;
+    const uint8_t* tile = ring + d * kKv4Half;
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      uint32_t pp[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int tok = at + 8 * f + e;
-        w[f][e] = __ldg(reinterpret_cast<const uint2*>(tile + tok * kKv4Row + r * 8));
-        pp[e] = __ldg(reinterpret_cast<const uint16_t*>(tile + kKv4Params + tok * 8 + (r & 3) * 2));
-      }
-      const uint32_t par = __byte_perm(pp[0], pp[1], 0x5410);
-      s[f] = par & 0x7F807F80u;
-      sz[f] = h2_mul(h2_sub(and_or(par, 0x000F000Fu, 0x64006400u), 0x64006400u), s[f]);
-    }
-    mma_f16(oz, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, sz[0], sz[1]);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      uint32_t a[2][2][4];  // [channel parity][tokens 0-7, 8-15][nibble]
+    for (int g = 0; g < kKv4Tile / 16; ++g) {
+      uint2 w[2][2];
+      uint32_t s[2], sz[2];  // scales, and scales times zero points, of group r % 4 for the lane's tokens
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        const uint32_t x0 = x ? w[f][0].y : w[f][0].x, x1 = x ? w[f][1].y : w[f][1].x;
+        uint32_t pp[2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t u = __byte_perm(x0, x1, c ? 0x7632 : 0x5410), v = u >> 8;
-          a[c][f][0] = u & 0x000F000Fu;
-          a[c][f][1] = u & 0x00F000F0u;
-          a[c][f][2] = v & 0x000F000Fu;
-          a[c][f][3] = v & 0x00F000F0u;
+        for (int e = 0; e < 2; ++e) {
+          const int tok = g * 16 + 8 * f + 2 * qd + (e ^ (qd & 1));
+          w[f][e] = *reinterpret_cast<const uint2*>(tile + tok * kKv4Row + r * 8);
+          pp[e] = *reinterpret_cast<const uint16_t*>(tile + kKv4Params + tok * 8 + (r & 3) * 2);
         }
+        const uint32_t par = __byte_perm(pp[0], pp[1], 0x5410);
+        s[f] = par & 0x7F807F80u;
+        sz[f] = h2_mul(h2_sub(and_or(par, 0x000F000Fu, 0x64006400u), 0x64006400u), s[f]);
       }
+      mma_f16(oz, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, sz[0], sz[1]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) mma_f16(o[x * 4 + i], a[0][0][i], a[1][0][i], a[0][1][i], a[1][1][i], s[0], s[1]);
+      for (int x = 0; x < 2; ++x) {
+        uint32_t a[2][2][4];  // [channel parity][tokens 0-7, 8-15][nibble]
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const uint32_t x0 = x ? w[f][0].y : w[f][0].x, x1 = x ? w[f][1].y : w[f][1].x;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t u = __byte_perm(x0, x1, c ? 0x7632 : 0x5410), v = u >> 8;
+            a[c][f][0] = u & 0x000F000Fu;
+            a[c][f][1] = u & 0x00F000F0u;
+            a[c][f][2] = v & 0x000F000Fu;
+            a[c][f][3] = v & 0x00F000F0u;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mma_f16(o[x * 4 + i], a[0][0][i], a[1][0][i], a[0][1][i], a[1][1][i], s[0], s[1]);
+      }
     }
+    __syncwarp();  // the tile is read: the one after next may take its place
   }
   // channels 16 r .. are of group r / 2: the lane that holds this column has their sums
   if (qd == r >> 2) {

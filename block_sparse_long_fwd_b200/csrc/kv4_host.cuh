@@ -94,6 +94,8 @@ int kv4_begin(DeviceInfo* dev, cudaStream_t st) {
                                      moba::kKv4ChunkSmemBytes));
       MOBA_CUDA(cudaFuncSetAttribute(moba::kv4_chunk_weight_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      moba::kKv4ColSmemBytes));
+      MOBA_CUDA(cudaFuncSetAttribute(moba::kv4_pool_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     moba::kKv4PoolThreads / 32 * moba::kKv4PoolStages * moba::kKv4Half));
       MOBA_CUDA(cudaFuncSetAttribute(moba::kv4_gate_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      MOBA_KV4_MAX_BLOCKS * 4 + 4));
       g_kv4_ready[d] = true;
@@ -194,12 +196,14 @@ int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch, int heads_
   p.blocks = (int)(capacity / block_size);
   p.kmean = kmean;
   if (p.blocks) {
-    // a warp for 64 tokens, 4 to 16 of them; up to 8 CTAs share a large block while there are SMs for them
+    // a warp for 64 tokens, 4 to 8 of them; up to 8 CTAs share a large block while there are SMs for them
     const int threads = std::min(moba::kKv4PoolThreads, std::max(moba::kHeadDim, block_size / 64 * 32));
+    const size_t ring = (size_t)threads / 32 * moba::kKv4PoolStages * moba::kKv4Half;
     int csize = 1;
-    while (csize < 8 && (int64_t)p.blocks * heads_kv * batch * csize * 2 <= dev.sms && block_size / csize > 2048) csize *= 2;
+    while (csize < 8 && (int64_t)p.blocks * heads_kv * batch * csize * 2 <= 2 * dev.sms && block_size / csize > 1024)
+      csize *= 2;
     if ((int64_t)p.blocks * csize > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many blocks");
-    launch_clusters(moba::kv4_pool_kernel, dim3(p.blocks * csize, heads_kv, batch), dim3(threads), 0, csize,
+    launch_clusters(moba::kv4_pool_kernel, dim3(p.blocks * csize, heads_kv, batch), dim3(threads), ring, csize,
                     stream, p);
     MOBA_CUDA(cudaGetLastError());
   }
