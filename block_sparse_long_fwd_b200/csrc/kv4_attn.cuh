@@ -121,22 +121,20 @@ __device__ __forceinline__ int kv4_items(const Kv4AttnParams& p, const Kv4Unit& 
 constexpr int kKv4GateThreads = 256;
 constexpr int kKv4GateRegs = 8;  // scores a lane keeps: rows with up to 256 past blocks select from registers
 
-// The best candidate after (ps, pj) in (score descending, block ascending)
-// order, over the warp.
-__device__ __forceinline__ void kv4_warp_best(double& s, int& j) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    const double s2 = __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    const int j2 = __shfl_xor_sync(0xFFFFFFFFu, j, d);
-    if (j2 >= 0 && (j < 0 || s2 > s || (s2 == s && j2 < j))) {
-      s = s2;
-      j = j2;
-    }
-  }
+// A score as an integer of the same order.
+__device__ __forceinline__ uint64_t kv4_score_key(double s) {
+  const uint64_t u = __double_as_longlong(s);
+  return u >> 63 ? ~u : u | 1ull << 63;
 }
 
-__device__ __forceinline__ bool kv4_after(double s, int j, double ps, int pj) {
-  return pj < 0 || s < ps || (s == ps && j > pj);
+// The largest (key, lowest block) over the warp; j < 0 takes no part, and comes
+// back where nobody does.
+__device__ __forceinline__ void kv4_warp_best(uint64_t& key, int& j) {
+  const uint32_t hi = j < 0 ? 0 : (uint32_t)(key >> 32), top = __reduce_max_sync(0xFFFFFFFFu, hi);
+  const uint32_t lo = j >= 0 && hi == top ? (uint32_t)key : 0, low = __reduce_max_sync(0xFFFFFFFFu, lo);
+  const bool best = j >= 0 && hi == top && (uint32_t)key == low;
+  j = (int)__reduce_min_sync(0xFFFFFFFFu, best ? (uint32_t)j : 0xFFFFFFFFu);
+  key = (uint64_t)top << 32 | low;
 }
 
 // One cluster per unit (looping over units): its CTAs score the past blocks
@@ -158,8 +156,20 @@ __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams
   constexpr int WARPS = kKv4GateThreads / 32;
   double* scores = p.scores + (int64_t)cluster * p.R * p.means;
   const int nu = p.slots * p.Hkv;
+  // offsets and lengths in one trip, where they fit
+  __shared__ int32_t copy[2 * kKv4GateThreads + 1];
+  const int32_t *cu = p.cu, *lengths = p.lengths;
+  if (p.batch <= kKv4GateThreads) {
+    if (tid < p.batch) copy[tid] = p.lengths[tid];
+    lengths = copy;
+    if (cu) {
+      for (int i = tid; i <= p.batch; i += kKv4GateThreads) copy[kKv4GateThreads + i] = p.cu[i];
+      cu = copy + kKv4GateThreads;
+    }
+    __syncthreads();
+  }
   for (int ui = cluster; ui < nu; ui += clusters) {
-    if (tid == 0) s_unit = kv4_unit_of(p, p.cu, p.lengths, ui / p.Hkv, ui % p.Hkv);
+    if (tid == 0) s_unit = kv4_unit_of(p, cu, lengths, ui / p.Hkv, ui % p.Hkv);
     __syncthreads();
     Kv4Unit u = s_unit;
     const int last = u.rows ? kv4_last_pos(p, u) : -1;
@@ -228,33 +238,33 @@ __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams
             continue;
           }
           const double* sc = scores + (int64_t)r * p.means;
-          double ps = 0.0;
-          int pj = -1;
           const bool few = mine <= 32 * kKv4GateRegs;
-          double mv[kKv4GateRegs];
+          uint64_t mv[kKv4GateRegs];
+          uint32_t left = 0;  // blocks of this lane that are still to be had
           if (few)
 #pragma unroll
-            for (int i = 0; i < kKv4GateRegs; ++i) mv[i] = i * 32 + lane < mine ? __ldcg(sc + i * 32 + lane) : 0.0;
+            for (int i = 0; i < kKv4GateRegs; ++i)
+              if (i * 32 + lane < mine) mv[i] = kv4_score_key(__ldcg(sc + i * 32 + lane)), left |= 1u << i;
+          uint64_t last_key = 0;
+          int last_j = -1;
           for (int k = 0; k < picks; ++k) {
-            double s = 0.0;
+            uint64_t key = 0;
             int j = -1;
             if (few) {
 #pragma unroll
-              for (int i = 0; i < kKv4GateRegs; ++i) {
-                const int jj = i * 32 + lane;
-                if (jj < mine && kv4_after(mv[i], jj, ps, pj) && (j < 0 || mv[i] > s)) s = mv[i], j = jj;
-              }
-            } else {
+              for (int i = 0; i < kKv4GateRegs; ++i)
+                if (left >> i & 1u && (j < 0 || mv[i] > key)) key = mv[i], j = i * 32 + lane;
+            } else {  // the best of those behind the last one
               for (int jj = lane; jj < mine; jj += 32) {
-                const double v = __ldcg(sc + jj);
-                if (kv4_after(v, jj, ps, pj) && (j < 0 || v > s)) s = v, j = jj;
+                const uint64_t v = kv4_score_key(__ldcg(sc + jj));
+                if ((last_j < 0 || v < last_key || (v == last_key && jj > last_j)) && (j < 0 || v > key)) key = v, j = jj;
               }
             }
-            kv4_warp_best(s, j);
-            if (j < 0) break;  // only NaN scores are left
+            kv4_warp_best(key, j);
+            if (few && (j & 31) == lane) left &= ~(1u << (j >> 5));
             if (lane == 0) atomicOr(&picked[j], bit);
-            ps = s;
-            pj = j;
+            last_key = key;
+            last_j = j;
           }
         }
       }
