@@ -9,9 +9,8 @@
 //
 // Work is cut into units: R consecutive rows (token, q head of one kv head) of
 // one sequence and kv head, with the 64-token tiles of the cache that at least
-// one of them attends. All units' tiles in a row are dealt out evenly, in half
-// tiles, one contiguous range to each warp of a grid of one CTA per SM,
-// wherever the units begin and end: lengths that differ, and few units with
+// one of them attends. All units' tiles in a row are dealt out evenly, one
+// contiguous range to each warp of a grid of one CTA per SM, wherever the units begin and end: lengths that differ, and few units with
 // many tiles, balance by themselves. A unit that several warps share is joined
 // in shared memory, and by a second kernel where it crosses CTAs.
 #pragma once
@@ -49,11 +48,11 @@ struct Kv4AttnParams {
   uint2* list;                  // [slots * Hkv][list_cap]: (block, rows that chose it), ascending
   uint32_t* chosen;             // [slots * Hkv][blocks]: rows of the unit that chose the block
   double* scores;               // [clusters][R][means]
-  float* seen;                  // or null: [items][4][32][2] log2 scores, of each half tile's keys and two rows
+  float* seen;                  // or null: [items][4][64][2] log2 scores, of each tile's keys and two rows
   float* part;                  // [2 * ctas][R * 130]: O, then m and l
   int list_cap, ctas;
   int parts;                    // ranges of a CTA
-  int steps;                    // ranges are dealt out in steps of 128 keys (else in half tiles)
+  int steps;                    // ranges are dealt out in steps of 128 keys (else in tiles)
   uint8_t* qtiles;              // [slots * Hkv][2][32768]: query tiles as fp16 operands
   float* qscale;                // [slots * Hkv][256]: their rows' scales
 };
@@ -111,9 +110,9 @@ __device__ __forceinline__ int kv4_last_pos(const Kv4AttnParams& p, const Kv4Uni
   return u.pos0 + (u.row0 + u.rows - 1) / p.G;
 }
 
-// What is dealt out of a unit: half tiles, or steps of two tiles.
+// What is dealt out of a unit: tiles, or steps of two tiles.
 __device__ __forceinline__ int kv4_items(const Kv4AttnParams& p, const Kv4Unit& u) {
-  return p.steps ? (u.tiles + 1) / 2 : 2 * u.tiles;
+  return p.steps ? (u.tiles + 1) / 2 : u.tiles;
 }
 
 // ------------------------------------------------------------------ gate
@@ -593,26 +592,23 @@ struct Kv4Cfg {
   static constexpr bool QREG = QREG_;       // query fragments in registers, else in shared memory
   static constexpr int PIECE = R * kHeadDim * 4;
   struct Shared {
-    // 2 x 32 tokens a warp (key codes, key parameters, value codes, value parameters): one half tile in use, one on
-    // its way; at the end, the warp's partial result of a unit that it began
-    uint8_t ring[WARPS][2][kKv4Half];
+    // a tile a warp: its keys are in use while the values come, and the next tile's keys come while the values are
+    // in use; at the end, the warp's partial result of a unit that it began
+    uint8_t ring[WARPS][kKv4TileBytes];
     uint8_t piece[WARPS][PIECE];            // the warp's partial result of a unit that it did not begin
     float2 ml[WARPS][2][R];                 // their maxima and sums
     uint2 q[QREG ? 1 : WARPS][NT][8][32];
-    uint64_t full[WARPS][2];
+    uint64_t full[WARPS][2];                // keys, values
     int unit[2 * WARPS];                    // units of the partial results, -1 for none
     int begins[2 * WARPS], ends[2 * WARPS];
     int abort_flag;
   };
-  static_assert(2 * kKv4Half >= PIECE, "a partial result fits the warp's ring");
+  static_assert(kKv4TileBytes >= PIECE, "a partial result fits the warp's ring");
 };
 
 using Kv4Few = Kv4Cfg<1, 16, true>;    // up to 8 rows
 using Kv4Many = Kv4Cfg<2, 8, false>;   // up to 16 rows
 
-constexpr int kKv4HalfTok = kKv4Tile / 2;
-constexpr int kKv4HalfParams = kKv4HalfTok * kKv4Row;         // 2048: offset of the parameters of 32 tokens
-constexpr int kKv4HalfRows = kKv4HalfParams + kKv4HalfTok * 8;  // 2304: their keys (or values)
 constexpr float kKv4Low = -1e30f;  // running maximum before the first score
 
 template <class C>
@@ -632,68 +628,69 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
   if (!range.any) return;
   const int n = range.n;
 
-  // A warp fetches its own half tiles, two ahead: the four pieces of one by bulk copies of four lanes. `issue` walks
-  // the units as far as its half tile.
-  const int piece = (lane & 2 ? kKv4Half : 0) + (lane & 1 ? kKv4Params : 0);
-  const int piece_half = lane & 1 ? kKv4HalfTok * 8 : kKv4HalfParams;  // its bytes, and from half to half
-  const int piece_dst = (lane & 2 ? kKv4HalfRows : 0) + (lane & 1 ? kKv4HalfParams : 0);
+  // A warp fetches its own tiles, one bulk copy for the keys and one for the values of each (32 tokens at a time, four
+  // copies and two ahead, cost 30 instructions more for 16 keys: 265 against ... us at 1M tokens). `next` walks the
+  // units to the next tile.
   const int tpb = p.B / kKv4Tile;
   int c_ui = range.unit - 1, c_off = range.off, c_left = n, c_end = 0, c_at = 0, c_in = 0;
-  const uint8_t* c_src = nullptr;       // the lane's piece of the half tile (with a gate, of the sequence's first)
-  int key_a = 0, key_b = 0, c_key = 0;  // first keys of the half tile in use, of the next and of the one after
-  uint32_t rows_a = ~0u, rows_b = ~0u;  // rows that chose their blocks
-  auto issue = [&](int d) {
-    key_a = key_b;
-    rows_a = rows_b;
-    if (c_left <= 0) return;
+  const uint8_t* c_src = nullptr;       // the next tile (with a gate, the first of the sequence)
+  const uint8_t* src = nullptr;         // the tile that comes
+  int key_b = 0, c_key = 0;             // their first keys
+  uint32_t rows_b = ~0u;                // rows that chose the block
+  auto next = [&] {
     if (c_off >= c_end) {  // on to the next unit that has tiles
       c_off -= c_end;
-      do c_end = 2 * range.at(++c_ui).tiles;
+      do c_end = range.at(++c_ui).tiles;
       while (c_end == 0);
       const Kv4Unit u = range.at(c_ui);
-      c_src = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, u.b, u.h, 0) + piece;
+      c_src = p.kv4 + kv4_tile_off(p.tiles, p.Hkv, u.b, u.h, 0);
       if (p.kmean) {
-        c_at = (c_off >> 1) / tpb;
-        c_in = (c_off >> 1) - c_at * tpb;
+        c_at = c_off / tpb;
+        c_in = c_off - c_at * tpb;
       } else {
-        c_src += (int64_t)(c_off >> 1) * kKv4TileBytes + (c_off & 1) * piece_half;
-        c_key = c_off * kKv4HalfTok;
+        c_src += (int64_t)c_off * kKv4TileBytes;
+        c_key = c_off * kKv4Tile;
       }
     }
-    uint64_t* bar = &sh->full[warp][d];
-    if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kKv4HalfRows);
-    const uint8_t* src = c_src;
     if (p.kmean) {
       if (c_in == tpb) c_in = 0, ++c_at;
       const uint2 e = p.list[(int64_t)c_ui * p.list_cap + c_at];
-      const int tile = (int)e.x * tpb + c_in, half = c_off & 1;
-      src += (int64_t)tile * kKv4TileBytes + half * piece_half;
-      key_b = tile * kKv4Tile + half * kKv4HalfTok;
+      const int tile = (int)e.x * tpb + c_in++;
+      src = c_src + (int64_t)tile * kKv4TileBytes;
+      key_b = tile * kKv4Tile;
       rows_b = e.y;
-      c_in += half;
     } else {
+      src = c_src;
       key_b = c_key;
-      c_key += kKv4HalfTok;
-      c_src += c_off & 1 ? kKv4TileBytes - piece_half : piece_half;
+      c_src += kKv4TileBytes;
+      c_key += kKv4Tile;
     }
     ++c_off;
     --c_left;
-    __syncwarp();
-    if (lane < 4) bulk_load(sh->ring[warp][d] + piece_dst, src, piece_half, bar);
   };
-  issue(0);
-  issue(1);
+  uint8_t* ring = sh->ring[warp];
+  auto issue = [&](int vals) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&sh->full[warp][vals], kKv4Half);
+      bulk_load(ring + vals * kKv4Half, src + vals * kKv4Half, kKv4Half, &sh->full[warp][vals]);
+    }
+  };
+  if (n) {
+    next();
+    issue(0);
+    issue(1);
+  }
 
   const int r = lane >> 2, qd = lane & 3;
   const int tok0 = kv4_token_of(r);
   const int vchunk = (r ^ (qd & 2 ? 4 : 0)) * 8;
   const int ve0 = 2 * qd + (qd & 1), ve1 = 2 * qd + ((qd & 1) ^ 1);
-  bool dead = false;
-  int death = 0;  // the half tile that never came
-  int k = 0;      // half tiles of this warp behind us
+  bool dead = false;  // a wait ran out: what follows is computed on what is there, and nothing more is fetched
+  int death = 0;      // in this tile
+  int k = 0;          // tiles of this warp behind us
   for (int ui = range.unit, off = range.off; k < n; ++ui, off = 0) {
     const Kv4Unit u = range.at(ui);
-    const int stop = k + min(n - k, 2 * u.tiles - off);
+    const int stop = k + min(n - k, u.tiles - off);
     if (stop == k) continue;
     // the rows' fragments, scales, and last keys (of this lane's two rows of each group of eight)
     uint32_t qf[16];
@@ -726,22 +723,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
 
     const int k0 = k;
     for (; k < stop; ++k) {
-      const int d = k & 1;
-      if (!dead && !mbar_wait(&sh->full[warp][d], (k >> 1) & 1, &sh->abort_flag)) dead = true, death = k;
-      if (dead) continue;
-      uint8_t* slot = sh->ring[warp][d];
-      const uint8_t* kt = slot;
-      const uint8_t* vt = slot + kKv4HalfRows;
+      const int key_a = key_b;
+      const uint32_t rows_a = rows_b;
+      const uint8_t* kt = ring;
+      const uint8_t* vt = ring + kKv4Half;
+      if (!dead && !mbar_wait(&sh->full[warp][0], k & 1, &sh->abort_flag)) dead = true, death = k;
 
       // scores: keys x rows, 16 keys at a time
-      float sc[2][NT][4];
+      float sc[4][NT][4];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
+      for (int g = 0; g < 4; ++g) {
         const int ta = tok0 + g * 16, tb = ta + 8;
         const uint4 wa = *reinterpret_cast<const uint4*>(kt + ta * kKv4Row + qd * 16);
         const uint4 wb = *reinterpret_cast<const uint4*>(kt + tb * kKv4Row + qd * 16);
-        const uint32_t pa = *reinterpret_cast<const uint16_t*>(kt + kKv4HalfParams + ta * 8 + qd * 2);
-        const uint32_t pb = *reinterpret_cast<const uint16_t*>(kt + kKv4HalfParams + tb * 8 + qd * 2);
+        const uint32_t pa = *reinterpret_cast<const uint16_t*>(kt + kKv4Params + ta * 8 + qd * 2);
+        const uint32_t pb = *reinterpret_cast<const uint16_t*>(kt + kKv4Params + tb * 8 + qd * 2);
         const Kv4Par fa = kv4_par(__byte_perm(pa, 0, 0x1010)), fb = kv4_par(__byte_perm(pb, 0, 0x1010));
         const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xb[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
@@ -765,17 +761,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
           }
         }
       }
-      // keys behind a row's position, and blocks that a row did not choose
-      const bool edge = key_a + kKv4HalfTok - 1 > first_pos;
-      if (edge && key_a + lane > last_pos) {
-        // what lies behind the last token may hold anything: its values' scales become zero
-        *reinterpret_cast<uint2*>(slot + kKv4HalfRows + kKv4HalfParams + lane * 8) = make_uint2(0, 0);
-        fence_proxy_async_smem();  // before the copy that will overwrite them
+      __syncwarp();  // the keys are read: the next tile's may take their place
+      const bool more = !dead && c_left > 0;
+      if (more) {
+        next();
+        issue(0);
       }
-      if (edge || (rows_a & all_rows) != all_rows) {
-        __syncwarp();
+      if (!dead && !mbar_wait(&sh->full[warp][1], k & 1, &sh->abort_flag)) dead = true, death = k;
+
+      // keys behind a row's position, and blocks that a row did not choose (a loop of one turn: a branch, where the
+      // compiler would have every tile pay for instructions that are switched off)
+      const bool edge = key_a + kKv4Tile - 1 > first_pos;
+#pragma unroll 1
+      for (bool mask = edge || (rows_a & all_rows) != all_rows; mask; mask = false) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < 4; ++g)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -784,12 +784,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
               const uint32_t row = nt * 8 + 2 * qd + (x & 1);
               if (key > last[nt][x & 1] || !(rows_a >> row & 1u)) sc[g][nt][x] = -INFINITY;
             }
+        // what lies behind the last token may hold anything: its values' scales become zero
+#pragma unroll
+        for (int x = 0; x < kKv4Tile; x += 32)
+          if (key_a + x + lane > last_pos)
+            *reinterpret_cast<uint2*>(ring + kKv4Half + kKv4Params + (x + lane) * 8) = make_uint2(0, 0);
+        fence_proxy_async_smem();  // before the copy that will overwrite them
+        __syncwarp();
       }
       if constexpr (NT == 1) {
         if (p.seen && 2 * qd < u.rows) {  // for the accumulated weights: the lane's two rows of its keys
-          float2* to = reinterpret_cast<float2*>(p.seen) + ((int64_t)(range.item + k) * 4 + qd) * kKv4HalfTok + tok0;
+          float2* to = reinterpret_cast<float2*>(p.seen) + ((int64_t)(range.item + k) * 4 + qd) * kKv4Tile + tok0;
 #pragma unroll
-          for (int g = 0; g < 2; ++g)
+          for (int g = 0; g < 4; ++g)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const uint64_t y = f2_fma(f2_pack(sc[g][0][2 * x], sc[g][0][2 * x + 1]), qs[0], 0);
@@ -804,8 +811,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
           const int t0 = ve0 + g * 16 + f * 8, t1 = ve1 + g * 16 + f * 8;
           w[f][0] = *reinterpret_cast<const uint2*>(vt + t0 * kKv4Row + vchunk);
           w[f][1] = *reinterpret_cast<const uint2*>(vt + t1 * kKv4Row + vchunk);
-          const uint32_t p0 = *reinterpret_cast<const uint16_t*>(vt + kKv4HalfParams + t0 * 8 + (r >> 1) * 2);
-          const uint32_t p1 = *reinterpret_cast<const uint16_t*>(vt + kKv4HalfParams + t1 * 8 + (r >> 1) * 2);
+          const uint32_t p0 = *reinterpret_cast<const uint16_t*>(vt + kKv4Params + t0 * 8 + (r >> 1) * 2);
+          const uint32_t p1 = *reinterpret_cast<const uint16_t*>(vt + kKv4Params + t1 * 8 + (r >> 1) * 2);
           pp[f] = __byte_perm(p0, p1, 0x5410);
         }
       };
@@ -814,13 +821,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
       values(0, w, vp);
       // weights 2^(score - m). The reference m moves when a score exceeds it by more than 15, to 12 below
       // the largest: weights then lie under 2^15, which fp16 holds, and end 2^-37 below the largest
-      uint32_t pf[NT][2][2];
+      uint32_t pf[NT][4][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float t[2][4];
+        float t[4][4];
         auto shifted = [&] {
 #pragma unroll
-          for (int g = 0; g < 2; ++g)
+          for (int g = 0; g < 4; ++g)
 #pragma unroll
             for (int x = 0; x < 4; x += 2) {
               const uint64_t y = f2_fma(f2_pack(sc[g][nt][x], sc[g][nt][x + 1]), qs[nt], nm[nt]);
@@ -829,13 +836,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
             }
         };
         shifted();
-        const float top = fmaxf(fmax3(fmax3(t[0][0], t[0][1], t[0][2]), fmax3(t[0][3], t[1][0], t[1][1]), t[1][2]), t[1][3]);
+        float top = t[3][3];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          top = fmax3(top, t[g][0], t[g][1]);
+          if (g < 3) top = fmax3(top, t[g][2], t[g][3]);
+        }
+        top = fmaxf(top, t[3][2]);
         if (__any_sync(0xFFFFFFFFu, top > 15.f)) {
           float a2[2], n2[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float q1 = x ? f2_hi(qs[nt]) : f2_lo(qs[nt]), m1 = -(x ? f2_hi(nm[nt]) : f2_lo(nm[nt]));
-            float mx = fmaxf(fmaxf(sc[0][nt][x], sc[0][nt][x + 2]), fmaxf(sc[1][nt][x], sc[1][nt][x + 2])) * q1;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) mx = fmax3(mx, sc[g][nt][x], sc[g][nt][x + 2]);
+            mx *= q1;
 #pragma unroll
             for (int d2 = 4; d2 < 32; d2 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d2));
             const bool move = mx > m1 + 15.f;
@@ -849,7 +865,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
           shifted();
         }
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < 4; ++g) {
           float e[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) e[x] = ex2_approx(t[g][x]);
@@ -860,7 +876,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
       }
       // O^T += V^T P^T: channels x rows
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
+      for (int g = 0; g < 4; ++g) {
         Kv4Par fp[2];
 #pragma unroll
         for (int f = 0; f < 2; ++f) fp[f] = kv4_par(vp[f]);
@@ -879,10 +895,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
             for (int nt = 0; nt < NT; ++nt)
               mma_f16(o[nt][h * 4 + j], a[0][0][j], a[1][0][j], a[0][1][j], a[1][1][j], pf[nt][g][0], pf[nt][g][1]);
         }
-        if (g == 0) values(1, w, vp);
+        if (g < 3) values(g + 1, w, vp);
       }
-      __syncwarp();  // the half tile is in registers: the next but one may take its place
-      issue(d);
+      __syncwarp();  // the values are read
+      if (more) issue(1);
     }
 
     // ---- this warp's part of the unit: all of it is a result, else a piece to be joined
@@ -898,7 +914,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nt][x] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][x], d);
-    const bool begins = off == 0, ends = off + (k - k0) == 2 * u.tiles;
+    const bool begins = off == 0, ends = off + (k - k0) == u.tiles;
     // lane: channels 16 r .. 16 r + 15 of rows 2 qd, 2 qd + 1 of each group of eight (a 64th of them so far)
     if (begins && ends) {
 #pragma unroll
@@ -930,7 +946,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
       }
       // a unit that this warp begins and does not end is its last: its ring is free
       __syncwarp();
-      float* at = reinterpret_cast<float*>(which ? &sh->ring[warp][0][0] : sh->piece[warp]);
+      float* at = reinterpret_cast<float*>(which ? ring : sh->piece[warp]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -946,12 +962,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
     }
   }
   if (dead) {
-    // the block's shared memory lives until the copies under way have landed
-    for (int i = death; i < min(death + 2, n); ++i) {
-      const uint64_t t0 = clock64();
-      while (!mbar_try_wait(&sh->full[warp][i & 1], (i >> 1) & 1) && (uint64_t)(clock64() - t0) < (1ull << 31)) {
-      }
-    }
+    // the block's shared memory lives until the copies under way have landed: keys of tile n - c_left - 1, values of
+    // tile `death`
+    volatile int keep_waiting = 0;
+    mbar_wait(&sh->full[warp][0], (n - c_left - 1) & 1, &keep_waiting, 1ull << 28);
+    mbar_wait(&sh->full[warp][1], death & 1, &keep_waiting, 1ull << 28);
   }
   __syncthreads();
 
@@ -983,7 +998,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
       for (int i = first; i <= fin; ++i) {
         if (!(of >> i & 1u)) continue;
         const float f = __shfl_sync(0xFFFFFFFFu, a, i);
-        const float* from = reinterpret_cast<const float*>(i & 1 ? &sh->ring[i >> 1][0][0] : sh->piece[i >> 1]);
+        const float* from = reinterpret_cast<const float*>(i & 1 ? sh->ring[i >> 1] : sh->piece[i >> 1]);
         const float4 v = reinterpret_cast<const float4*>(from + row * kHeadDim)[lane ^ (lane >> 2 & 3)];
         oo.x = fmaf(v.x, f, oo.x);
         oo.y = fmaf(v.y, f, oo.y);
@@ -1221,7 +1236,7 @@ __global__ void __launch_bounds__(kKv4SeenThreads) kv4_seen_kernel(Kv4AttnParams
   int t0;
   const int n = kv4_queries(p, p.cu, b, &t0);
   if (n == 0 || first >= len) return;
-  constexpr int PARTS = kKv4SeenKeys / (kKv4SeenThreads / 32) / kKv4HalfTok;
+  constexpr int PARTS = kKv4SeenKeys / (kKv4SeenThreads / 32) / 32;
   float sum[PARTS] = {};
   const int slot0 = kv4_first_slot(p, b, t0), tpb = p.B / kKv4Tile;
   for (int row0 = 0; row0 < n * p.G; row0 += p.R) {
@@ -1240,7 +1255,7 @@ __global__ void __launch_bounds__(kKv4SeenThreads) kv4_seen_kernel(Kv4AttnParams
     int block = -1, at = -1;  // the block that was looked up, and its place in the list
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
-      const int key0 = first + i * kKv4HalfTok;
+      const int key0 = first + i * 32;
       int tile = key0 / kKv4Tile;
       if (key0 >= len) break;
       if (p.kmean) {
@@ -1255,12 +1270,12 @@ __global__ void __launch_bounds__(kKv4SeenThreads) kv4_seen_kernel(Kv4AttnParams
         tile = at * tpb + tile % tpb;
       }
       if (tile >= u.tiles) continue;
-      const int64_t item = before + 2 * tile + (key0 / kKv4HalfTok & 1);
-      const float2* from = reinterpret_cast<const float2*>(p.seen) + item * 4 * kKv4HalfTok + lane;
+      const float2* from = reinterpret_cast<const float2*>(p.seen) + (int64_t)(before + tile) * 4 * kKv4Tile +
+                           key0 % kKv4Tile + lane;
 #pragma unroll
       for (int r = 0; r < 8; r += 2) {
         if (r >= u.rows) break;
-        const float2 s = __ldcs(from + r / 2 * kKv4HalfTok);
+        const float2 s = __ldcs(from + r / 2 * kKv4Tile);
         sum[i] += ex2_approx(s.x - le[r]);
         if (r + 1 < u.rows) sum[i] += ex2_approx(s.y - le[r + 1]);
       }
@@ -1269,7 +1284,7 @@ __global__ void __launch_bounds__(kKv4SeenThreads) kv4_seen_kernel(Kv4AttnParams
   float* acc = p.acc + ((int64_t)b * p.Hkv + h) * p.tiles * kKv4Tile + first + lane;
 #pragma unroll
   for (int i = 0; i < PARTS; ++i)
-    if (first + i * kKv4HalfTok + lane < len) acc[i * kKv4HalfTok] += sum[i];
+    if (first + i * 32 + lane < len) acc[i * 32] += sum[i];
 }
 
 // ------------------------------------------------------------------ pool

@@ -269,8 +269,8 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   p.parts = few ? moba::Kv4Few::WARPS : chunk ? 1 : moba::Kv4Many::WARPS;
   p.steps = chunk ? 1 : 0;
   const int64_t nu = slots * heads_kv;
-  // items (half tiles, or steps of two tiles) and the ends of all ranges are counted in 31 bits
-  const int64_t items = chunk ? (p.tiles + 1) / 2 : 2 * p.tiles;
+  // items (tiles, or steps of two tiles) and the ends of all ranges are counted in 31 bits
+  const int64_t items = chunk ? (p.tiles + 1) / 2 : p.tiles;
   if (nu * items > ((int64_t)1 << 30)) return fail(MOBA_ERR_UNSUPPORTED, "too many (row, key) tiles");
   p.list_cap = kmean ? (int)std::min<int64_t>(p.blocks, (int64_t)p.R * topk) : 0;
   // the gate: up to 8 CTAs share a unit's scores while there are few units
@@ -284,8 +284,8 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   const size_t o_scores = c.take((size_t)clusters * p.R * p.means * 8);
   const size_t o_part = c.take((size_t)2 * p.ctas * p.R * 130 * 4);
   // the scores of few rows are kept for their weights, up to a GiB of them
-  const int64_t most = kmean ? std::min<int64_t>(items, (int64_t)2 * p.list_cap * (block_size / moba::kKv4Tile)) : items;
-  const size_t seen = few && acc ? (size_t)nu * most * 4 * moba::kKv4HalfTok * 8 : 0;
+  const int64_t most = kmean ? std::min<int64_t>(items, (int64_t)p.list_cap * (block_size / moba::kKv4Tile)) : items;
+  const size_t seen = few && acc ? (size_t)nu * most * 4 * moba::kKv4Tile * 8 : 0;
   const bool keep = seen > 0 && seen <= ((size_t)1 << 30);
   const size_t o_seen = c.take(keep ? seen : 0);
   const size_t o_qtiles = c.take(chunk ? (size_t)nu * 2 * moba::kKv4TileOp : 0);
