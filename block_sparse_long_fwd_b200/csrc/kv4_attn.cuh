@@ -509,8 +509,8 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t t
 __device__ __forceinline__ Kv4Par kv4_par(uint32_t pp) {
   Kv4Par r;
   r.t = h2_mul(pp & 0x7F807F80u, 0x24002400u);  // 2^-6
-  r.tz = h2_mul(and_or(pp << 4, 0x00F000F0u, 0xD400D400u), r.t);
   r.z = and_or(pp, 0x000F000Fu, 0x64006400u);
+  r.tz = h2_mul(h2_sub(0x63806380u, r.z), r.t);  // 960 - (1024 + z)
   return r;
 }
 // t (c - z) for nibbles 0..3 of both halves of a word.
@@ -532,6 +532,19 @@ __device__ __forceinline__ float kv4_query_scale(uint32_t top, float scale_log2,
   f1 = __int_as_float((127 + k1) << 23);
   f2 = __int_as_float((127 + k2) << 23);
   return 64.f * scale_log2 * __int_as_float((127 - k1) << 23) * __int_as_float((127 - k2) << 23);
+}
+
+// The same for a word of one token, the first (HI = 0) or second of the two that
+// the parameters are of: fp16 instructions take either half twice for free.
+template <int HI>
+__device__ __forceinline__ uint32_t h2_half(uint32_t x) {
+  const __half2 h = *reinterpret_cast<const __half2*>(&x), y = HI ? __high2half2(h) : __low2half2(h);
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+template <int HI>
+__device__ __forceinline__ void kv4_pairs_of(uint32_t w, const Kv4Par& p, uint32_t (&x)[4]) {
+  const Kv4Par q = {h2_half<HI>(p.t), h2_half<HI>(p.tz), h2_half<HI>(p.z)};
+  kv4_pairs(w, q, x);
 }
 
 // A query row enters the products as fp16: times the power of two that brings
@@ -738,13 +751,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
         const uint4 wb = *reinterpret_cast<const uint4*>(kt + tb * kKv4Row + qd * 16);
         const uint32_t pa = *reinterpret_cast<const uint16_t*>(kt + kKv4Params + ta * 8 + qd * 2);
         const uint32_t pb = *reinterpret_cast<const uint16_t*>(kt + kKv4Params + tb * 8 + qd * 2);
-        const Kv4Par fa = kv4_par(__byte_perm(pa, 0, 0x1010)), fb = kv4_par(__byte_perm(pb, 0, 0x1010));
+        const Kv4Par f = kv4_par(__byte_perm(pa, pb, 0x5410));
         const uint32_t xa[4] = {wa.x, wa.y, wa.z, wa.w}, xb[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t a[4], b[4];
-          kv4_pairs(xa[w], fa, a);
-          kv4_pairs(xb[w], fb, b);
+          kv4_pairs_of<0>(xa[w], f, a);
+          kv4_pairs_of<1>(xb[w], f, b);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             uint2 q0, q1;
