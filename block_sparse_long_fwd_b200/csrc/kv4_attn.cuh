@@ -120,9 +120,9 @@ __device__ __forceinline__ int kv4_items(const Kv4AttnParams& p, const Kv4Unit& 
 constexpr int kKv4GateThreads = 256;
 constexpr int kKv4GateRegs = 8;  // scores a lane keeps: rows with up to 256 past blocks select from registers
 
-// A score as an integer of the same order.
+// A score as an integer of the same order, -0 as 0.
 __device__ __forceinline__ uint64_t kv4_score_key(double s) {
-  const uint64_t u = __double_as_longlong(s);
+  const uint64_t u = __double_as_longlong(s + 0.);
   return u >> 63 ? ~u : u | 1ull << 63;
 }
 
@@ -1362,13 +1362,16 @@ __global__ void __launch_bounds__(kKv4PoolThreads, 2) kv4_pool_kernel(Kv4PoolPar
   issue(0);
   issue(1);
   float o[8][4] = {}, oz[4] = {};
-  bool dead = false;
   for (int k = 0; k < n; ++k) {
     issue(k + 2);
     const int d = k % kKv4PoolStages;
-    // a wait that ran out is followed by those for the copies under way, so that none outlives the block
-    if (!mbar_wait(&full[warp][d], (k / kKv4PoolStages) & 1, &abort_flag)) dead = true;
-    if (dead) continue;
+    if (!mbar_wait(&full[warp][d], (k / kKv4PoolStages) & 1, &abort_flag)) {
+      // the block's shared memory lives until the copies under way have landed
+      volatile int keep_waiting = 0;
+      for (int i = k; i < min(n, k + 3); ++i)
+        mbar_wait(&full[warp][i % kKv4PoolStages], (i / kKv4PoolStages) & 1, &keep_waiting, 1ull << 28);
+      break;
+    }
     const uint8_t* tile = ring + d * kKv4Half;
 #pragma unroll
     for (int g = 0; g < kKv4Tile / 16; ++g) {

@@ -175,6 +175,18 @@ def test_pool_gives_the_means_of_complete_blocks(hkv, lengths, block):
         assert (f64(m[b])[:, L // block:] == 0).all()
 
 
+@pytest.mark.parametrize("block", [1536, 4096, 8192])
+def test_pool_of_large_blocks_by_several_ctas(block):
+    hkv, cap, lengths = 2, 8192, [8192, 5000]
+    kv4, vals = random_cache(lengths, hkv, cap, 12)
+    m = moba.kv4_pool(kv4, ints(lengths), block)
+    ok()
+    for b, L in enumerate(lengths):
+        want, size = (ref.means(x, L, block, cap // block) for x in (vals[b][0], np.abs(vals[b][0])))
+        assert (np.abs(f64(m[b]) - want) <= (block + 1) * U * size).all()
+        assert (f64(m[b])[:, L // block:] == 0).all()
+
+
 def test_pool_of_less_than_a_block_is_empty():
     kv4, _ = random_cache([64], 1, 64, 1)
     assert moba.kv4_pool(kv4, ints([64]), 128).shape == (1, 1, 0, 128)
@@ -218,10 +230,14 @@ def check_attend(got, q, vals, lengths, news, hkv, sparse=None, kmean=None, rows
         t += n
 
 
-def attend_case(hkv, G, lengths, news, sparse=None, acc=True, seed=0, cap=None, qscale=1.0, pad=3):
+def attend_case(hkv, G, lengths, news, sparse=None, acc=True, seed=0, cap=None, qscale=1.0, pad=3, distinct=None):
+    """distinct: so many different sequences, one after the other again and again."""
     rng = np.random.default_rng(seed + 100)
     cap = cap or -(-max(max(lengths), 1) // 64) * 64 + 64
-    kv4, vals = random_cache(lengths, hkv, cap, seed)
+    kv4, vals = random_cache(lengths[:distinct], hkv, cap, seed)
+    if distinct:
+        at = np.arange(len(lengths)) % distinct
+        kv4, vals = kv4[torch.from_numpy(at).cuda()], [vals[i] for i in at]
     T = sum(news)
     q = bf16(rng.standard_normal((T + pad, hkv * G, 128)) * qscale)
     kmean = moba.kv4_pool(kv4, ints(lengths), sparse[0]) if sparse else None
@@ -281,6 +297,16 @@ def test_many_short_sequences_with_empty_ones_between():
     attend_case(1, 2, lengths, [1] * 700, acc=False, seed=1, cap=128)  # a query without keys for each empty one
 
 
+def test_more_sequences_than_a_cta_copies():
+    # the offsets and lengths of 9000 sequences do not fit beside the pieces: they are read where they lie
+    attend_case(1, 2, [1 + 7 * i % 64 for i in range(9000)], [1] * 9000, acc=False, seed=4, cap=64, distinct=16)
+
+
+def test_many_sequences_with_many_rows_each():
+    # a CTA of the kernel for many rows walks over more units than it keeps beside it
+    attend_case(1, 7, [20 + i % 45 for i in range(2600)], [7 + i % 2 for i in range(2600)], seed=5, cap=64, distinct=16)
+
+
 SPARSE = [
     # hkv, G, lengths, new tokens, block, topk
     (1, 1, [1], [1], 128, 2),
@@ -295,6 +321,8 @@ SPARSE = [
     (1, 16, [1100], [5], 128, 3),
     (1, 4, [700, 0, 3], [3, 0, 4], 128, 2),
     (1, 2, [600], [1], 128, 1),
+    (1, 2, [40000], [3], 128, 5),               # more past blocks than a warp keeps in registers
+    (2, 1, [50 + i % 400 for i in range(300)], [1] * 300, 128, 2),  # more sequences than the gate copies
 ]
 
 
@@ -342,6 +370,21 @@ def test_equal_scores_go_to_the_lower_block():
     out, _ = moba.kv4_attend(q, kv4, length, kmean=moba.kv4_pool(kv4, length, B), block_size=B, topk=3)
     ok()
     assert set(np.nonzero(f64(out)[0, 0] > 0)[0]) == {1, 3, 6}
+
+
+def test_zero_scores_of_either_sign_are_equal():
+    # a query of zeros scores -0 against a mean of negative numbers: a tie all the same
+    cap, B = 1024, 128
+    k = np.ones((1, cap, 128))
+    k[:, :2 * B] = -1
+    v = np.zeros((1, cap, 128))
+    v[0] = (np.arange(cap) // B)[:, None] == np.arange(128)
+    kv4 = torch.from_numpy(ref.pack(k, v)[None]).cuda()
+    q = torch.zeros(1, 1, 128, dtype=torch.bfloat16, device="cuda")
+    length = ints([6 * B + 1])
+    out, _ = moba.kv4_attend(q, kv4, length, kmean=moba.kv4_pool(kv4, length, B), block_size=B, topk=3)
+    ok()
+    assert set(np.nonzero(f64(out)[0, 0] > 0)[0]) == {0, 1, 6}
 
 
 def test_garbage_behind_the_last_token_is_not_read_into_results():
@@ -485,6 +528,31 @@ def test_evict_of_awkward_weights(kind):
            "special": lambda: rng.choice([np.nan, np.inf, -np.inf, 0.0, 1e-45, 1.0], (1, 2, cap)),
            "close": lambda: 1.0 + rng.integers(0, 4, (1, 2, cap)) * 2.0**-23}[kind]()
     evict_case(2, [2000], 700, 33, acc, cap, 704, seed=1)
+
+
+@pytest.mark.parametrize("hkv,length,budget,recent,distinct", [
+    (1, 300000, 5000, 100, 1 << 20), (1, 300000, 299000, 0, 1 << 20), (1, 280001, 70000, 64, 50), (160, 33000, 900, 10, 1 << 20),
+])
+def test_evict_from_long_caches(hkv, length, budget, recent, distinct):
+    # parts longer than one sweep of a CTA, read again in each pass; whatever the cache holds is moved as it is
+    cap, dcap = -(-length // 64) * 64, -(-budget // 64) * 64
+    g = torch.Generator(device="cuda").manual_seed(7)
+    kv4 = torch.randint(0, 256, (1, hkv, cap // 64, 9216), dtype=torch.uint8, device="cuda", generator=g)
+    acc = torch.randint(0, distinct, (1, hkv, cap), device="cuda", generator=g).float()
+    dst, dst_acc = moba.kv4_cache(1, hkv, dcap), torch.zeros(1, hkv, dcap, device="cuda")
+    new, kept = moba.kv4_evict(kv4, acc, ints([length]), budget, recent, dst, dst_acc)
+    ok()
+    assert new.tolist() == [budget]
+    for h in range(0, hkv, 40):
+        want = ref.evict(f64(acc[0, h]), length, budget, recent)
+        assert np.array_equal(kept[0, h].cpu().numpy(), want)
+        assert np.array_equal(dst_acc[0, h, :budget].cpu().numpy(), acc[0, h].cpu().numpy()[want])
+        src, to = kv4[0, h].cpu().numpy(), dst[0, h].cpu().numpy()
+        for new_at, old_at in [(i, want[i]) for i in (0, 1, budget // 2, budget - 1)]:
+            for off in (0, 4096):  # keys: codes and parameters (the values' codes change places with the token's index)
+                n = 64 if off == 0 else 8
+                a, b = off + n * (old_at % 64), off + n * (new_at % 64)
+                assert np.array_equal(src[old_at // 64, a:a + n], to[new_at // 64, b:b + n])
 
 
 # ------------------------------------------------------------------ together, streams, graphs
