@@ -51,7 +51,7 @@ struct Kv4AttnParams {
   float* seen;                  // or null: [items][4][64][2] log2 scores, of each tile's keys and two rows
   float* part;                  // [2 * ctas][R * 130]: O, then m and l
   int list_cap, ctas;
-  int parts;                    // ranges of a CTA
+  int least;                    // items of a CTA that has any
   int steps;                    // ranges are dealt out in steps of 128 keys (else in tiles)
   uint8_t* qtiles;              // [slots * Hkv][2][32768]: query tiles as fp16 operands
   float* qscale;                // [slots * Hkv][256]: their rows' scales
@@ -297,11 +297,10 @@ __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams
 
 // ------------------------------------------------------------------ plan
 
-// Items of a part's range: the same for all but the last that has any. (Items
+// Items of a CTA's range: the same for all but the last that has any. (Items
 // fit 31 bits: the host sees to it.)
 __device__ __forceinline__ int kv4_quota(const Kv4AttnParams& p, int all) {
-  const uint32_t n = p.ctas * p.parts;
-  return (int)(((uint32_t)all + n - 1) / n);
+  return max((all + p.ctas - 1) / p.ctas, p.least);
 }
 
 // Where each part's range begins (a part is a warp, or the CTA): every CTA scans all units' tiles for itself
@@ -408,8 +407,8 @@ __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* co
       before = s - x + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? y : 0);
       all = __reduce_add_sync(0xFFFFFFFFu, y);
       quota = kv4_quota(p, all);
-      lo = (int)min((int64_t)cta * PARTS * quota, (int64_t)all);
-      hi = min(lo + PARTS * quota, all);
+      lo = (int)min((int64_t)cta * quota, (int64_t)all);
+      hi = min(lo + quota, all);
       if (cta == 0 && tid == 0) p.before[nu] = all;
     } else {
       __syncthreads();
@@ -421,12 +420,13 @@ __device__ __forceinline__ Kv4Range kv4_plan(const Kv4AttnParams& p, int32_t* co
   g.units = p.units;
   g.first = s_first;
   g.any = hi > lo;
-  g.n = max(0, min(quota, hi - lo - part * quota));
-  g.item = lo + part * quota;
+  const int even = (hi - lo) / PARTS, more = (hi - lo) % PARTS;  // the first `more` parts take one item more
+  g.n = even + (part < more ? 1 : 0);
+  g.item = lo + part * even + min(part, more);
   g.unit = g.off = 0;
   if (g.n) {
     // the unit that this part begins in: among the kept ones, a lane each, or further on
-    const int start = lo + part * quota;
+    const int start = g.item;
     const bool in = lane < kKv4Kept && s_kept[lane].tiles && s_at[lane] <= start &&
                     start < s_at[lane] + kv4_items(p, s_kept[lane]);
     const uint32_t found = __ballot_sync(0xFFFFFFFFu, in);
@@ -1049,7 +1049,7 @@ __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams
   int c0 = 0, c1 = -1;
   if (u.tiles) {
     const int all = p.before[p.slots * p.Hkv], x = p.before[ui];
-    const int per_cta = kv4_quota(p, all) * p.parts;
+    const int per_cta = kv4_quota(p, all);
     c0 = x / per_cta;
     c1 = (x + kv4_items(p, u) - 1) / per_cta;
     if (c0 == c1) return;  // written by the CTA itself

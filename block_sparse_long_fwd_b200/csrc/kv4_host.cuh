@@ -266,7 +266,7 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   if (slots * heads_kv * p.R > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
   p.slots = (int)slots;
   p.ctas = dev.sms;
-  p.parts = few ? moba::Kv4Few::WARPS : chunk ? 1 : moba::Kv4Many::WARPS;
+  p.least = chunk ? 1 : 4;
   p.steps = chunk ? 1 : 0;
   const int64_t nu = slots * heads_kv;
   // items (tiles, or steps of two tiles) and the ends of all ranges are counted in 31 bits
