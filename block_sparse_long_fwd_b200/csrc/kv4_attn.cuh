@@ -10,9 +10,10 @@
 // Work is cut into units: R consecutive rows (token, q head of one kv head) of
 // one sequence and kv head, with the 64-token tiles of the cache that at least
 // one of them attends. All units' tiles in a row are dealt out evenly, one
-// contiguous range to each warp of a grid of one CTA per SM, wherever the units begin and end: lengths that differ, and few units with
-// many tiles, balance by themselves. A unit that several warps share is joined
-// in shared memory, and by a second kernel where it crosses CTAs.
+// contiguous range to each CTA of a grid of one CTA per SM, and of that one to
+// each warp, wherever the units begin and end: lengths that differ, and few
+// units with many tiles, balance by themselves. A unit that several warps share
+// is joined in shared memory, and by a second kernel where it crosses CTAs.
 #pragma once
 
 #include "kv4.cuh"
@@ -140,7 +141,8 @@ __device__ __forceinline__ void kv4_warp_best(uint64_t& key, int& j) {
 // for all rows of the unit, the first CTA selects and lists. Scores are sums
 // in fp64 of products that are exact there (bf16 times fp32), so near ties
 // fall as in exact arithmetic; they are a few per cent of the work of the
-// attention itself (one mean per block of at least 128 keys).
+// attention itself (one mean per block of at least 128 keys). Latency-bound:
+// 14 us for 255 past blocks and 4 rows of each of 8 kv heads.
 __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
   extern __shared__ uint32_t picked[];  // [blocks]: rows of the unit that chose the block
@@ -303,9 +305,10 @@ __device__ __forceinline__ int kv4_quota(const Kv4AttnParams& p, int all) {
   return max((all + p.ctas - 1) / p.ctas, p.least);
 }
 
-// Where each part's range begins (a part is a warp, or the CTA): every CTA scans all units' tiles for itself
-// (they follow from the lengths alone, or the gate has left them), which is
-// a round trip to L2 where a kernel of its own was 6 to 9 us with its launch.
+// Where each part's range begins (a part is a warp, or the CTA): every CTA scans
+// all units' tiles for itself (they follow from the lengths alone, or the gate
+// has left them): 3 us for one sequence of 8 kv heads, 5 for 64, where a kernel
+// of its own was 6 to 9 us with its launch.
 // The units that the CTA's range touches, and the items before them, are
 // left in scratch for the rest of the CTA and for the join (units of several
 // CTAs get the same values from each); CTA 0 leaves those without tiles.
@@ -490,13 +493,16 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
   return d;
 }
 
-// A nibble at bit 4 under fp16's 64 is 64 + c, and t (64 + c) - t (64 + z) is
-// one fused multiply-add without a rounding: 64 + z has seven significant bits
-// and t four, so the product fits fp16's eleven, and the difference is
-// t (c - z). (A nibble at bit 0 stands under 1024: eleven bits and four, so a
-// subtraction and a multiplication for each pair instead, and the kernel is
-// bound by instructions.) t is a 64th of the scale, so that t (64 + z) stays
-// below fp16's largest number; t is a multiple of 2^-23, so all stays exact.
+// t (c - z) from codes, without a rounding. A nibble at bit 4 under fp16's 64 is
+// 64 + c, and t (64 + c) - t (64 + z) is one fused multiply-add: 64 + z has
+// seven significant bits and t four, so the product fits fp16's eleven. A nibble
+// at bit 0 stands under 1024, whose eleven bits and t's four do not fit: a
+// subtraction and a multiplication. Shifting nibbles 0 and 2 up to bit 4 would
+// cost as much and one register more (1M tokens of 8 heads 263 against 265 us);
+// zero points taken off by a product of their own, which leaves masks and
+// multiplications, were no faster (274 against 267) and cancel digits. t is a
+// 64th of the scale, so that t (64 + z) stays below fp16's largest number; t is
+// a multiple of 2^-23, so all stays exact.
 struct Kv4Par {
   uint32_t t, tz, z;  // t, -t (64 + z) and 1024 + z, of two tokens (or of one, twice)
 };
@@ -624,6 +630,15 @@ using Kv4Many = Kv4Cfg<2, 8, false>;   // up to 16 rows
 
 constexpr float kKv4Low = -1e30f;  // running maximum before the first score
 
+// Per tile of 64 keys a warp widens the keys' codes into the A operand of
+// S^T = K Q^T (keys x rows; the codes' own order is the operand's), finds the
+// weights in registers, transposes them 8 x 8, and widens the values' codes into
+// the A operand of O^T += V^T P^T. 16 warps of 128 registers (12 of 168 took 276
+// us where these took 262). Bound by the issue slots, not HBM: 311 instructions
+// for 16 keys and up to 8 rows. 1M tokens of 8 heads: 238 us, 5.1 TB/s, 78 % of
+// a copy's rate. Where there are few tiles the chain counts: 12 us for 4096
+// tokens of one head; 47 for 128K tokens of 8, of which the plan takes 4, the
+// tiles 27 and the two joins 6.
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p) {
   constexpr int NT = C::NT, R = C::R;
@@ -642,7 +657,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
   const int n = range.n;
 
   // A warp fetches its own tiles, one bulk copy for the keys and one for the values of each (32 tokens at a time, four
-  // copies and two ahead, cost 30 instructions more for 16 keys: 265 against ... us at 1M tokens). `next` walks the
+  // copies and two ahead, cost 30 instructions more for 16 keys: 265 against 247 us at 1M tokens). `next` walks the
   // units to the next tile.
   const int tpb = p.B / kKv4Tile;
   int c_ui = range.unit - 1, c_off = range.off, c_left = n, c_end = 0, c_at = 0, c_in = 0;
@@ -1037,7 +1052,7 @@ constexpr int kKv4JoinThreads = 128;
 // of its warps takes every fourth partial result, all at once (a loop that
 // carries the maximum along waits for each in turn: 38 us for 64 of them
 // against 4), and the four sums meet in a fixed order. Rows without keys get
-// their zero here.
+// their zero here. 2048 rows of 8 kv heads over 32K tokens: 29 us, 28 MB.
 __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
   __shared__ float s_l[kKv4JoinThreads / 32];
@@ -1099,7 +1114,8 @@ constexpr int kKv4WeightThreads = 128, kKv4WeightTiles = 8;
 // of four warps per SM), else widened for each eight rows, and a warp goes
 // through kKv4WeightTiles tiles, with the rows' fragments kept where there are
 // at most eight rows (few rows: what counts is how many warps have loads under
-// way, and what a tile costs beside them).
+// way, and what a tile costs beside them; taken only where their scores would
+// fill more scratch than kv4_seen_kernel may have).
 template <bool HOLD>
 __global__ void __launch_bounds__(kKv4WeightThreads, HOLD ? 2 : 5) kv4_weight_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
@@ -1238,9 +1254,10 @@ __global__ void __launch_bounds__(kKv4WeightThreads, HOLD ? 2 : 5) kv4_weight_ke
 constexpr int kKv4SeenThreads = 128, kKv4SeenKeys = 1024;
 
 // The same from the scores that the attention has left: 4 bytes written and
-// read a row and key, against 72 read again and widened a key (at 128K tokens of
-// 8 heads, 4 rows each: 8 against 28 us, and 1 us more in the attention). A warp takes 256 keys
-// of a kv head, a lane a key, over the units of the sequence in order.
+// read a row and key, against 72 read again and widened a key. Whole calls: 128K
+// tokens of 8 heads, 4 rows each, 68 us against 79; 8 such sequences of 12 chosen
+// blocks 242 against 297. A warp takes 256 keys of a kv head, a lane a key, over
+// the units of the sequence in order.
 __global__ void __launch_bounds__(kKv4SeenThreads) kv4_seen_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
   const int lane = threadIdx.x & 31, b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;
@@ -1314,8 +1331,8 @@ constexpr int kKv4PoolThreads = 256, kKv4PoolStages = 3;
 
 // A cluster of CTAs per (block, head, sequence), a part of the block's tiles
 // each; each warp brings its tiles of keys into a ring of its own, one bulk
-// copy each, two ahead (with loads into registers instead, 16 warps of two
-// groups of tokens at a time, 128K tokens of 8 heads took 27 us).
+// copy each, two ahead (128K tokens of 8 heads: 18 us a call, 4.2 TB/s in a
+// short kernel, 27 with loads into registers, two groups of tokens a warp).
 // The tensor core sums in fp32: codes, as they stand in a word, are fp16
 // subnormals (a nibble at bit 0 is c 2^-24, at bit 4 c 2^-20), so a mask is all
 // that they need; they meet the scales of the four groups in four columns, of
