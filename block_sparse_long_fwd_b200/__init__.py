@@ -292,11 +292,13 @@ def _on(x, name: str, dtype, shape, device: int):
 
 def _call(device: int, stream, fn, *args) -> None:
     """fn(*args, stream) with `device` current (a switch only when another one is)."""
+    # the current stream's handle as such: the object around it would cost a microsecond, a tenth of a small call
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == device:
-        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream))
+        _check(fn(*args, raw))
         return
     with torch.cuda.device(device):
-        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream))
+        _check(fn(*args, raw))
 
 
 def kv4_append(k: torch.Tensor, v: torch.Tensor, kv4: torch.Tensor, start: torch.Tensor, cu=None, acc=None,
@@ -331,7 +333,7 @@ def kv4_load(kv4: torch.Tensor, lengths: torch.Tensor, n: int, first=None, strea
     fp = _on(first, "first", torch.int32, (batch,), dev)
     if not 0 <= n <= cap:
         raise ValueError("n must be in [0, capacity]")
-    k = torch.empty((batch, n, hkv, HEAD_DIM), dtype=torch.bfloat16, device=kv4.device)
+    k = kv4.new_empty((batch, n, hkv, HEAD_DIM), dtype=torch.bfloat16)
     v = torch.empty_like(k)
     if n:
         _call(dev, stream, lib().moba_kv4_load, kv4.data_ptr(), lp, fp, batch, hkv, HEAD_DIM, cap, n, k.data_ptr(),
@@ -349,8 +351,10 @@ def kv4_pool(kv4: torch.Tensor, lengths: torch.Tensor, block_size: int, kmean=No
         raise ValueError("block_size must be positive")
     shape = (batch, hkv, cap // block_size, HEAD_DIM)
     if kmean is None:
-        kmean = torch.empty(shape, dtype=torch.float32, device=kv4.device)
-    mp = _on(kmean, "kmean", torch.float32, shape, dev)
+        kmean = kv4.new_empty(shape, dtype=torch.float32)
+        mp = kmean.data_ptr()
+    else:
+        mp = _on(kmean, "kmean", torch.float32, shape, dev)
     if shape[2]:
         _call(dev, stream, lib().moba_kv4_pool, kv4.data_ptr(), lp, batch, hkv, HEAD_DIM, cap, block_size, mp)
     return kmean
@@ -384,10 +388,16 @@ def kv4_attend(q: torch.Tensor, kv4: torch.Tensor, lengths: torch.Tensor, cu=Non
         mp = mp if kmean.numel() else None  # less than a block of room: every key is in the own block
     elif block_size or topk:
         raise ValueError("block_size and topk need kmean")
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((hq, T), dtype=torch.float32, device=kv4.device) if lse is None else lse
-    op = _on(out, "out", torch.bfloat16, (T, hq, HEAD_DIM), dev)
-    ep = _on(lse, "lse", torch.float32, (hq, T), dev)
+    if out is None:
+        out = torch.empty_like(q)
+        op = out.data_ptr()
+    else:
+        op = _on(out, "out", torch.bfloat16, (T, hq, HEAD_DIM), dev)
+    if lse is None:
+        lse = kv4.new_empty((hq, T), dtype=torch.float32)
+        ep = lse.data_ptr()
+    else:
+        ep = _on(lse, "lse", torch.float32, (hq, T), dev)
     if T:
         _call(dev, stream, lib().moba_kv4_attend, qp, T, cp, kv4.data_ptr(), lp, mp, batch, hq, hkv, HEAD_DIM, cap,
               block_size, topk, ap, op, ep)
@@ -416,7 +426,7 @@ def kv4_evict(kv4: torch.Tensor, acc: torch.Tensor, lengths: torch.Tensor, budge
     if not 1 <= budget <= dcap or not 0 <= recent <= budget:
         raise ValueError("budget must be in [1, dst's capacity] and recent in [0, budget]")
     new = torch.empty_like(lengths)
-    kept = torch.empty((batch, hkv, budget), dtype=torch.int32, device=kv4.device)
+    kept = lengths.new_empty((batch, hkv, budget))
     _call(dev, stream, lib().moba_kv4_evict, kv4.data_ptr(), ap, lp, batch, hkv, HEAD_DIM, cap, budget, recent,
           dst.data_ptr(), dp, dcap, kept.data_ptr(), new.data_ptr())
     return new, kept

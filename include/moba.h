@@ -396,6 +396,10 @@ int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch,
  * acc        if not NULL: acc[b][g][j] += the sum, over the query rows of
  *            the sequence and the q heads of kv head g, of the softmax weight
  *            of token j. In a fixed order.
+ *            (With at most 8 rows a sequence and kv head on average, their
+ *            scores stay in scratch until then: 32 bytes a sequence, kv head
+ *            and token of the capacity, or of the chosen blocks, up to 1 GiB;
+ *            where they would need more, they are computed again.)
  * out        device bf16 output [total][heads_q][head_dim].
  * lse        device fp32 output [heads_q][total], natural log.
  */
