@@ -1048,17 +1048,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
 
 constexpr int kKv4JoinThreads = 128;
 
-// One CTA per (unit, row) whose tiles lie in more than one CTA's range: each
-// of its warps takes every fourth partial result, all at once (a loop that
-// carries the maximum along waits for each in turn: 38 us for 64 of them
-// against 4), and the four sums meet in a fixed order. Rows without keys get
-// their zero here. 2048 rows of 8 kv heads over 32K tokens: 29 us, 28 MB.
+// SPLIT warps per (unit, row) whose tiles lie in more than one CTA's range: each
+// takes every SPLIT-th partial result, all at once (a loop that carries the
+// maximum along waits for each in turn: 38 us for 64 of them against 4), and the
+// sums meet in a fixed order. Rows without keys get their zero here. With one
+// warp a row (few partial results each), 2048 rows of 8 kv heads over 32K tokens
+// take JOIN1 us for 28 MB, with four 29; with four (many results), 4 rows of 8 kv
+// heads over 128K tokens JOIN4.
+template <int SPLIT>
 __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
-  __shared__ float s_l[kKv4JoinThreads / 32];
-  __shared__ float4 s_o[kKv4JoinThreads / 32][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ui = blockIdx.x / p.R, row = blockIdx.x % p.R;
+  __shared__ float s_l[SPLIT];
+  __shared__ float4 s_o[SPLIT][32];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % SPLIT;
+  const int item = blockIdx.x * (kKv4JoinThreads / 32 / SPLIT) + (threadIdx.x >> 5) / SPLIT;
+  const int ui = item / p.R, row = item % p.R;
   const Kv4Unit u = p.units[ui];
   if (row >= u.rows) return;
   int c0 = 0, c1 = -1;
@@ -1079,7 +1083,7 @@ __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams
   float ll = 0.f;
   float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int c = c0 + warp; c <= c1; c += 4) {
+  for (int c = c0 + warp; c <= c1; c += SPLIT) {
     const float2 x = ml(c);
     const float4 v = __ldcg(reinterpret_cast<const float4*>(part(c) + row * kHeadDim) + lane);
     const float e = ex2_approx(x.x - mm);
@@ -1089,17 +1093,19 @@ __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams
     oo.z = fmaf(v.z, e, oo.z);
     oo.w = fmaf(v.w, e, oo.w);
   }
-  s_o[warp][lane] = oo;
-  if (lane == 0) s_l[warp] = ll;
-  __syncthreads();
-  if (warp) return;
-  for (int w = 1; w < kKv4JoinThreads / 32; ++w) {
-    const float4 v = s_o[w][lane];
-    ll += s_l[w];
-    oo.x += v.x;
-    oo.y += v.y;
-    oo.z += v.z;
-    oo.w += v.w;
+  if constexpr (SPLIT > 1) {
+    s_o[warp][lane] = oo;
+    if (lane == 0) s_l[warp] = ll;
+    __syncthreads();
+    if (warp) return;
+    for (int w = 1; w < SPLIT; ++w) {
+      const float4 v = s_o[w][lane];
+      ll += s_l[w];
+      oo.x += v.x;
+      oo.y += v.y;
+      oo.z += v.z;
+      oo.w += v.w;
+    }
   }
   kv4_write_row(p, u, row, lane, mm, ll, oo);
 }
@@ -1268,6 +1274,7 @@ __global__ void __launch_bounds__(kKv4SeenThreads) kv4_seen_kernel(Kv4AttnParams
   if (n == 0 || first >= len) return;
   constexpr int PARTS = kKv4SeenKeys / (kKv4SeenThreads / 32) / 32;
   float sum[PARTS] = {};
+  uint32_t touched = 0;  // parts that a unit attends
   const int slot0 = kv4_first_slot(p, b, t0), tpb = p.B / kKv4Tile;
   for (int row0 = 0; row0 < n * p.G; row0 += p.R) {
     const int ui = (slot0 + (row0 >> p.rshift)) * p.Hkv + h;
@@ -1284,8 +1291,8 @@ __global__ void __launch_bounds__(kKv4SeenThreads) kv4_seen_kernel(Kv4AttnParams
     }
     int block = -1, at = -1;  // the block that was looked up, and its place in the list
 #pragma unroll
-    for (int i = 0; i < PARTS; ++i) {
-      const int key0 = first + i * 32;
+    for (int i0 = 0; i0 < PARTS; i0 += 4) {  // 128 keys: two tiles of one block
+      const int key0 = first + i0 * 32;
       int tile = key0 / kKv4Tile;
       if (key0 >= len) break;
       if (p.kmean) {
@@ -1300,21 +1307,31 @@ __global__ void __launch_bounds__(kKv4SeenThreads) kv4_seen_kernel(Kv4AttnParams
         tile = at * tpb + tile % tpb;
       }
       if (tile >= u.tiles) continue;
-      const float2* from = reinterpret_cast<const float2*>(p.seen) + (int64_t)(before + tile) * 4 * kKv4Tile +
-                           key0 % kKv4Tile + lane;
+      touched |= 1u << i0;
+      const float2* from = reinterpret_cast<const float2*>(p.seen) + (int64_t)(before + tile) * 4 * kKv4Tile + lane;
+      float2 z[4][4];  // all under way at once
 #pragma unroll
-      for (int r = 0; r < 8; r += 2) {
-        if (r >= u.rows) break;
-        const float2 s = __ldcs(from + r / 2 * kKv4Tile);
-        sum[i] += ex2_approx(s.x - le[r]);
-        if (r + 1 < u.rows) sum[i] += ex2_approx(s.y - le[r + 1]);
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          z[i][r] = 2 * r < u.rows && tile + i / 2 < u.tiles
+                        ? __ldcs(from + (i / 2 * 4 + r) * kKv4Tile + i % 2 * 32)
+                        : make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (2 * r >= u.rows) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[i0 + i] += ex2_approx(z[i][r].x - le[2 * r]);
+          if (2 * r + 1 < u.rows) sum[i0 + i] += ex2_approx(z[i][r].y - le[2 * r + 1]);
+        }
       }
     }
   }
   float* acc = p.acc + ((int64_t)b * p.Hkv + h) * p.tiles * kKv4Tile + first + lane;
 #pragma unroll
   for (int i = 0; i < PARTS; ++i)
-    if (first + i * 32 + lane < len) acc[i * 32] += sum[i];
+    if (touched >> (i & ~3) & 1u && first + i * 32 + lane < len) acc[i * 32] += sum[i];
 }
 
 // ------------------------------------------------------------------ pool

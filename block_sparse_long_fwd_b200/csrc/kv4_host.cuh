@@ -315,7 +315,12 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
     } else {
       launch_kv4_attn<moba::Kv4Many>(p, st);
     }
-    launch_chained(moba::kv4_join_kernel, dim3((unsigned)(nu * p.R)), dim3(moba::kKv4JoinThreads), 0, st, p);
+    // a unit's partial results come from about ctas / nu CTAs and one or two at its ends
+    constexpr int split = moba::kKv4JoinThreads / 32;
+    if (nu * 4 < p.ctas)
+      launch_chained(moba::kv4_join_kernel<split>, dim3((unsigned)(nu * p.R)), dim3(moba::kKv4JoinThreads), 0, st, p);
+    else
+      launch_chained(moba::kv4_join_kernel<1>, dim3((unsigned)(nu * p.R / split)), dim3(moba::kKv4JoinThreads), 0, st, p);
     if (acc && chunk) {
       launch_chained(moba::kv4_chunk_weight_kernel, dim3((unsigned)((capacity + 255) / 256), batch * heads_kv),
                      dim3(moba::kKv4ColThreads), moba::kKv4ColSmemBytes, st, p);
