@@ -299,13 +299,9 @@ __device__ __forceinline__ uint32_t kv4_block_scan(uint32_t x, uint32_t* warp_su
   __syncthreads();
   if (lane == 31) warp_sums[warp] = s;
   __syncthreads();
-  uint32_t before = 0, all = 0;
-  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) {
-    if (i < warp) before += warp_sums[i];
-    all += warp_sums[i];
-  }
-  *total = all;
-  return before + s - x;
+  const uint32_t y = lane < (int)(blockDim.x >> 5) ? warp_sums[lane] : 0;
+  *total = __reduce_add_sync(0xFFFFFFFFu, y);
+  return __reduce_add_sync(0xFFFFFFFFu, lane < warp ? y : 0) + s - x;
 }
 
 __device__ __forceinline__ void kv4_cluster_sync() {
@@ -333,7 +329,7 @@ __device__ __forceinline__ void kv4_remote_st(uint32_t* p, uint32_t rank, uint32
 // through distributed shared memory); a last pass writes the kept indexes,
 // each thread's neighbouring weights at its place in the order. Bound by its
 // chain of passes, each a round of counts, two cluster barriers and a scan: 128K
-// weights of 8 heads 30 us, 32 sequences of 4608 and 8 heads 24 us.
+// weights of 8 heads 27 us, 32 sequences of 4608 and 8 heads 21 us.
 __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictParams p) {
   grid_dependency_sync();
   // neighbouring lanes count in copies of their own: weights crowd into few bins
@@ -489,26 +485,28 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
 
 constexpr int kKv4MoveThreads = 256;
 
-// Half a warp per kept token, four tokens at a time: codes, parameters and
-// weight. 148 bytes read and as many written a token; bound by its scattered
-// pieces of 64 and 8 bytes (32 sequences of up to 4096 kept tokens, 8 heads: 52
-// us; 8192 of 128K tokens, 8 heads: 11). Done by the selecting CTAs instead, the
-// first took 195 us a call against 177: too few loads under way.
+// Eight lanes per kept token, four tokens at a time: 16 bytes of codes each, the
+// parameters and the weight. 148 bytes read and as many written a token; bound by
+// its scattered pieces of 64 and 8 bytes (32 sequences of up to 4096 kept tokens,
+// 8 heads: 38 us, 52 with words of 4 bytes; 8192 of 128K tokens, 8 heads: 9).
+// Done by the selecting CTAs instead, the first took 195 us a call against 177:
+// too few loads under way.
 constexpr int kKv4MoveTokens = 4;
 __global__ void __launch_bounds__(kKv4MoveThreads) kv4_move_kernel(Kv4EvictParams p) {
   grid_dependency_sync();
-  const int lane = threadIdx.x & 15;
-  const int to0 = (int)(blockIdx.x * (kKv4MoveThreads / 16 * kKv4MoveTokens)) + (threadIdx.x >> 4);
+  const int lane = threadIdx.x & 7, vals = lane >> 2, c = lane & 3;  // four lanes for the keys, four for the values
+  const int to0 = (int)(blockIdx.x * (kKv4MoveThreads / 8 * kKv4MoveTokens)) + (threadIdx.x >> 3);
   const int64_t pair = blockIdx.y;  // sequence * heads + head
   const int32_t* kept = p.kept + pair * p.budget;
-  const uint8_t* src = p.kv4 + pair * p.tiles * kKv4TileBytes;
-  uint8_t* dst = p.dst + pair * p.dst_tiles * kKv4TileBytes;
+  const uint8_t* src = p.kv4 + pair * p.tiles * kKv4TileBytes + vals * kKv4Half;
+  uint8_t* dst = p.dst + pair * p.dst_tiles * kKv4TileBytes + vals * kKv4Half;
   int from[kKv4MoveTokens];
-  uint32_t word[kKv4MoveTokens][2], par[kKv4MoveTokens];
+  uint4 codes[kKv4MoveTokens];
+  uint2 par[kKv4MoveTokens];
   float weight[kKv4MoveTokens];
 #pragma unroll
   for (int i = 0; i < kKv4MoveTokens; ++i) {
-    const int to = to0 + i * (kKv4MoveThreads / 16);
+    const int to = to0 + i * (kKv4MoveThreads / 8);
     from[i] = to < p.budget ? kept[to] : -1;
   }
 #pragma unroll
@@ -516,24 +514,19 @@ __global__ void __launch_bounds__(kKv4MoveThreads) kv4_move_kernel(Kv4EvictParam
     if (from[i] < 0) continue;
     const uint8_t* t = src + (int64_t)(from[i] / kKv4Tile) * kKv4TileBytes;
     const int ft = from[i] % kKv4Tile;
-    word[i][0] = __ldg(reinterpret_cast<const uint32_t*>(t + kv4_word_off(ft, lane, false)));
-    word[i][1] = __ldg(reinterpret_cast<const uint32_t*>(t + kKv4Half + kv4_word_off(ft, lane, true)));
-    // lanes 0, 1: the keys' parameters; 2, 3: the values'
-    if (lane < 4)
-      par[i] = __ldg(reinterpret_cast<const uint32_t*>(t + (lane >> 1) * kKv4Half + kKv4Params + ft * 8 + (lane & 1) * 4));
-    if (lane == 4) weight[i] = __ldg(p.acc + pair * p.tiles * kKv4Tile + from[i]);
+    codes[i] = __ldg(reinterpret_cast<const uint4*>(t + kv4_word_off(ft, 4 * c, vals)));
+    if (c == 0) par[i] = __ldg(reinterpret_cast<const uint2*>(t + kKv4Params + ft * 8));
+    if (lane == 1) weight[i] = __ldg(p.acc + pair * p.tiles * kKv4Tile + from[i]);
   }
 #pragma unroll
   for (int i = 0; i < kKv4MoveTokens; ++i) {
     if (from[i] < 0) continue;
-    const int to = to0 + i * (kKv4MoveThreads / 16);
+    const int to = to0 + i * (kKv4MoveThreads / 8);
     uint8_t* t = dst + (int64_t)(to / kKv4Tile) * kKv4TileBytes;
     const int tt = to % kKv4Tile;
-    *reinterpret_cast<uint32_t*>(t + kv4_word_off(tt, lane, false)) = word[i][0];
-    *reinterpret_cast<uint32_t*>(t + kKv4Half + kv4_word_off(tt, lane, true)) = word[i][1];
-    if (lane < 4)
-      *reinterpret_cast<uint32_t*>(t + (lane >> 1) * kKv4Half + kKv4Params + tt * 8 + (lane & 1) * 4) = par[i];
-    if (lane == 4) p.dst_acc[pair * p.dst_tiles * kKv4Tile + to] = weight[i];
+    *reinterpret_cast<uint4*>(t + kv4_word_off(tt, 4 * c, vals)) = codes[i];
+    if (c == 0) *reinterpret_cast<uint2*>(t + kKv4Params + tt * 8) = par[i];
+    if (lane == 1) p.dst_acc[pair * p.dst_tiles * kKv4Tile + to] = weight[i];
   }
 }
 

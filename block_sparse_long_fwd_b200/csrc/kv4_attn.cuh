@@ -142,7 +142,7 @@ __device__ __forceinline__ void kv4_warp_best(uint64_t& key, int& j) {
 // in fp64 of products that are exact there (bf16 times fp32), so near ties
 // fall as in exact arithmetic; they are a few per cent of the work of the
 // attention itself (one mean per block of at least 128 keys). Latency-bound:
-// 14 us for 255 past blocks and 4 rows of each of 8 kv heads.
+// 13 us for 255 past blocks and 4 rows of each of 8 kv heads.
 __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
   extern __shared__ uint32_t picked[];  // [blocks]: rows of the unit that chose the block
@@ -1053,8 +1053,8 @@ constexpr int kKv4JoinThreads = 128;
 // maximum along waits for each in turn: 38 us for 64 of them against 4), and the
 // sums meet in a fixed order. Rows without keys get their zero here. With one
 // warp a row (few partial results each), 2048 rows of 8 kv heads over 32K tokens
-// take JOIN1 us for 28 MB, with four 29; with four (many results), 4 rows of 8 kv
-// heads over 128K tokens JOIN4.
+// take 16 us for 28 MB, with four 29; whole calls of 4 rows of each of 8 kv heads
+// over 128K tokens (some 19 results each) 50 us with one, 47.6 with four.
 template <int SPLIT>
 __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
@@ -1263,7 +1263,8 @@ constexpr int kKv4SeenThreads = 128, kKv4SeenKeys = 1024;
 // read a row and key, against 72 read again and widened a key. Whole calls: 128K
 // tokens of 8 heads, 4 rows each, 68 us against 79; 8 such sequences of 12 chosen
 // blocks 242 against 297. A warp takes 256 keys of a kv head, a lane a key, over
-// the units of the sequence in order.
+// the units of the sequence in order, 128 keys' scores under way at once (which
+// brought those calls to 59 and 204).
 __global__ void __launch_bounds__(kKv4SeenThreads) kv4_seen_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
   const int lane = threadIdx.x & 31, b = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv;

@@ -385,7 +385,7 @@ int moba_kv4_evict(const void* kv4, const float* acc, const int32_t* lengths, in
   while (csize < 8 && (int64_t)pairs * csize * 2 <= 2 * dev.sms && capacity / csize > 4096) csize *= 2;
   launch_clusters(moba::kv4_select_kernel, dim3((unsigned)pairs * csize), dim3(moba::kKv4SelectThreads), 0, csize, stream,
                   p);
-  const int64_t per = moba::kKv4MoveThreads / 16 * moba::kKv4MoveTokens;
+  const int64_t per = moba::kKv4MoveThreads / 8 * moba::kKv4MoveTokens;
   launch_chained(moba::kv4_move_kernel, dim3((unsigned)((budget + per - 1) / per), (unsigned)pairs),
                  dim3(moba::kKv4MoveThreads), 0, stream, p);
   MOBA_CUDA(cudaGetLastError());
