@@ -53,15 +53,21 @@ __device__ __forceinline__ float kv4_scale(uint32_t par) {
   return __half2float(__ushort_as_half((unsigned short)(par & 0x7F80u)));
 }
 
-// The eight channels of a code word, in fp32.
-__device__ __forceinline__ void kv4_decode(uint32_t word, uint32_t par, float (&x)[8]) {
-  const float s = kv4_scale(par);
-  const float z = (float)(par & 15u);
+// The eight channels of a code word as bf16. 128 + c has bf16's eight bits (a
+// nibble under 0x4300), so has its difference from 128 + z, and times a scale of
+// four it is a value that bf16 holds: all exact.
+__device__ __forceinline__ uint4 kv4_decode(uint32_t word, uint32_t par) {
+  const __nv_bfloat162 s = __float2bfloat162_rn(kv4_scale(par));
+  const uint32_t zz = 0x43004300u | (par & 15u) * 0x10001u;
+  const __nv_bfloat162 z = *reinterpret_cast<const __nv_bfloat162*>(&zz);
+  uint32_t x[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    x[2 * j] = s * ((float)((word >> (4 * j)) & 15u) - z);
-    x[2 * j + 1] = s * ((float)((word >> (4 * j + 16)) & 15u) - z);
+    const uint32_t c = (word >> (4 * j) & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 y = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c), z), s);
+    x[j] = *reinterpret_cast<const uint32_t*>(&y);
   }
+  return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
 // A length the caller left on the device: outside [0, capacity] it is a
@@ -224,7 +230,7 @@ constexpr int kKv4LoadThreads = 256, kKv4LoadRows = 4;
 
 // A CTA per 64 tokens of a kv head, half a warp per row, 8 channels a lane,
 // four rows of keys and values at a time: 144 bytes read, 512 written a row,
-// HBM-bound. 128K tokens of 8 heads: 119 us, 5.8 TB/s.
+// HBM-bound. 128K tokens of 8 heads: 116 us, 5.9 TB/s.
 __global__ void __launch_bounds__(kKv4LoadThreads) kv4_load_kernel(Kv4LoadParams p) {
   grid_dependency_sync();
   const int lane = threadIdx.x & 15, h = blockIdx.y, b = blockIdx.z;
@@ -253,12 +259,8 @@ __global__ void __launch_bounds__(kKv4LoadThreads) kv4_load_kernel(Kv4LoadParams
     if (at >= p.n) continue;
     const int64_t row = ((int64_t)b * p.n + at) * p.heads + h;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      float x[8];
-      kv4_decode(word[i][s], par[i][s], x);
-      reinterpret_cast<uint4*>((s ? p.v : p.k) + row * kHeadDim)[lane] =
-          make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-    }
+    for (int s = 0; s < 2; ++s)
+      reinterpret_cast<uint4*>((s ? p.v : p.k) + row * kHeadDim)[lane] = kv4_decode(word[i][s], par[i][s]);
   }
 }
 
