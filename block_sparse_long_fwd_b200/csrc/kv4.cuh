@@ -278,7 +278,7 @@ struct Kv4EvictParams {
   int32_t* new_lengths;    // [batch]
 };
 
-constexpr int kKv4SelectThreads = 1024;
+constexpr int kKv4SelectFew = 512, kKv4SelectMany = 1024;  // threads
 constexpr int kKv4SelectItems = 16;  // neighbouring weights a thread takes at a time
 constexpr int kKv4SelectBins = 2048, kKv4SelectCopies = 4;
 
@@ -331,8 +331,10 @@ __device__ __forceinline__ void kv4_remote_st(uint32_t* p, uint32_t rank, uint32
 // through distributed shared memory); a last pass writes the kept indexes,
 // each thread's neighbouring weights at its place in the order. Bound by its
 // chain of passes, each a round of counts, two cluster barriers and a scan: 128K
-// weights of 8 heads 27 us, 32 sequences of 4608 and 8 heads 21 us.
-__global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictParams p) {
+// weights of 8 heads 24 us; 32 sequences of 4608 and 8 heads 18 us with 512
+// threads, two CTAs an SM, 21 with 1024.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv4_select_kernel(Kv4EvictParams p) {
   grid_dependency_sync();
   // neighbouring lanes count in copies of their own: weights crowd into few bins
   __shared__ uint32_t hist[kKv4SelectCopies][kKv4SelectBins];
@@ -347,13 +349,13 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
   if (h == 0 && rank == 0 && tid == 0) p.new_lengths[b] = min(len, p.budget);
   int32_t* kept = p.kept + (int64_t)pair * p.budget;
   if (len <= p.budget) {  // the whole cluster leaves
-    for (int i = rank * kKv4SelectThreads + tid; i < p.budget; i += csize * kKv4SelectThreads) kept[i] = i < len ? i : -1;
+    for (int i = rank * THREADS + tid; i < p.budget; i += csize * THREADS) kept[i] = i < len ? i : -1;
     return;
   }
   const float* acc = p.acc + (int64_t)pair * p.tiles * kKv4Tile;
   const int older = len - p.recent;        // > budget - recent >= 0
   const uint32_t want = p.budget - p.recent;
-  for (int i = rank * kKv4SelectThreads + tid; i < p.recent; i += csize * kKv4SelectThreads) kept[want + i] = older + i;
+  for (int i = rank * THREADS + tid; i < p.recent; i += csize * THREADS) kept[want + i] = older + i;
   if (want == 0) return;
   const int part = (int)(((int64_t)older + csize * kKv4SelectItems - 1) / (csize * kKv4SelectItems)) * kKv4SelectItems;
   const int i0 = (int)min((int64_t)rank * part, (int64_t)older), i1 = (int)min((int64_t)i0 + part, (int64_t)older);
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
       for (int x = 0; x < kKv4SelectItems; ++x) k[x] = at + x < i1 ? kv4_weight_key(__ldg(acc + at + x)) : 0;
     }
   };
-  constexpr int kSweep = kKv4SelectThreads * kKv4SelectItems;
+  constexpr int kSweep = THREADS * kKv4SelectItems;
   // a part that is one sweep stays in registers, a longer one is read again in each pass
   const bool once = i1 - i0 <= kSweep;
   uint32_t k[kKv4SelectItems];
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 32 : pass == 1 ? 21 : 10;
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
-    for (int i = tid; i < kKv4SelectCopies * kKv4SelectBins; i += kKv4SelectThreads) (&hist[0][0])[i] = 0;
+    for (int i = tid; i < kKv4SelectCopies * kKv4SelectBins; i += THREADS) (&hist[0][0])[i] = 0;
     __syncthreads();
     for (int at = i0 + tid * kKv4SelectItems; at < i1; at += kSweep) {
       if (!once) keys(at, k);
@@ -393,25 +395,27 @@ __global__ void __launch_bounds__(kKv4SelectThreads) kv4_select_kernel(Kv4EvictP
           atomicAdd(&hist[tid % kKv4SelectCopies][(k[x] >> shift) & mask], 1u);
     }
     __syncthreads();
-    for (int i = tid; i < kKv4SelectBins; i += kKv4SelectThreads)
+    for (int i = tid; i < kKv4SelectBins; i += THREADS)
       hist[0][i] += (hist[1][i] + hist[2][i]) + hist[3][i];
     kv4_cluster_sync();
     if (rank == 0) {
-      // two bins a thread, from the highest down: the bin in which the need is met
-      uint32_t c[2], total;
+      // neighbouring bins for each thread, from the highest down: the bin in which the need is met
+      constexpr int BINS = kKv4SelectBins / THREADS;
+      uint32_t c[BINS], mine = 0, total;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int bin = kKv4SelectBins - 1 - (2 * tid + x);
+      for (int x = 0; x < BINS; ++x) {
+        const int bin = kKv4SelectBins - 1 - (BINS * tid + x);
         uint32_t y[8];  // all under way at once
 #pragma unroll
         for (uint32_t r = 0; r < 8; ++r) y[r] = r < csize ? kv4_remote_ld(&hist[0][bin], r) : 0;
         c[x] = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+        mine += c[x];
       }
-      uint32_t before = kv4_block_scan(c[0] + c[1], warp_sums, &total);
+      uint32_t before = kv4_block_scan(mine, warp_sums, &total);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < BINS; ++x) {
         if (before < need && before + c[x] >= need) {
-          const uint32_t found = prefix | (uint32_t)(kKv4SelectBins - 1 - (2 * tid + x)) << shift;
+          const uint32_t found = prefix | (uint32_t)(kKv4SelectBins - 1 - (BINS * tid + x)) << shift;
           for (uint32_t r = 0; r < csize; ++r) {
             kv4_remote_st(&s_found[0], r, found);
             kv4_remote_st(&s_found[1], r, need - before);

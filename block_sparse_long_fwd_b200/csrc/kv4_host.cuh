@@ -272,9 +272,12 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   p.steps = chunk ? 1 : 0;
   const int64_t nu = slots * heads_kv;
   // items (tiles, or steps of two tiles) and the ends of all ranges are counted in 31 bits
-  const int64_t items = chunk ? (p.tiles + 1) / 2 : p.tiles;
-  if (nu * items > ((int64_t)1 << 30)) return fail(MOBA_ERR_UNSUPPORTED, "too many (row, key) tiles");
   p.list_cap = kmean ? (int)std::min<int64_t>(p.blocks, (int64_t)p.R * topk) : 0;
+  const int64_t items = kmean   ? std::min<int64_t>(p.tiles, (int64_t)p.list_cap * (block_size / moba::kKv4Tile))
+                        : chunk ? (p.tiles + 1) / 2
+                                : p.tiles;
+  if (nu * items > ((int64_t)1 << 30))
+    return fail(MOBA_ERR_UNSUPPORTED, "too many (query row, cached token) pairs for one call: attend in chunks");
   // the gate: up to 8 CTAs share a unit's scores while there are few units
   int csize = 1;
   while (csize < 8 && nu * csize * 2 <= dev.sms) csize *= 2;
@@ -286,8 +289,7 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   const size_t o_scores = c.take((size_t)clusters * p.R * p.means * 8);
   const size_t o_part = c.take((size_t)2 * p.ctas * p.R * 130 * 4);
   // the scores of few rows are kept for their weights, up to a GiB of them (sized by the capacity, which alone is known)
-  const int64_t most = kmean ? std::min<int64_t>(items, (int64_t)p.list_cap * (block_size / moba::kKv4Tile)) : items;
-  const size_t seen = few && acc ? (size_t)nu * most * 4 * moba::kKv4Tile * 8 : 0;
+  const size_t seen = few && acc ? (size_t)nu * items * 4 * moba::kKv4Tile * 8 : 0;
   const bool keep = seen > 0 && seen <= ((size_t)1 << 30);
   const size_t o_seen = c.take(keep ? seen : 0);
   const size_t o_qtiles = c.take(chunk ? (size_t)nu * 2 * moba::kKv4TileOp : 0);
@@ -383,8 +385,13 @@ int moba_kv4_evict(const void* kv4, const float* acc, const int32_t* lengths, in
   // up to 8 CTAs select for a kv head while there are SMs for them and 4096 weights for each
   int csize = 1;
   while (csize < 8 && (int64_t)pairs * csize * 2 <= 2 * dev.sms && capacity / csize > 4096) csize *= 2;
-  launch_clusters(moba::kv4_select_kernel, dim3((unsigned)pairs * csize), dim3(moba::kKv4SelectThreads), 0, csize, stream,
-                  p);
+  // where a part is one sweep of 512 threads, so many take it, and two CTAs share an SM
+  if ((capacity + csize - 1) / csize <= moba::kKv4SelectFew * moba::kKv4SelectItems)
+    launch_clusters(moba::kv4_select_kernel<moba::kKv4SelectFew>, dim3((unsigned)pairs * csize),
+                    dim3(moba::kKv4SelectFew), 0, csize, stream, p);
+  else
+    launch_clusters(moba::kv4_select_kernel<moba::kKv4SelectMany>, dim3((unsigned)pairs * csize),
+                    dim3(moba::kKv4SelectMany), 0, csize, stream, p);
   const int64_t per = moba::kKv4MoveThreads / 8 * moba::kKv4MoveTokens;
   launch_chained(moba::kv4_move_kernel, dim3((unsigned)((budget + per - 1) / per), (unsigned)pairs),
                  dim3(moba::kKv4MoveThreads), 0, stream, p);

@@ -388,7 +388,9 @@ int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch,
  * in fp64 here; ties to the lower block index). A row without keys (its
  * position is negative) has out 0 and lse -infinity.
  *
- * q          device bf16 [total][heads_q][head_dim], packed by cu.
+ * q          device bf16 [total][heads_q][head_dim], packed by cu. With
+ *            total * heads_q * capacity from 2^39 on a call may be refused
+ *            (MOBA_ERR_UNSUPPORTED): chunks then.
  * kmean      device fp32 as moba_kv4_pool writes it, or NULL: every key, and
  *            block_size and topk are not looked at.
  * block_size, topk  with kmean, as moba_fwd (block_size a positive multiple

@@ -454,6 +454,14 @@ def test_tensors_of_another_kind_are_refused():
     ok()
 
 
+def test_more_pairs_than_are_counted_are_refused():
+    # a million tokens against room for 2^30: refused before anything is launched or read
+    x = torch.zeros(64, device="cuda").data_ptr()
+    rc = moba.lib().moba_kv4_attend(x, 1 << 20, None, x, x, None, 1, 1, 1, 128, 1 << 30, 0, 0, None, x, x, 0)
+    assert rc == moba.MOBA_ERR_UNSUPPORTED and "chunks" in moba.last_error()
+    ok()
+
+
 def test_a_length_beyond_the_capacity_is_cut_and_reported():
     kv4, vals = random_cache([128], 1, 128, 5)
     q = bf16(np.random.default_rng(1).standard_normal((1, 2, 128))).cuda()
