@@ -1342,15 +1342,20 @@ struct Kv4PoolParams {
   const int32_t* lengths;
   int64_t tiles;
   int heads, B, blocks;  // blocks = capacity / B
+  int per;               // blocks of a CTA: several where they are small
+  int stages;            // of a warp's ring: kKv4PoolStages, or its tiles where these are fewer
   float* kmean;          // [batch][heads][blocks][128]
 };
 
 constexpr int kKv4PoolThreads = 256, kKv4PoolStages = 3;
 
 // A cluster of CTAs per (block, head, sequence), a part of the block's tiles
-// each; each warp brings its tiles of keys into a ring of its own, one bulk
-// copy each, two ahead (128K tokens of 8 heads: 18 us a call, 4.2 TB/s in a
-// short kernel, 27 with loads into registers, two groups of tokens a warp).
+// each, or a CTA for two or four small blocks; each warp brings its tiles of keys
+// into a ring of its own, one bulk copy each, two ahead. HBM-bound where the
+// kernel is not short: 1M tokens of 8 heads in blocks of 4096 98 us, 6.2 TB/s;
+// 128K tokens 18 a call (27 with loads into registers, two groups of tokens a
+// warp); 64 sequences of 16K, 8 heads, blocks of 128 171 us, 3.5 TB/s (a CTA per
+// block 308, and 516 with room for three tiles a warp, so two CTAs an SM).
 // The tensor core sums in fp32: codes, as they stand in a word, are fp16
 // subnormals (a nibble at bit 0 is c 2^-24, at bit 4 c 2^-20), so a mask is all
 // that they need; they meet the scales of the four groups in four columns, of
@@ -1358,11 +1363,11 @@ constexpr int kKv4PoolThreads = 256, kKv4PoolStages = 3;
 // by one product more and taken off at the end. The warps' and CTAs' sums meet
 // in a fixed order. Blocks that the sequence has not completed are written as
 // zero.
-__global__ void __launch_bounds__(kKv4PoolThreads, 2) kv4_pool_kernel(Kv4PoolParams p) {
+__global__ void __launch_bounds__(kKv4PoolThreads, 3) kv4_pool_kernel(Kv4PoolParams p) {
   grid_dependency_sync();
   constexpr int MOST = kKv4PoolThreads / 32;
   const int WARPS = blockDim.x / 32;
-  extern __shared__ __align__(16) uint8_t pool_ring[];  // [WARPS][kKv4PoolStages][kKv4Half]
+  extern __shared__ __align__(16) uint8_t pool_ring[];  // [WARPS][stages][kKv4Half]
   __shared__ float sums[MOST][kHeadDim];
   __shared__ uint32_t total[kHeadDim];  // fp32 bits
   __shared__ uint64_t full[MOST][kKv4PoolStages];
@@ -1370,12 +1375,14 @@ __global__ void __launch_bounds__(kKv4PoolThreads, 2) kv4_pool_kernel(Kv4PoolPar
   uint32_t rank, csize;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
-  const int j = blockIdx.x / csize, h = blockIdx.y, b = blockIdx.z;
+  const int h = blockIdx.y, b = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, qd = lane & 3;
+  const int wpb = WARPS / p.per, j0 = blockIdx.x / csize * p.per, j = j0 + warp / wpb;  // warps of a block, first block
   const int len = kv4_length(p.lengths, b, p.tiles * kKv4Tile);
-  float* out = p.kmean + (((int64_t)b * p.heads + h) * p.blocks + j) * kHeadDim;
-  if ((int64_t)(j + 1) * p.B > len) {  // the whole cluster leaves
-    if (rank == 0 && threadIdx.x < kHeadDim) out[threadIdx.x] = 0.f;
+  float* out = p.kmean + (((int64_t)b * p.heads + h) * p.blocks + j0) * kHeadDim;
+  const int outs = min(p.per, p.blocks - j0) * kHeadDim;
+  if ((int64_t)(j0 + 1) * p.B > len) {  // no complete block: the whole cluster leaves
+    for (int i = threadIdx.x; rank == 0 && i < outs; i += blockDim.x) out[i] = 0.f;
     return;
   }
   if (threadIdx.x == 0) {
@@ -1384,10 +1391,11 @@ __global__ void __launch_bounds__(kKv4PoolThreads, 2) kv4_pool_kernel(Kv4PoolPar
     fence_barrier_init();
   }
   __syncthreads();
-  const int tiles = p.B / kKv4Tile, step = csize * WARPS, t0 = rank * WARPS + warp;
-  const int n = t0 < tiles ? (tiles - t0 + step - 1) / step : 0;  // tiles of this warp
+  const int tiles = p.B / kKv4Tile, step = csize * wpb, t0 = rank * wpb + warp % wpb;
+  // tiles of this warp; none of a block that is not complete, whose sums stay zero
+  const int n = t0 < tiles && (int64_t)(j + 1) * p.B <= len ? (tiles - t0 + step - 1) / step : 0;
   const uint8_t* src = p.kv4 + kv4_tile_off(p.tiles, p.heads, b, h, (int64_t)j * tiles + t0);
-  uint8_t* ring = pool_ring + warp * kKv4PoolStages * kKv4Half;
+  uint8_t* ring = pool_ring + warp * p.stages * kKv4Half;
   auto issue = [&](int k) {
     if (k >= n || lane != 0) return;
     const int d = k % kKv4PoolStages;
@@ -1459,11 +1467,13 @@ __global__ void __launch_bounds__(kKv4PoolThreads, 2) kv4_pool_kernel(Kv4PoolPar
     }
   }
   __syncthreads();
-  if (threadIdx.x < kHeadDim) {
+  for (int i = threadIdx.x; i < outs; i += blockDim.x) {
     float s = 0.f;
-    for (int w = 0; w < WARPS; ++w) s += sums[w][threadIdx.x];
-    total[threadIdx.x] = __float_as_uint(s);
+    for (int w = 0; w < wpb; ++w) s += sums[i / kHeadDim * wpb + w][i % kHeadDim];
+    if (csize == 1) out[i] = s / (float)p.B;
+    else total[i] = __float_as_uint(s);  // one block
   }
+  if (csize == 1) return;
   kv4_cluster_sync();
   if (rank == 0 && threadIdx.x < kHeadDim) {
     float s = 0.f;

@@ -196,15 +196,19 @@ int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch, int heads_
   p.blocks = (int)(capacity / block_size);
   p.kmean = kmean;
   if (p.blocks) {
-    // a warp for 64 tokens, 4 to 8 of them; up to 8 CTAs share a large block while there are SMs for them
-    const int threads = std::min(moba::kKv4PoolThreads, std::max(moba::kHeadDim, block_size / 64 * 32));
-    const size_t ring = (size_t)threads / 32 * moba::kKv4PoolStages * moba::kKv4Half;
+    // a warp for 64 tokens, up to 8 of them, which are several blocks' where a block has two or four; up to 8 CTAs
+    // share a large block while there are SMs for them
+    const int most = moba::kKv4PoolThreads / 32, wpb = std::min(most, block_size / moba::kKv4Tile);
+    p.per = most / wpb;
+    const int threads = wpb * p.per * 32;
     int csize = 1;
     while (csize < 8 && (int64_t)p.blocks * heads_kv * batch * csize * 2 <= 2 * dev.sms && block_size / csize > 1024)
       csize *= 2;
+    p.stages = std::min(moba::kKv4PoolStages, (block_size / moba::kKv4Tile + wpb * csize - 1) / (wpb * csize));
+    const size_t ring = (size_t)threads / 32 * p.stages * moba::kKv4Half;
     if ((int64_t)p.blocks * csize > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many blocks");
-    launch_clusters(moba::kv4_pool_kernel, dim3(p.blocks * csize, heads_kv, batch), dim3(threads), ring, csize,
-                    stream, p);
+    launch_clusters(moba::kv4_pool_kernel, dim3((p.blocks + p.per - 1) / p.per * csize, heads_kv, batch), dim3(threads),
+                    ring, csize, stream, p);
     MOBA_CUDA(cudaGetLastError());
   }
   return finish_call(MOBA_OK, stream);

@@ -187,6 +187,22 @@ def test_pool_of_large_blocks_by_several_ctas(block):
         assert (f64(m[b])[:, L // block:] == 0).all()
 
 
+@pytest.mark.parametrize("block,blocks", [(128, 1), (128, 2), (128, 3), (128, 5), (256, 1), (256, 3), (512, 1)])
+def test_pool_writes_the_means_and_nothing_behind_them(block, blocks):
+    # a CTA takes several small blocks: the last one may have fewer
+    cap, hkv = block * blocks + 64, 2
+    lengths = [cap, block * blocks - 1]
+    kv4, vals = random_cache(lengths, hkv, cap, 13)
+    buf = torch.full((2 * hkv * blocks + 4, 128), 7.0, device="cuda")
+    m = moba.kv4_pool(kv4, ints(lengths), block, kmean=buf[:2 * hkv * blocks].view(2, hkv, blocks, 128))
+    ok()
+    assert (buf[2 * hkv * blocks:] == 7).all()
+    for b, L in enumerate(lengths):
+        want, size = (ref.means(x, L, block, blocks) for x in (vals[b][0], np.abs(vals[b][0])))
+        assert (np.abs(f64(m[b]) - want) <= (block + 1) * U * size).all()
+        assert (f64(m[b])[:, L // block:] == 0).all()
+
+
 def test_pool_of_less_than_a_block_is_empty():
     kv4, _ = random_cache([64], 1, 64, 1)
     assert moba.kv4_pool(kv4, ints([64]), 128).shape == (1, 1, 0, 128)
