@@ -47,7 +47,7 @@ struct Kv4AttnParams {
   Kv4Unit* units;               // [slots * Hkv]
   int* before;                  // [slots * Hkv + 1]: items of the units before
   uint2* list;                  // [slots * Hkv][list_cap]: (block, rows that chose it), ascending
-  uint32_t* chosen;             // [slots * Hkv][blocks]: rows of the unit that chose the block
+  uint32_t* chosen;             // or null: [slots * Hkv][blocks]: rows of the unit that chose the block
   double* scores;               // [clusters][R][means]
   float* seen;                  // or null: [items][4][64][2] log2 scores, of each tile's keys and two rows
   float* part;                  // [2 * ctas][R * 130]: O, then m and l
@@ -56,6 +56,8 @@ struct Kv4AttnParams {
   int steps;                    // ranges are dealt out in steps of 128 keys (else in tiles)
   uint8_t* qtiles;              // [slots * Hkv][2][32768]: query tiles as fp16 operands
   float* qscale;                // [slots * Hkv][256]: their rows' scales
+  const uint32_t* picks;        // or null: the gate's `chosen` of units of 32 rows
+  int pick_B, pick_blocks;      // its block size and blocks
 };
 
 // Queries of sequence b: packed index of the first and their number. Offsets
@@ -104,6 +106,13 @@ __device__ __forceinline__ Kv4Unit kv4_unit_of(const Kv4AttnParams& p, const int
   u.t0 = t0;
   u.pos0 = kv4_length(lengths, lo, p.tiles * kKv4Tile) - n;
   return u;
+}
+
+// The rows of 32 (from row `row`, a multiple of 32, of sequence b's kv head h) that
+// chose a block, a bit each.
+__device__ __forceinline__ uint32_t kv4_picks(const Kv4AttnParams& p, int b, int h, int t0, int row, int block) {
+  const int64_t slot = ((uint32_t)t0 * (uint32_t)p.G >> 5) + b + (row >> 5);
+  return __ldcg(p.picks + (slot * p.Hkv + h) * p.pick_blocks + block);
 }
 
 // Position of the unit's last row: the last key that any of its rows attends.
@@ -283,7 +292,7 @@ __global__ void __launch_bounds__(kKv4GateThreads) kv4_gate_kernel(Kv4AttnParams
           count += total;
         }
         count = min(count, (uint32_t)p.list_cap);
-        if (p.acc)
+        if (p.chosen)
           for (int j = tid; j < p.blocks; j += kKv4GateThreads) p.chosen[(int64_t)ui * p.blocks + j] = picked[j];
       }
       if (tid == 0) {

@@ -135,6 +135,7 @@ constexpr int kKv4ChunkSmemBytes = (2 + 2 * kKv4ChunkStages) * kKv4TileOp + 1024
 // TMEM columns, as in attn.cuh
 constexpr uint32_t kKv4TmemS = 0, kKv4TmemP = 128, kKv4TmemO = 256;
 
+template <bool MASKED>
 __global__ void __launch_bounds__(kKv4ChunkThreads, 1) kv4_chunk_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
   extern __shared__ uint8_t smem_raw[];
@@ -208,7 +209,18 @@ __global__ void __launch_bounds__(kKv4ChunkThreads, 1) kv4_chunk_kernel(Kv4AttnP
       const int pos = row < u.rows ? u.pos0 + (u.row0 + row) / p.G : -1;
       const int first_pos = u.pos0 + (u.row0 + X * kTile) / p.G;
       float ref = kKv4Low, l = 0.f;
+      // with a gate: the warp's 32 rows that chose the step's block (rows behind the unit's, and rows before token 0,
+      // which no gate has looked at, have no keys anyway)
+      uint32_t on = ~0u;
+      int block = -1;
+      const int row32 = u.row0 + (row & ~31);
       for (int s = s0; s < s1; ++s, ++sx) {
+        if constexpr (MASKED) {
+          if (s * kTile / p.pick_B != block) {
+            block = s * kTile / p.pick_B;
+            on = (row & ~31) < u.rows ? kv4_picks(p, u.b, u.h, u.t0, row32, block) : 0;
+          }
+        }
         if (!mbar_wait(&sh->s_full[X], sx & 1, abort_flag)) goto done;
         __syncwarp();
         tc_fence_after();
@@ -227,8 +239,8 @@ __global__ void __launch_bounds__(kKv4ChunkThreads, 1) kv4_chunk_kernel(Kv4AttnP
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->s_free);
-        if ((s + 1) * kTile - 1 > first_pos) {
-          const int lim = pos - s * kTile;  // keys e > lim are masked
+        if ((s + 1) * kTile - 1 > first_pos || (MASKED && on != ~0u)) {
+          const int lim = !MASKED || on >> lane & 1u ? pos - s * kTile : -1;  // keys e > lim are masked
 #pragma unroll
           for (int e = 0; e < 128; ++e)
             if (e > lim) r[e] = __float_as_uint(-INFINITY);
@@ -488,6 +500,7 @@ struct Kv4ColShared {
 };
 constexpr int kKv4ColSmemBytes = 3 * kKv4TileOp + 1024 + sizeof(Kv4ColShared);
 
+template <bool MASKED>
 __global__ void __launch_bounds__(kKv4ColThreads, 2) kv4_chunk_weight_kernel(Kv4AttnParams p) {
   grid_dependency_sync();
   extern __shared__ uint8_t smem_raw[];
@@ -549,6 +562,13 @@ __global__ void __launch_bounds__(kKv4ColThreads, 2) kv4_chunk_weight_kernel(Kv4
       tc_fence_after();
       // the first row's position is the smallest
       const bool edge = key0 + (X + 1) * kTile - 1 > sh->pos[k & 1][0];
+      uint32_t on[4] = {~0u, ~0u, ~0u, ~0u};  // with a gate: the rows that chose this key tile's block
+      if constexpr (MASKED) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          on[c] = i * kTile + c * 32 < rows && key0 + X * kTile < len
+                      ? kv4_picks(p, b, h, t0, i * kTile + c * 32, (key0 + X * kTile) / p.pick_B) : 0;
+      }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t r[32];
@@ -558,6 +578,11 @@ __global__ void __launch_bounds__(kKv4ColThreads, 2) kv4_chunk_weight_kernel(Kv4
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (key > sh->pos[k & 1][c * 32 + e]) r[e] = __float_as_uint(-INFINITY);
+        }
+        if (MASKED && on[c] != ~0u) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(on[c] >> e & 1u)) r[e] = __float_as_uint(-INFINITY);
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {

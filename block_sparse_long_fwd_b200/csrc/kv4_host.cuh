@@ -70,12 +70,26 @@ cudaError_t set_kv4_attn_smem() {
                               (int)kv4_attn_smem<C>());
 }
 
+template <bool MASKED>
+cudaError_t set_kv4_chunk_smem() {
+  const cudaError_t e = cudaFuncSetAttribute(moba::kv4_chunk_kernel<MASKED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             moba::kKv4ChunkSmemBytes);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(moba::kv4_chunk_weight_kernel<MASKED>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, moba::kKv4ColSmemBytes);
+}
+
 // Rows of a sequence and kv head, on average, above which the tcgen05 kernel
 // (256 rows a unit) takes over from mma.sync (16 rows a unit, every key widened
 // for each of them). At 32K tokens, 32 / 8 heads, one sequence: 32 rows 43
 // against 44 us, 64 rows 45 against 65, 2048 rows 293 against 1430; 16
 // sequences of 8K: 16 rows 162 against 70, 64 rows 173 against 219.
 constexpr int kKv4ManyRows = 48;
+
+// With a gate the tcgen05 kernel goes over all keys and masks, where mma.sync goes over the blocks that its 16 rows
+// chose: 16 topk blocks of the capacity at most. It costs a fifth a row and key, so it takes over where those are a fifth
+// of the cache. BOTHSIDES
+constexpr int kKv4Union = 5 * moba::Kv4Many::R;
 
 bool g_kv4_ready[64] = {};
 
@@ -90,10 +104,8 @@ int kv4_begin(DeviceInfo* dev, cudaStream_t st) {
     if (!g_kv4_ready[d]) {
       MOBA_CUDA(set_kv4_attn_smem<moba::Kv4Few>());
       MOBA_CUDA(set_kv4_attn_smem<moba::Kv4Many>());
-      MOBA_CUDA(cudaFuncSetAttribute(moba::kv4_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     moba::kKv4ChunkSmemBytes));
-      MOBA_CUDA(cudaFuncSetAttribute(moba::kv4_chunk_weight_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     moba::kKv4ColSmemBytes));
+      MOBA_CUDA(set_kv4_chunk_smem<false>());
+      MOBA_CUDA(set_kv4_chunk_smem<true>());
       MOBA_CUDA(cudaFuncSetAttribute(moba::kv4_pool_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      moba::kKv4PoolThreads / 32 * moba::kKv4PoolStages * moba::kKv4Half));
       MOBA_CUDA(cudaFuncSetAttribute(moba::kv4_gate_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -261,20 +273,38 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   p.topk = kmean ? topk : 0;
   p.means = kmean ? (int)(capacity / block_size) : 0;
   p.blocks = kmean ? (int)((capacity + block_size - 1) / block_size) : 0;
-  const bool few = total * p.G <= (int64_t)moba::Kv4Few::R * batch;
-  const bool chunk = !kmean && total * p.G > (int64_t)kKv4ManyRows * batch;
-  p.R = few ? moba::Kv4Few::R : chunk ? moba::kKv4ChunkRows : moba::Kv4Many::R;
-  while (1 << p.rshift < p.R) ++p.rshift;
   p.each = cu ? 0 : (int)(total / batch);
-  const int64_t slots = total * p.G / p.R + batch;
-  if (slots * heads_kv * p.R > INT32_MAX) return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
-  p.slots = (int)slots;
   p.ctas = dev.sms;
+  const bool few = total * p.G <= (int64_t)moba::Kv4Few::R * batch;
+  const bool chunk = total * p.G > (int64_t)kKv4ManyRows * batch &&
+                     (!kmean || (int64_t)kKv4Union * topk * block_size >= capacity);
+  // many rows with a gate: it writes which blocks each row chose, the attention goes over all keys and masks
+  const bool masked = chunk && kmean;
+  moba::Kv4AttnParams gp = p;
+  if (masked) {
+    p.kmean = nullptr;
+    p.B = moba::kKv4Tile;
+    p.topk = p.means = p.blocks = 0;
+    p.pick_B = block_size;
+    p.pick_blocks = gp.blocks;
+    kmean = nullptr;
+  }
+  const auto rows_of = [&](moba::Kv4AttnParams& x, int R) {
+    x.R = R;
+    while (1 << x.rshift < R) ++x.rshift;
+    const int64_t slots = total * x.G / R + batch;
+    if (slots * heads_kv * R > INT32_MAX) return false;
+    x.slots = (int)slots;
+    return true;
+  };
+  if (!rows_of(p, few ? moba::Kv4Few::R : chunk ? moba::kKv4ChunkRows : moba::Kv4Many::R) ||
+      !rows_of(gp, masked ? 32 : p.R))
+    return fail(MOBA_ERR_UNSUPPORTED, "too many rows");
   // a warp for each of an SM's four schedulers at least: 4096 tokens of one head take 12.1 us with 4 tiles a CTA (on 16
   // CTAs), 15.0 with 1, 13.0 with 2 and with 8, 16.3 with 16
   p.least = chunk ? 1 : 4;
   p.steps = chunk ? 1 : 0;
-  const int64_t nu = slots * heads_kv;
+  const int64_t nu = (int64_t)p.slots * heads_kv, gnu = (int64_t)gp.slots * heads_kv;
   // items (tiles, or steps of two tiles) and the ends of all ranges are counted in 31 bits
   p.list_cap = kmean ? (int)std::min<int64_t>(p.blocks, (int64_t)p.R * topk) : 0;
   const int64_t items = kmean   ? std::min<int64_t>(p.tiles, (int64_t)p.list_cap * (block_size / moba::kKv4Tile))
@@ -284,13 +314,14 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
     return fail(MOBA_ERR_UNSUPPORTED, "too many (query row, cached token) pairs for one call: attend in chunks");
   // the gate: up to 8 CTAs share a unit's scores while there are few units
   int csize = 1;
-  while (csize < 8 && nu * csize * 2 <= dev.sms) csize *= 2;
-  const int64_t clusters = std::min<int64_t>(nu, 4 * dev.sms / csize);
+  while (csize < 8 && gnu * csize * 2 <= dev.sms) csize *= 2;
+  const int64_t clusters = std::min<int64_t>(gnu, 4 * dev.sms / csize);
   Carve c;
   const size_t o_units = c.take((size_t)nu * sizeof(moba::Kv4Unit)), o_before = c.take((size_t)(nu + 1) * 4);
   const size_t o_list = c.take((size_t)nu * p.list_cap * 8);
-  const size_t o_chosen = c.take(acc ? (size_t)nu * p.blocks * 4 : 0);
-  const size_t o_scores = c.take((size_t)clusters * p.R * p.means * 8);
+  const size_t o_gunits = c.take(masked ? (size_t)gnu * sizeof(moba::Kv4Unit) : 0);
+  const size_t o_chosen = c.take(gp.kmean && (acc || masked) ? (size_t)gnu * gp.blocks * 4 : 0);
+  const size_t o_scores = c.take((size_t)clusters * gp.R * gp.means * 8);
   const size_t o_part = c.take((size_t)2 * p.ctas * p.R * 130 * 4);
   // the scores of few rows are kept for their weights, up to a GiB of them (sized by the capacity, which alone is known)
   const size_t seen = few && acc ? (size_t)nu * items * 4 * moba::kKv4Tile * 8 : 0;
@@ -305,18 +336,25 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
     p.units = reinterpret_cast<moba::Kv4Unit*>(ws + o_units);
     p.before = reinterpret_cast<int*>(ws + o_before);
     p.list = reinterpret_cast<uint2*>(ws + o_list);
-    p.chosen = reinterpret_cast<uint32_t*>(ws + o_chosen);
+    p.chosen = acc || masked ? reinterpret_cast<uint32_t*>(ws + o_chosen) : nullptr;
+    p.picks = masked ? p.chosen : nullptr;
     p.scores = reinterpret_cast<double*>(ws + o_scores);
     p.part = reinterpret_cast<float*>(ws + o_part);
-    if (kmean)
+    if (gp.kmean) {
+      gp.units = masked ? reinterpret_cast<moba::Kv4Unit*>(ws + o_gunits) : p.units;
+      gp.list = p.list;
+      gp.list_cap = p.list_cap;  // 0 where the attention masks
+      gp.chosen = p.chosen;
+      gp.scores = p.scores;
       launch_clusters(moba::kv4_gate_kernel, dim3((unsigned)(clusters * csize)), dim3(moba::kKv4GateThreads),
-                      (size_t)p.blocks * 4, csize, st, p);
+                      (size_t)gp.blocks * 4, csize, st, gp);
+    }
     if (few) {
       launch_kv4_attn<moba::Kv4Few>(p, st);
     } else if (chunk) {
       launch_chained(moba::kv4_prep_kernel, dim3((unsigned)nu, moba::kKv4ChunkRows * 16 / moba::kKv4PrepThreads),
                      dim3(moba::kKv4PrepThreads), 0, st, p);
-      launch_chained(moba::kv4_chunk_kernel, dim3(p.ctas), dim3(moba::kKv4ChunkThreads), moba::kKv4ChunkSmemBytes, st,
+      launch_chained(masked ? moba::kv4_chunk_kernel<true> : moba::kv4_chunk_kernel<false>, dim3(p.ctas), dim3(moba::kKv4ChunkThreads), moba::kKv4ChunkSmemBytes, st,
                      p);
     } else {
       launch_kv4_attn<moba::Kv4Many>(p, st);
@@ -328,7 +366,7 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
     else
       launch_chained(moba::kv4_join_kernel<1>, dim3((unsigned)(nu * p.R / split)), dim3(moba::kKv4JoinThreads), 0, st, p);
     if (acc && chunk) {
-      launch_chained(moba::kv4_chunk_weight_kernel, dim3((unsigned)((capacity + 255) / 256), batch * heads_kv),
+      launch_chained(masked ? moba::kv4_chunk_weight_kernel<true> : moba::kv4_chunk_weight_kernel<false>, dim3((unsigned)((capacity + 255) / 256), batch * heads_kv),
                      dim3(moba::kKv4ColThreads), moba::kKv4ColSmemBytes, st, p);
     } else if (keep) {
       launch_chained(moba::kv4_seen_kernel,

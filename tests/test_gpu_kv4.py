@@ -337,6 +337,12 @@ SPARSE = [
     (1, 16, [1100], [5], 128, 3),
     (1, 4, [700, 0, 3], [3, 0, 4], 128, 2),
     (1, 2, [600], [1], 128, 1),
+    # many rows: masks a row and block, units of 256 rows over several blocks of picks
+    (2, 4, [1500], [200], 256, 3),
+    (1, 8, [700, 0, 3, 1300, 260], [90, 70, 80, 64, 0], 128, 2),
+    (2, 3, [1100, 1000], [300, 1], 384, 2),
+    (1, 1, [2000], [513], 128, 4),
+    (1, 40, [300], [9], 128, 1),
     (1, 2, [40000], [3], 128, 5),               # more past blocks than a warp keeps in registers
     (2, 1, [50 + i % 400 for i in range(300)], [1] * 300, 128, 2),  # more sequences than the gate copies
 ]
@@ -346,6 +352,11 @@ SPARSE = [
 @pytest.mark.parametrize("acc", [False, True])
 def test_attention_over_chosen_blocks(hkv, G, lengths, news, block, topk, acc):
     attend_case(hkv, G, lengths, news, sparse=(block, topk), acc=acc, seed=block + topk)
+
+
+@pytest.mark.parametrize("acc", [False, True])
+def test_many_rows_that_choose_a_small_part_of_a_large_cache(acc):
+    attend_case(1, 4, [900, 130], [100, 60], sparse=(128, 1), acc=acc, seed=6, cap=16384)
 
 
 @pytest.mark.parametrize("qscale", [1e-4, 30.0])
