@@ -11,6 +11,9 @@
 //   warp 12         TMEM owner; issues S = Q K^T
 //   warp 13         issues O += P V
 //   warp 14         fetches the units' query tiles
+// With a gate (MASKED), a unit goes over all keys, and a step's weights are those
+// of the rows that chose its block: the 32 rows of a warp are one word of the
+// gate's.
 // Products, roles and barriers are those of the bf16 attention kernel
 // (attn.cuh): one S buffer for both tiles, P in TMEM columns of its own, two
 // issuers. What differs: operands are fp16 (queries times a power of two, a

@@ -87,9 +87,11 @@ cudaError_t set_kv4_chunk_smem() {
 constexpr int kKv4ManyRows = 48;
 
 // With a gate the tcgen05 kernel goes over all keys and masks, where mma.sync goes over the blocks that its 16 rows
-// chose: 16 topk blocks of the capacity at most. It costs a fifth a row and key, so it takes over where those are a fifth
-// of the cache. BOTHSIDES
-constexpr int kKv4Union = 5 * moba::Kv4Many::R;
+// chose, at most 16 topk blocks of the capacity, at some four times the cost a row and key. So the former takes over
+// where those are a third of the cache. 512 tokens of 32 / 8 heads: at 32K tokens, block 512, top-12 (all of it) 487
+// against 1306 us; at 128K, block 4096, top-12 1372 against 4949; at 128K, block 128, top-12 (a fifth) 2777 against
+// 2101, and each pick more costs 36 against 95.
+constexpr int kKv4Union = 3 * moba::Kv4Many::R;
 
 bool g_kv4_ready[64] = {};
 
