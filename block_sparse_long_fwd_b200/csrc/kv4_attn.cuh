@@ -17,6 +17,7 @@
 #pragma once
 
 #include "kv4.cuh"
+#include "kv4_feed.cuh"
 
 namespace moba {
 
@@ -669,7 +670,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
   // copies and two ahead, cost 30 instructions more for 16 keys: 265 against 247 us at 1M tokens). `next` walks the
   // units to the next tile.
   const int tpb = p.B / kKv4Tile;
-  int c_ui = range.unit - 1, c_off = range.off, c_left = n, c_end = 0, c_at = 0, c_in = 0;
+  Kv4Fetch fetch;
+  fetch.left = n;
+  int c_ui = range.unit - 1, c_off = range.off, c_end = 0, c_at = 0, c_in = 0;
   const uint8_t* c_src = nullptr;       // the next tile (with a gate, the first of the sequence)
   const uint8_t* src = nullptr;         // the tile that comes
   int key_b = 0, c_key = 0;             // their first keys
@@ -703,7 +706,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
       c_key += kKv4Tile;
     }
     ++c_off;
-    --c_left;
+    --fetch.left;
   };
   uint8_t* ring = sh->ring[warp];
   auto issue = [&](int vals) {
@@ -722,8 +725,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
   const int tok0 = kv4_token_of(r);
   const int vchunk = (r ^ (qd & 2 ? 4 : 0)) * 8;
   const int ve0 = 2 * qd + (qd & 1), ve1 = 2 * qd + ((qd & 1) ^ 1);
-  bool dead = false;  // a wait ran out: what follows is computed on what is there, and nothing more is fetched
-  int death = 0;      // in this tile
+  // once a wait has run out (fetch.dead), what follows is computed on what is there, and nothing more is fetched
   int k = 0;          // tiles of this warp behind us
   for (int ui = range.unit, off = range.off; k < n; ++ui, off = 0) {
     const Kv4Unit u = range.at(ui);
@@ -764,7 +766,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
       const uint32_t rows_a = rows_b;
       const uint8_t* kt = ring;
       const uint8_t* vt = ring + kKv4Half;
-      if (!dead && !mbar_wait(&sh->full[warp][0], k & 1, &sh->abort_flag)) dead = true, death = k;
+      if (!fetch.dead && !mbar_wait(&sh->full[warp][0], k & 1, &sh->abort_flag)) fetch.gave_up(k);
 
       // scores: keys x rows, 16 keys at a time
       float sc[4][NT][4];
@@ -799,12 +801,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
         }
       }
       __syncwarp();  // the keys are read: the next tile's may take their place
-      const bool more = !dead && c_left > 0;
-      if (more) {
+      if (fetch.next_keys()) {
         next();
         issue(0);
       }
-      if (!dead && !mbar_wait(&sh->full[warp][1], k & 1, &sh->abort_flag)) dead = true, death = k;
+      if (!fetch.dead && !mbar_wait(&sh->full[warp][1], k & 1, &sh->abort_flag)) fetch.gave_up(k);
 
       // keys behind a row's position, and blocks that a row did not choose (a loop of one turn: a branch, where the
       // compiler would have every tile pay for instructions that are switched off)
@@ -935,7 +936,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
         if (g < 3) values(g + 1, w, vp);
       }
       __syncwarp();  // the values are read
-      if (more) issue(1);
+      if (fetch.next_values()) issue(1);
     }
 
     // ---- this warp's part of the unit: all of it is a result, else a piece to be joined
@@ -998,12 +999,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
         }
     }
   }
-  if (dead) {
-    // the block's shared memory lives until the copies under way have landed: keys of tile n - c_left - 1, values of
-    // tile `death`
+  if (fetch.dead) {
+    // the block's shared memory lives until the copies under way have landed
     volatile int keep_waiting = 0;
-    mbar_wait(&sh->full[warp][0], (n - c_left - 1) & 1, &keep_waiting, 1ull << 28);
-    mbar_wait(&sh->full[warp][1], death & 1, &keep_waiting, 1ull << 28);
+    mbar_wait(&sh->full[warp][0], fetch.last_keys(n) & 1, &keep_waiting, 1ull << 28);
+    mbar_wait(&sh->full[warp][1], fetch.last_values() & 1, &keep_waiting, 1ull << 28);
   }
   __syncthreads();
 
