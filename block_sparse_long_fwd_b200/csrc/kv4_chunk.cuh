@@ -80,6 +80,25 @@ __global__ void __launch_bounds__(kKv4PrepThreads) kv4_prep_kernel(Kv4AttnParams
   if (lane == 0) p.qscale[(int64_t)ui * kKv4ChunkRows + row] = scale;
 }
 
+// A kernel's buffers of query tiles, for the warp that fills them (one of its lanes starts the copies).
+struct Kv4QueryPort {
+  uint64_t *full, *empty_;
+  uint8_t* dst;
+  const uint8_t* src;  // the next tile
+  volatile int* abort_flag;
+  bool starts;
+  __device__ __forceinline__ bool empty(int x, uint32_t parity) { return mbar_wait(&empty_[x], parity, abort_flag); }
+  __device__ __forceinline__ void start(int x) {
+    if (!starts) return;
+    mbar_arrive_expect_tx(&full[x], kKv4TileOp);
+    bulk_load(dst + x * kKv4TileOp, src, kKv4TileOp, &full[x]);
+  }
+  __device__ __forceinline__ void landed(int x, uint32_t parity) {
+    volatile int keep_waiting = 0;
+    if (starts) mbar_wait(&full[x], parity, &keep_waiting);
+  }
+};
+
 // ------------------------------------------------------------------ widening
 
 // Codes of up to four (key, 32 channels) pieces a thread: 128 keys of one
@@ -449,27 +468,21 @@ __global__ void __launch_bounds__(kKv4ChunkThreads, 1) kv4_chunk_kernel(Kv4AttnP
     }
   } else if (warp == 14 && lane == 0) {
     // ------------------------------------------------ query tiles
-    uint32_t ux[2] = {0, 0};
+    Kv4QueryPort port = {sh->q_full, sh->q_empty, sQ, nullptr, abort_flag, true};
+    Kv4Feeder<2> feed;
+    bool going = true;
     int done = 0;
-    for (int ui = range.unit, s0 = range.off; done < range.n; ++ui, s0 = 0) {
+    for (int ui = range.unit, s0 = range.off; going && done < range.n; ++ui, s0 = 0) {
       const Kv4Unit u = range.at(ui);
       const int s1 = min(kv4_items(p, u), s0 + range.n - done);
       if (s1 <= s0) continue;
       done += s1 - s0;
-      for (int x = 0; x < (u.rows > kTile ? 2 : 1); ++x) {
-        if (!mbar_wait(&sh->q_empty[x], (ux[x] & 1) ^ 1, abort_flag)) goto q_done;
-        mbar_arrive_expect_tx(&sh->q_full[x], kKv4TileOp);
-        bulk_load(sQ + x * kKv4TileOp, p.qtiles + ((int64_t)ui * 2 + x) * kKv4TileOp, kKv4TileOp, &sh->q_full[x]);
-        ++ux[x];
+      for (int x = 0; going && x < (u.rows > kTile ? 2 : 1); ++x) {
+        port.src = p.qtiles + ((int64_t)ui * 2 + x) * kKv4TileOp;
+        going = feed.load(port, x);
       }
     }
-  q_done:
-    // the block's shared memory lives until the copies under way have landed
-    if (*abort_flag)
-      for (int x = 0; x < 2; ++x) {
-        volatile int keep_waiting = 0;
-        if (ux[x]) mbar_wait(&sh->q_full[x], (ux[x] - 1) & 1, &keep_waiting, (1ull << 28));
-      }
+    feed.finish(port);
   }
 done:
   __syncwarp();
@@ -633,15 +646,14 @@ __global__ void __launch_bounds__(kKv4ColThreads, 2) kv4_chunk_weight_kernel(Kv4
       mbar_wait(&sh->drain, 0, &keep_waiting, (1ull << 28));
     }
   } else {
+    Kv4QueryPort port = {&sh->q_full, &sh->q_empty, sQ, nullptr, abort_flag, lane == 0};
+    Kv4Feeder<1> feed;
     int k = 0;
     for (int i = tile0; i < tiles; ++i, ++k) {
-      // the rows' numbers of two tiles ago have been read once the products of the last one could start
-      if (k > 0 && !mbar_wait(&sh->q_empty, (k - 1) & 1, abort_flag)) break;
       const int64_t ui = (int64_t)(slot0 + i / 2) * p.Hkv + h;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&sh->q_full, kKv4TileOp);
-        bulk_load(sQ, p.qtiles + (ui * 2 + (i & 1)) * kKv4TileOp, kKv4TileOp, &sh->q_full);
-      }
+      port.src = p.qtiles + (ui * 2 + (i & 1)) * kKv4TileOp;
+      // the rows' numbers of two tiles ago have been read once the products of the last one could start
+      if (!feed.load(port, 0)) break;
       for (int c = lane; c < kTile; c += 32) {
         const int row = i * kTile + c, tok = row / p.G;
         const bool on = row < rows && pos0 + tok >= 0;
@@ -653,10 +665,7 @@ __global__ void __launch_bounds__(kKv4ColThreads, 2) kv4_chunk_weight_kernel(Kv4
       }
       mbar_arrive(&sh->row_full[k & 1]);
     }
-    if (*abort_flag && lane == 0 && k > 0) {
-      volatile int keep_waiting = 0;
-      mbar_wait(&sh->q_full, (k - 1) & 1, &keep_waiting, (1ull << 28));
-    }
+    feed.finish(port);
   }
 done:
   __syncwarp();

@@ -32,4 +32,26 @@ struct Kv4Fetch {
   MOBA_HD int last_values() const { return death; }
 };
 
+// A loader of query tiles in kv4_chunk.cuh, with BUFS buffers that each hold
+// one at a time. The port waits until buffer x is empty (phase `parity`; false:
+// the wait ran out), starts a copy into it, and waits until the copy has landed.
+// That last wait is made whatever has happened: another warp may give up on the
+// copy after this one has started it and has nothing left to do.
+template <int BUFS>
+struct Kv4Feeder {
+  uint32_t n[BUFS] = {};  // copies started
+  template <class Port>
+  MOBA_HD bool load(Port& port, int x) {
+    if (!port.empty(x, (n[x] & 1) ^ 1)) return false;
+    port.start(x);
+    ++n[x];
+    return true;
+  }
+  template <class Port>
+  MOBA_HD void finish(Port& port) {
+    for (int x = 0; x < BUFS; ++x)
+      if (n[x]) port.landed(x, (n[x] - 1) & 1);
+  }
+};
+
 }  // namespace moba

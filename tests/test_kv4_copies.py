@@ -70,3 +70,67 @@ int main() {
 def test_a_warp_that_gives_up_starts_no_copy_and_waits_for_those_under_way(tmp_path):
     r = run(tmp_path, ATTENTION)
     assert r.returncode == 0, r.stdout
+
+
+FEED = """
+// The loader starts its tiles; the products' warp then waits for them. `fails` is the wait that runs out, of those two
+// roles' in the order in which they happen; the copy that was waited for lands only when the loader waits for it.
+template <int BUFS>
+struct Port {
+  bool flag = false, flying[BUFS] = {};
+  int waits = 0, fails = -1, taken[BUFS] = {}, sent[BUFS] = {};
+  bool gone() { return flag || waits++ == fails ? (flag = true) : false; }
+  bool empty(int x, uint32_t parity) {
+    CHECK(parity == (uint32_t)((sent[x] & 1) ^ 1));
+    if (taken[x] < sent[x]) take(x);  // the products come by when the loader has to wait for them
+    return !gone();
+  }
+  void start(int x) {
+    CHECK(!flying[x]);
+    flying[x] = true;
+    ++sent[x];
+  }
+  void take(int x) {
+    if (gone()) return;
+    flying[x] = false;
+    ++taken[x];
+  }
+  void landed(int x, uint32_t parity) {
+    CHECK(parity == (uint32_t)((sent[x] - 1) & 1));
+    flying[x] = false;
+  }
+};
+
+template <int BUFS>
+void feed() {
+  for (int tiles = 0; tiles <= 4; ++tiles)
+    for (int fails = -1; fails <= 2 * BUFS * tiles; ++fails) {
+      Port<BUFS> port;
+      port.fails = fails;
+      moba::Kv4Feeder<BUFS> f;
+      bool going = true;
+      for (int t = 0; going && t < tiles; ++t)
+        for (int x = 0; going && x < BUFS; ++x) going = f.load(port, x);
+      bool left[BUFS];
+      const bool late = !port.flag;  // the other warps are still at work when the loader has nothing left to start
+      f.finish(port);
+      for (int x = 0; x < BUFS; ++x) left[x] = port.flying[x];
+      if (late)
+        for (int x = 0; x < BUFS; ++x)
+          if (port.taken[x] < port.sent[x]) port.take(x);
+      if (port.flag)  // given up: the block goes as it is
+        for (int x = 0; x < BUFS; ++x) CHECK(!left[x]);
+    }
+}
+
+int main() {
+  feed<1>();
+  feed<2>();
+  return bad != 0;
+}
+"""
+
+
+def test_no_query_tile_is_on_its_way_when_a_block_leaves(tmp_path):
+    r = run(tmp_path, FEED)
+    assert r.returncode == 0, r.stdout
