@@ -237,7 +237,7 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   if (rc) return rc;
   if (heads_q < 1 || heads_q % heads_kv)
     return fail(MOBA_ERR_INVALID_ARG, "heads_q (%d) must be a positive multiple of heads_kv (%d)", heads_q, heads_kv);
-  if (total < 0 || total * heads_q > INT32_MAX) return fail(MOBA_ERR_INVALID_ARG, "total * heads_q must be in [0, 2^31)");
+  if (total < 0 || total > INT32_MAX / heads_q) return fail(MOBA_ERR_INVALID_ARG, "total * heads_q must be in [0, 2^31)");
   if (!cu && total % batch) return fail(MOBA_ERR_INVALID_ARG, "without cu, total must be a multiple of batch");
   if (kmean) {
     rc = check_shape(capacity, heads_q, heads_kv, head_dim, block_size, topk);

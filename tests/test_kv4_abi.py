@@ -93,3 +93,10 @@ def test_the_binding_refuses_tensors_of_another_kind():
     with pytest.raises(ValueError):
         moba.kv4_evict(cache, torch.zeros(1, 2, 64), i, 1, 0, cache, torch.zeros(1, 2, 64))
     assert moba.kv4_cache(2, 3, 65, device="cpu").shape == (2, 3, 2, 9216)
+
+
+@pytest.mark.parametrize("total,heads_q", [(1 << 62, 4), ((1 << 62) + 2, 4), (1 << 61, 8), ((1 << 31) + 2, 2), ((1 << 63) - 1, 2)])
+def test_rows_whose_number_wraps_are_refused(lib, total, heads_q):
+    # total * heads_q is a small number, or a negative one, in 64 bits
+    assert call(lib, "attend", total=total, heads_q=heads_q) == BAD
+    assert "total" in moba.last_error()
