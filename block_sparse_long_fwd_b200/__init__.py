@@ -96,6 +96,32 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+def _lend(stream, *tensors):
+    """The stream as torch knows it. The caller's tensors that it will use may be dropped right after the call: their
+    memory is handed out again only behind the stream's work.
+    """
+    given = [x for x in tensors if x is not None]
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=given[0].device)
+    for x in given:
+        x.record_stream(stream)
+    return stream
+
+
+def _empty(like: torch.Tensor, stream, shape, dtype) -> torch.Tensor:
+    """Memory for an output, of the stream that writes it (None: the current one): another stream's could still be in
+    use there. Where the caller's current stream reads the result, that is waited for too before it is handed out again.
+    """
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    current = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        x = like.new_empty(shape, dtype=dtype)
+    if current != stream:
+        x.record_stream(current)
+    return x
+
+
 def _dev_bf16(x: torch.Tensor, name: str) -> torch.Tensor:
     if not (x.is_cuda and x.dtype == torch.bfloat16 and x.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor")
@@ -118,10 +144,12 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_size: int, topk
     Hkv = k.shape[1]
     if k.shape != (S, Hkv, d) or v.shape != k.shape:
         raise ValueError("k and v must be [S, heads_kv, head_dim] matching q")
+    if stream is not None:
+        stream = _lend(stream, q, k, v, out, lse)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q, stream, q.shape, q.dtype)
     if lse is None:
-        lse = torch.empty((Hq, S), dtype=torch.float32, device=q.device)
+        lse = _empty(q, stream, (Hq, S), torch.float32)
     _check(lib().moba_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), S, Hq, Hkv, d, block_size, topk,
                           out.data_ptr(), lse.data_ptr(), _stream(stream)))
     return out, lse
@@ -141,10 +169,12 @@ def fwd_chunk(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_size: int
     S, Hkv = k.shape[0], k.shape[1]
     if v.shape != k.shape or k.shape[2] != d or not 1 <= n <= S:
         raise ValueError("q must be [n, heads_q, head_dim] with 1 <= n <= S; k and v [S, heads_kv, head_dim]")
+    if stream is not None:
+        stream = _lend(stream, q, k, v, kmean, out, lse)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q, stream, q.shape, q.dtype)
     if lse is None:
-        lse = torch.empty((Hq, n), dtype=torch.float32, device=q.device)
+        lse = _empty(q, stream, (Hq, n), torch.float32)
     if kmean is not None:
         # block means from pool() for these k and block_size, kept by the caller
         if kmean.dtype != torch.float32 or not kmean.is_cuda or not kmean.is_contiguous():
@@ -174,10 +204,12 @@ def fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens, bl
     cu = torch.as_tensor(cu_seqlens, dtype=torch.int64, device="cpu").contiguous()
     if cu.dim() != 1 or cu.numel() < 2 or int(cu[-1]) != T:
         raise ValueError("cu_seqlens must be 1-D with batch + 1 entries ending at q.shape[0]")
+    if stream is not None:
+        stream = _lend(stream, q, k, v, out, lse)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q, stream, q.shape, q.dtype)
     if lse is None:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+        lse = _empty(q, stream, (Hq, T), torch.float32)
     _check(lib().moba_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu.data_ptr(), cu.numel() - 1, Hq, Hkv, d,
                                  block_size, topk, out.data_ptr(), lse.data_ptr(), _stream(stream)))
     return out, lse
@@ -198,9 +230,9 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, ls
         raise ValueError("k, v must be [S, heads_kv, head_dim]; out and dout [S, heads_q, head_dim]")
     if lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous() or lse.shape != (Hq, S):
         raise ValueError("lse must be a contiguous fp32 CUDA tensor [heads_q, S]")
-    dq = torch.empty_like(q)
-    dk = torch.empty_like(k)
-    dv = torch.empty_like(v)
+    if stream is not None:
+        stream = _lend(stream, q, k, v, out, lse, dout)
+    dq, dk, dv = (_empty(x, stream, x.shape, x.dtype) for x in (q, k, v))
     _check(lib().moba_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                           S, Hq, Hkv, d, block_size, topk, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                           _stream(stream)))
@@ -248,7 +280,9 @@ def pool(k: torch.Tensor, block_size: int, stream=None) -> torch.Tensor:
     _dev_bf16(k, "k")
     S, Hkv, d = k.shape
     nbp = max(nblocks(S, block_size) - 1, 0)
-    kmean = torch.empty((Hkv, max(nbp, 1), d), dtype=torch.float32, device=k.device)
+    if stream is not None:
+        stream = _lend(stream, k)
+    kmean = _empty(k, stream, (Hkv, max(nbp, 1), d), torch.float32)
     _check(lib().moba_pool(k.data_ptr(), S, Hkv, d, block_size, kmean.data_ptr(), _stream(stream)))
     return kmean[:, :nbp]
 
@@ -258,7 +292,9 @@ def gate(q: torch.Tensor, kmean: torch.Tensor, heads_kv: int, block_size: int, t
     _dev_bf16(q, "q")
     S, Hq, d = q.shape
     k_eff = min(topk, nblocks(S, block_size))
-    sel = torch.empty((Hq, S, k_eff), dtype=torch.int32, device=q.device)
+    if stream is not None:
+        stream = _lend(stream, q, kmean)
+    sel = _empty(q, stream, (Hq, S, k_eff), torch.int32)
     kp = kmean.data_ptr() if kmean is not None and kmean.numel() else None
     _check(lib().moba_gate(q.data_ptr(), kp, S, Hq, heads_kv, d, block_size, topk, sel.data_ptr(),
                            _stream(stream)))
@@ -320,6 +356,8 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, kv4: torch.Tensor, start: torch
     ap = _on(acc, "acc", torch.float32, (batch, hkv, cap), dev)
     if T == 0:
         return
+    if stream is not None:
+        stream = _lend(stream, k, v, kv4, start, cu, acc)
     _call(dev, stream, lib().moba_kv4_append, kp, vp, T, cp, sp, batch, hkv, HEAD_DIM, cap, kv4.data_ptr(), ap)
 
 
@@ -333,8 +371,9 @@ def kv4_load(kv4: torch.Tensor, lengths: torch.Tensor, n: int, first=None, strea
     fp = _on(first, "first", torch.int32, (batch,), dev)
     if not 0 <= n <= cap:
         raise ValueError("n must be in [0, capacity]")
-    k = kv4.new_empty((batch, n, hkv, HEAD_DIM), dtype=torch.bfloat16)
-    v = torch.empty_like(k)
+    if stream is not None:
+        stream = _lend(stream, kv4, lengths, first)
+    k, v = (_empty(kv4, stream, (batch, n, hkv, HEAD_DIM), torch.bfloat16) for _ in "kv")
     if n:
         _call(dev, stream, lib().moba_kv4_load, kv4.data_ptr(), lp, fp, batch, hkv, HEAD_DIM, cap, n, k.data_ptr(),
               v.data_ptr())
@@ -350,11 +389,12 @@ def kv4_pool(kv4: torch.Tensor, lengths: torch.Tensor, block_size: int, kmean=No
     if block_size < 1:
         raise ValueError("block_size must be positive")
     shape = (batch, hkv, cap // block_size, HEAD_DIM)
+    mp = _on(kmean, "kmean", torch.float32, shape, dev)
+    if stream is not None:
+        stream = _lend(stream, kv4, lengths, kmean)
     if kmean is None:
-        kmean = kv4.new_empty(shape, dtype=torch.float32)
+        kmean = _empty(kv4, stream, shape, torch.float32)
         mp = kmean.data_ptr()
-    else:
-        mp = _on(kmean, "kmean", torch.float32, shape, dev)
     if shape[2]:
         _call(dev, stream, lib().moba_kv4_pool, kv4.data_ptr(), lp, batch, hkv, HEAD_DIM, cap, block_size, mp)
     return kmean
@@ -388,16 +428,16 @@ def kv4_attend(q: torch.Tensor, kv4: torch.Tensor, lengths: torch.Tensor, cu=Non
         mp = mp if kmean.numel() else None  # less than a block of room: every key is in the own block
     elif block_size or topk:
         raise ValueError("block_size and topk need kmean")
+    op = _on(out, "out", torch.bfloat16, (T, hq, HEAD_DIM), dev)
+    ep = _on(lse, "lse", torch.float32, (hq, T), dev)
+    if stream is not None:
+        stream = _lend(stream, q, kv4, lengths, cu, kmean, acc, out, lse)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q, stream, q.shape, torch.bfloat16)
         op = out.data_ptr()
-    else:
-        op = _on(out, "out", torch.bfloat16, (T, hq, HEAD_DIM), dev)
     if lse is None:
-        lse = kv4.new_empty((hq, T), dtype=torch.float32)
+        lse = _empty(q, stream, (hq, T), torch.float32)
         ep = lse.data_ptr()
-    else:
-        ep = _on(lse, "lse", torch.float32, (hq, T), dev)
     if T:
         _call(dev, stream, lib().moba_kv4_attend, qp, T, cp, kv4.data_ptr(), lp, mp, batch, hq, hkv, HEAD_DIM, cap,
               block_size, topk, ap, op, ep)
@@ -425,8 +465,10 @@ def kv4_evict(kv4: torch.Tensor, acc: torch.Tensor, lengths: torch.Tensor, budge
     lp = _on(lengths, "lengths", torch.int32, (batch,), dev)
     if not 1 <= budget <= dcap or not 0 <= recent <= budget:
         raise ValueError("budget must be in [1, dst's capacity] and recent in [0, budget]")
-    new = torch.empty_like(lengths)
-    kept = lengths.new_empty((batch, hkv, budget))
+    if stream is not None:
+        stream = _lend(stream, kv4, acc, lengths, dst, dst_acc)
+    new = _empty(lengths, stream, (batch,), torch.int32)
+    kept = _empty(lengths, stream, (batch, hkv, budget), torch.int32)
     _call(dev, stream, lib().moba_kv4_evict, kv4.data_ptr(), ap, lp, batch, hkv, HEAD_DIM, cap, budget, recent,
           dst.data_ptr(), dp, dcap, kept.data_ptr(), new.data_ptr())
     return new, kept

@@ -669,6 +669,75 @@ def test_calls_on_other_streams():
         assert torch.equal(o, want[0]) and torch.equal(e, want[1])
 
 
+def pool_of(x):
+    """The stream whose memory a tensor lies in."""
+    at = x.data_ptr()
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= at < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("not the allocator's memory")
+
+
+def stream_calls():
+    kv4, _ = random_cache([256, 200], 2, 256, 2)
+    L, acc = ints([256, 200]), torch.zeros(2, 2, 256, device="cuda")
+    q = torch.zeros(2, 4, 128, dtype=torch.bfloat16, device="cuda")
+    p = torch.zeros(300, 2, 128, dtype=torch.bfloat16, device="cuda")
+    dst, dst_acc = moba.kv4_cache(2, 2, 128), torch.zeros(2, 2, 128, device="cuda")
+    out, lse = moba.fwd(p, p, p, 128, 2)
+    return {
+        "load": lambda s: moba.kv4_load(kv4, L, 256, stream=s),
+        "pool": lambda s: [moba.kv4_pool(kv4, L, 128, stream=s)],
+        "attend": lambda s: moba.kv4_attend(q, kv4, L, acc=acc, stream=s),
+        "evict": lambda s: moba.kv4_evict(kv4, acc, L, 100, 10, dst, dst_acc, stream=s),
+        "fwd": lambda s: moba.fwd(p, p, p, 128, 2, stream=s),
+        "fwd_chunk": lambda s: moba.fwd_chunk(p[200:], p, p, 128, 2, stream=s),
+        "fwd_varlen": lambda s: moba.fwd_varlen(p, p, p, [0, 100, 300], 128, 2, stream=s),
+        "bwd": lambda s: moba.bwd(p, p, p, out, lse, p, 128, 2, stream=s),
+        "key means": lambda s: [moba.pool(p, 128, stream=s)],
+        "gate": lambda s: [moba.gate(p, moba.pool(p, 128), 2, 128, 2, stream=s)],
+    }
+
+
+@pytest.mark.parametrize("name", ["load", "pool", "attend", "evict", "fwd", "fwd_chunk", "fwd_varlen", "bwd", "key means", "gate"])
+def test_outputs_lie_in_the_memory_of_the_stream_that_writes_them(name):
+    call = stream_calls()[name]
+    here, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    assert all(pool_of(x) == here.cuda_stream for x in call(None))
+    assert all(pool_of(x) == side.cuda_stream for x in call(side))
+    handle = type("handle", (), {"cuda_stream": side.cuda_stream})  # a stream of another library
+    assert all(pool_of(x) == side.cuda_stream for x in call(handle))
+    ok()
+
+
+def test_tensors_dropped_after_a_call_on_another_stream_are_not_handed_out_at_once():
+    kv4, _ = random_cache([1000], 2, 1024, 2)
+    L = ints([1000])
+    side = torch.cuda.Stream()
+    want = moba.kv4_load(kv4, L, 1000)
+    shape = want[0].shape
+    at = kv4.data_ptr()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # a tenth of a second of work before the call
+    got = moba.kv4_load(kv4, L, 1000, stream=side)
+    places = {x.data_ptr() for x in got}
+    size = kv4.shape
+    del kv4
+    taken = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(4)]  # while the call still waits
+    assert at not in {x.data_ptr() for x in taken}
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(200_000_000)
+    copy = [x.clone() for x in got]  # read here, later
+    del got
+    with torch.cuda.stream(side):
+        taken = [torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    assert not places & {x.data_ptr() for x in taken}
+    ok()
+    assert all(torch.equal(x, y) for x, y in zip(copy, want))
+
+
 @pytest.mark.parametrize("sparse", [False, True])
 def test_a_captured_decode_step_takes_the_lengths_of_its_replay(sparse):
     rng = np.random.default_rng(6)
