@@ -93,6 +93,13 @@ constexpr int kKv4ManyRows = 48;
 // 2101, and each pick more costs 36 against 95.
 constexpr int kKv4Union = 3 * moba::Kv4Many::R;
 
+// Bytes of scores that few rows may leave in scratch for their weights. MOBA_TEST_KEPT_SCORES=<n> sets another limit: a
+// test hook that reaches the kernel behind it without a large cache.
+size_t kept_scores_limit() {
+  const char* e = getenv("MOBA_TEST_KEPT_SCORES");
+  return e ? (size_t)strtoull(e, nullptr, 10) : (size_t)1 << 30;
+}
+
 bool g_kv4_ready[64] = {};
 
 // The device, and an error that an earlier call's kernels left behind.
@@ -327,7 +334,7 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   const size_t o_part = c.take((size_t)2 * p.ctas * p.R * 130 * 4);
   // the scores of few rows are kept for their weights, up to a GiB of them (sized by the capacity, which alone is known)
   const size_t seen = few && acc ? (size_t)nu * items * 4 * moba::kKv4Tile * 8 : 0;
-  const bool keep = seen > 0 && seen <= ((size_t)1 << 30);
+  const bool keep = seen > 0 && seen <= kept_scores_limit();
   const size_t o_seen = c.take(keep ? seen : 0);
   const size_t o_qtiles = c.take(chunk ? (size_t)nu * 2 * moba::kKv4TileOp : 0);
   const size_t o_qscale = c.take(chunk ? (size_t)nu * moba::kKv4ChunkRows * 4 : 0);

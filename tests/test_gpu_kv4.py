@@ -832,3 +832,60 @@ def test_offsets_beyond_32_bits():
         assert np.abs(f64(lse)[2 * h:2 * h + 2, 0] - np.log(total)).max() <= 2.0**-12
         assert (np.abs(f64(out)[0, 2 * h:2 * h + 2] - want) <= 2.0**-7 * np.abs(want) + 2.0**-10 * np.abs(vv).max() * 300 / L).all()
     assert abs(f64(acc)[0].sum(-1) - 2).max() <= 2.0**-8
+
+
+FEW = [(hkv, G, lengths, news, None) for hkv, G, lengths, news in DENSE]
+FEW += [(hkv, G, lengths, news, (block, topk)) for hkv, G, lengths, news, block, topk in SPARSE]
+FEW = [c for c in FEW if sum(c[3]) * c[1] <= 8 * len(c[3])]  # at most eight rows a sequence and kv head, on average
+FEW += [
+    # one sequence of many rows among short ones: its rows pass by eight at a time
+    (2, 4, [300, 64, 1, 200, 700, 90, 640, 513], [9, 1, 1, 1, 1, 1, 1, 1], None),
+    (1, 8, [600, 64, 1300], [3, 0, 0], None),
+    (1, 3, [130, 2000, 1, 0, 65, 64, 63, 128, 500], [1, 16, 1, 0, 1, 1, 1, 1, 1], None),
+    (2, 4, [300, 64, 1, 200, 700, 1900, 640, 513], [9, 1, 1, 1, 1, 1, 1, 1], (128, 2)),
+    (1, 8, [1600, 64, 1300], [3, 0, 0], (256, 2)),
+    (1, 3, [130, 2000, 1, 0, 65, 1064, 63, 128, 500], [1, 16, 1, 0, 1, 1, 1, 1, 1], (128, 3)),
+    (1, 1, [5, 4000], [0, 16], (128, 1)),
+    (1, 2, [9000, 100], [2, 5], (128, 4)),
+]
+
+
+@pytest.mark.parametrize("hkv,G,lengths,news,sparse", FEW)
+def test_weights_of_few_rows_whose_scores_are_not_kept(hkv, G, lengths, news, sparse, monkeypatch):
+    # where the scores would fill too much scratch they are computed again, key by key
+    monkeypatch.setenv("MOBA_TEST_KEPT_SCORES", "0")
+    attend_case(hkv, G, lengths, news, sparse=sparse, seed=len(lengths) + G)
+
+
+@pytest.mark.parametrize("hkv,G,lengths,news,sparse", FEW[-8:])
+def test_weights_of_a_sequence_with_many_rows_among_short_ones(hkv, G, lengths, news, sparse):
+    attend_case(hkv, G, lengths, news, sparse=sparse, seed=len(lengths) + G)
+
+
+@pytest.mark.parametrize("sparse", [None, (128, 2)])
+@pytest.mark.parametrize("n,kept", [(1, True), (1, False), (9, True), (100, True)])
+def test_garbage_behind_the_last_token_changes_nothing(n, kept, sparse, monkeypatch):
+    # for each of the kernels, with and without chosen blocks, and their weights
+    hkv, G, cap, lengths = 2, 4, 1024, [333, 700, 448]
+    if not kept:
+        monkeypatch.setenv("MOBA_TEST_KEPT_SCORES", "0")
+    kv4, _ = random_cache(lengths, hkv, cap, 5)
+    dirty = kv4.clone()
+    for b, L in enumerate(lengths):
+        dirty[b, :, -(-L // 64):] = 0xFF
+        if L % 64:
+            for off in (0, 4608):
+                dirty[b, :, L // 64, off + 64 * (L % 64):off + 4096] = 0xFF
+                dirty[b, :, L // 64, off + 4096 + 8 * (L % 64):off + 4608] = 0xFF
+    q = bf16(np.random.default_rng(1).standard_normal((3 * n, hkv * G, 128))).cuda()
+    got = []
+    for cache in (kv4, dirty):
+        more = {}
+        if sparse:
+            more = {"kmean": moba.kv4_pool(cache, ints(lengths), sparse[0]), "block_size": sparse[0], "topk": sparse[1]}
+        acc = torch.zeros(3, hkv, cap, device="cuda")
+        got.append((*moba.kv4_attend(q, cache, ints(lengths), acc=acc, **more), acc, *moba.kv4_load(cache, ints(lengths), cap)))
+    ok()
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    assert got[1][0].isfinite().all() and got[1][1].isfinite().all()
