@@ -106,6 +106,13 @@ __device__ __forceinline__ uint32_t kv4_scale_code(float step) {
   return min(max(code, kKv4ScaleMin), kKv4ScaleMax);
 }
 
+// hi - lo, rounded to odd: a span that fp32 does not hold (hi has 8 bits, lo may lie far below) stays on its side of
+// the ties between two scales, which are spans of few bits, and so does its 15th.
+__device__ __forceinline__ float kv4_span(float lo, float hi) {
+  const float d = __fsub_rz(hi, lo);
+  return __uint_as_float(__float_as_uint(d) | (__fsub_ru(hi, lo) != d ? 1u : 0u));
+}
+
 // A nudge for floor(x / s + 1/2): x has 8 significant bits and s four, so a
 // quotient between 1/2 and 16 that is not k + 1/2 is at least 2^-10 away from
 // it, while x * fl(1/s) is off by less than 2^-18: with the nudge added, halves
@@ -142,7 +149,7 @@ __device__ __forceinline__ uint4 kv4_quantise(const uint4 (&raw)[4], uint32_t* p
       hi = fmaxf(hi, fmaxf(x, y));
     }
   }
-  const uint32_t code = kv4_scale_code(__fdiv_rn(hi - lo, 15.f));
+  const uint32_t code = kv4_scale_code(__fdiv_rn(kv4_span(lo, hi), 15.f));
   const float inv = __frcp_rn(kv4_scale(code << 7));
   const float z = fminf(__fadd_rd(fmaf(-lo, inv, 0.5f + kKv4Nudge), 8388608.f) - 8388608.f, 15.f);
   const float k = inv * 0.0625f, c0 = (z + (0.5f + kKv4Nudge)) * 0.0625f;

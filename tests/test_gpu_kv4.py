@@ -889,3 +889,21 @@ def test_garbage_behind_the_last_token_changes_nothing(n, kept, sparse, monkeypa
     for x, y in zip(*got):
         assert torch.equal(x, y)
     assert got[1][0].isfinite().all() and got[1][1].isfinite().all()
+
+
+def test_append_of_spans_that_fp32_does_not_hold():
+    # 255 is 17 times 15, half way between the scales 16 and 18, of which 16 is even; a least value a little below zero
+    # makes the span larger, by less than fp32 shows, and the nearest scale the upper one
+    x = np.zeros((64, 1, 128))
+    for i in range(64):
+        for g in range(4):
+            top = 255.0 * 2.0 ** (g * 2 - 20 + i % 32)
+            top = top if top <= 28800 else 255.0
+            x[i, 0, 32 * g:32 * g + 8] = np.array([top, -top * 2.0 ** -(17 + i % 24), 0.3 * top, 0.94 * top, 0.97 * top,
+                                                   top / 2, 0, 0]) * (1 if i < 32 else -1)
+    kv4 = moba.kv4_cache(1, 1, 64)
+    moba.kv4_append(bf16(x).cuda(), bf16(-x).cuda(), kv4, ints([0]))
+    k, v = moba.kv4_load(kv4, ints([64]), 64)
+    ok()
+    assert np.array_equal(f64(k)[0, :, 0], ref.stored(f64(bf16(x)))[:, 0])
+    assert np.array_equal(f64(v)[0, :, 0], ref.stored(f64(bf16(-x)))[:, 0])
