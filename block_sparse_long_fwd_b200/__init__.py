@@ -371,9 +371,13 @@ def kv4_load(kv4: torch.Tensor, lengths: torch.Tensor, n: int, first=None, strea
     fp = _on(first, "first", torch.int32, (batch,), dev)
     if not 0 <= n <= cap:
         raise ValueError("n must be in [0, capacity]")
-    if stream is not None:
+    shape = (batch, n, hkv, HEAD_DIM)
+    if stream is None:
+        k = kv4.new_empty(shape, dtype=torch.bfloat16)
+        v = torch.empty_like(k)
+    else:
         stream = _lend(stream, kv4, lengths, first)
-    k, v = (_empty(kv4, stream, (batch, n, hkv, HEAD_DIM), torch.bfloat16) for _ in "kv")
+        k, v = (_empty(kv4, stream, shape, torch.bfloat16) for _ in "kv")
     if n:
         _call(dev, stream, lib().moba_kv4_load, kv4.data_ptr(), lp, fp, batch, hkv, HEAD_DIM, cap, n, k.data_ptr(),
               v.data_ptr())
@@ -393,7 +397,7 @@ def kv4_pool(kv4: torch.Tensor, lengths: torch.Tensor, block_size: int, kmean=No
     if stream is not None:
         stream = _lend(stream, kv4, lengths, kmean)
     if kmean is None:
-        kmean = _empty(kv4, stream, shape, torch.float32)
+        kmean = kv4.new_empty(shape, dtype=torch.float32) if stream is None else _empty(kv4, stream, shape, torch.float32)
         mp = kmean.data_ptr()
     if shape[2]:
         _call(dev, stream, lib().moba_kv4_pool, kv4.data_ptr(), lp, batch, hkv, HEAD_DIM, cap, block_size, mp)
@@ -433,10 +437,10 @@ def kv4_attend(q: torch.Tensor, kv4: torch.Tensor, lengths: torch.Tensor, cu=Non
     if stream is not None:
         stream = _lend(stream, q, kv4, lengths, cu, kmean, acc, out, lse)
     if out is None:
-        out = _empty(q, stream, q.shape, torch.bfloat16)
+        out = torch.empty_like(q) if stream is None else _empty(q, stream, q.shape, torch.bfloat16)
         op = out.data_ptr()
     if lse is None:
-        lse = _empty(q, stream, (hq, T), torch.float32)
+        lse = kv4.new_empty((hq, T), dtype=torch.float32) if stream is None else _empty(kv4, stream, (hq, T), torch.float32)
         ep = lse.data_ptr()
     if T:
         _call(dev, stream, lib().moba_kv4_attend, qp, T, cp, kv4.data_ptr(), lp, mp, batch, hq, hkv, HEAD_DIM, cap,
