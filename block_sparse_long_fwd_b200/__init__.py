@@ -414,7 +414,8 @@ def kv4_attend(q: torch.Tensor, kv4: torch.Tensor, lengths: torch.Tensor, cu=Non
     before a query is attended, or with ``kmean`` (``kv4_pool``'s) its own
     block and the ``topk - 1`` best past blocks, as in ``fwd_chunk``.
     ``acc`` (fp32 [batch, Hkv, capacity]) grows by the tokens' attention
-    weights. Returns (out [T, Hq, 128] bf16, lse [Hq, T] fp32).
+    weights. ``out`` may be ``q`` where no weights are asked for. Returns
+    (out [T, Hq, 128] bf16, lse [Hq, T] fp32).
     """
     batch, hkv, cap, dev = _kv4(kv4)
     if q.dim() != 3:
@@ -434,6 +435,8 @@ def kv4_attend(q: torch.Tensor, kv4: torch.Tensor, lengths: torch.Tensor, cu=Non
         raise ValueError("block_size and topk need kmean")
     op = _on(out, "out", torch.bfloat16, (T, hq, HEAD_DIM), dev)
     ep = _on(lse, "lse", torch.float32, (hq, T), dev)
+    if op is not None and abs(op - qp) < q.nbytes and (op != qp or acc is not None):
+        raise ValueError("out must not overlap q (without acc it may be q): rows are read after others are written")
     if stream is not None:
         stream = _lend(stream, q, kv4, lengths, cu, kmean, acc, out, lse)
     if out is None:

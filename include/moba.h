@@ -402,7 +402,9 @@ int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch,
  *            scores stay in scratch until then: 32 bytes a sequence, kv head
  *            and token of the capacity, or of the chosen blocks, up to 1 GiB;
  *            where they would need more, they are computed again.)
- * out        device bf16 output [total][heads_q][head_dim].
+ * out        device bf16 output [total][heads_q][head_dim]. It must not
+ *            overlap q, but without acc it may be q itself (with acc the
+ *            queries are read again once rows of out have been written).
  * lse        device fp32 output [heads_q][total], natural log.
  */
 int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu,

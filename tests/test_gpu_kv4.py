@@ -907,3 +907,22 @@ def test_append_of_spans_that_fp32_does_not_hold():
     ok()
     assert np.array_equal(f64(k)[0, :, 0], ref.stored(f64(bf16(x)))[:, 0])
     assert np.array_equal(f64(v)[0, :, 0], ref.stored(f64(bf16(-x)))[:, 0])
+
+
+@pytest.mark.parametrize("n,sparse", [(1, None), (9, None), (100, None), (1, (128, 2)), (9, (128, 2)), (100, (128, 2))])
+def test_results_in_the_place_of_the_queries(n, sparse):
+    lengths = [700, 333]
+    kv4, _ = random_cache(lengths, 2, 704, 5)
+    kmean = moba.kv4_pool(kv4, ints(lengths), 128)
+    more = {"kmean": kmean, "block_size": sparse[0], "topk": sparse[1]} if sparse else {}
+    q = bf16(np.random.default_rng(1).standard_normal((2 * n, 8, 128))).cuda()
+    want = moba.kv4_attend(q, kv4, ints(lengths), **more)
+    buf = torch.cat((q, q[:1]))
+    acc = torch.zeros(2, 2, 704, device="cuda")
+    with pytest.raises(ValueError):  # the weights' kernels read the queries again
+        moba.kv4_attend(buf[:2 * n], kv4, ints(lengths), out=buf[:2 * n], acc=acc, **more)
+    with pytest.raises(ValueError):
+        moba.kv4_attend(buf[:2 * n], kv4, ints(lengths), out=buf[1:], **more)
+    got = moba.kv4_attend(buf[:2 * n], kv4, ints(lengths), out=buf[:2 * n], **more)
+    ok()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and (acc == 0).all()
