@@ -638,7 +638,17 @@ struct Kv4Cfg {
 using Kv4Few = Kv4Cfg<1, 16, true>;    // up to 8 rows
 using Kv4Many = Kv4Cfg<2, 8, false>;   // up to 16 rows
 
-constexpr float kKv4Low = -1e30f;  // running maximum before the first score
+constexpr float kKv4Low = -3.402823466e38f;  // reference before the first score: fp32's lowest
+// A row's reference of this magnitude is coarse: from here on fp32 numbers are 2^-3 and more apart, and score minus
+// reference, exact but for that, may miss the 12 that it should be by as much. The reference is then rounded down, so
+// that the largest weight is 2^12 at least, and what would exceed 2^15, fp16's last power of two, is cut to it: scores
+// that close together are not told apart by fp32 sums of that size anyway.
+constexpr float kKv4Coarse = 1048576.f;
+__device__ __forceinline__ float kv4_reference(float top, float scale) {
+  const float mx = top * scale;
+  return fabsf(mx) < kKv4Coarse ? mx - 12.f : __fmaf_rd(top, scale, -12.f);
+}
+__device__ __forceinline__ float kv4_cut(float x) { return x > 15.f ? 15.f : x; }  // a NaN stays one
 
 // Per tile of 64 keys a warp widens the keys' codes into the A operand of
 // S^T = K Q^T (keys x rows; the codes' own order is the operand's), finds the
@@ -889,18 +899,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p
             float mx = -INFINITY;
 #pragma unroll
             for (int g = 0; g < 4; ++g) mx = fmax3(mx, sc[g][nt][x], sc[g][nt][x + 2]);
-            mx *= q1;
 #pragma unroll
             for (int d2 = 4; d2 < 32; d2 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d2));
-            const bool move = mx > m1 + 15.f;
-            n2[x] = move ? 12.f - mx : -m1;
-            a2[x] = move ? ex2_approx(m1 - (mx - 12.f)) : 1.f;
+            const bool move = mx * q1 > m1 + 15.f;
+            n2[x] = move ? -kv4_reference(mx, q1) : -m1;
+            a2[x] = move ? ex2_approx(m1 + n2[x]) : 1.f;
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) o[nt][mt][x] *= a2[x], o[nt][mt][x + 2] *= a2[x];
           }
           nm[nt] = f2_pack(n2[0], n2[1]);
           l2[nt] = f2_pack(f2_lo(l2[nt]) * a2[0], f2_hi(l2[nt]) * a2[1]);
           shifted();
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) t[g][x] = kv4_cut(t[g][x]);
         }
 #pragma unroll
         for (int g = 0; g < 4; ++g) {

@@ -277,15 +277,23 @@ __global__ void __launch_bounds__(kKv4ChunkThreads, 1) kv4_chunk_kernel(Kv4AttnP
         }
         const float mx = qs * fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
         // the reference moves as in kv4_attn.cuh: weights stay under 2^15
-        const bool move = mx > ref + 15.f;
+        const bool move = mx > __fadd_rd(ref, 15.f);
         float factor = 1.f;
         if (move) {
-          factor = ex2_approx(ref - (mx - 12.f));
-          ref = mx - 12.f;
+          const float to = __fadd_ru(mx, -12.f);
+          factor = ex2_approx(ref - to);
+          ref = to;
         }
         uint32_t pk[64];
         {
-          const uint64_t c2 = f2_pack(qs, qs), nm2 = f2_pack(-ref, -ref);
+          uint64_t c2 = f2_pack(qs, qs);
+          const uint64_t nm2 = f2_pack(-ref, -ref);
+          // a coarse reference: scores rounded as the largest was then lie on one grid with it, and the largest 0 to 15 above
+          if (fabsf(ref) >= kKv4Coarse && ref > kKv4Low) {
+#pragma unroll
+            for (int e = 0; e < 128; ++e) r[e] = __float_as_uint(__fmul_rn(__uint_as_float(r[e]), qs));
+            c2 = f2_pack(1.f, 1.f);
+          }
           uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
           for (int e = 0; e < 128; e += 2) {

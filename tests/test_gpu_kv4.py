@@ -926,3 +926,47 @@ def test_results_in_the_place_of_the_queries(n, sparse):
     got = moba.kv4_attend(buf[:2 * n], kv4, ints(lengths), out=buf[:2 * n], **more)
     ok()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and (acc == 0).all()
+
+
+def scores_of_size(size, n, sparse):
+    """A call whose scores are some `size` in magnitude: (out, lse, growth of acc, z, d, values), in fp64."""
+    hkv, G, L, cap = 1, 4, 700, 704
+    rng = np.random.default_rng(5)
+    k, v = (f64(bf16(rng.standard_normal((hkv, cap, 128)))) for _ in "kv")
+    q = rng.standard_normal((n, hkv * G, 128)) * abs(size)
+    if size < 0:  # every score is negative
+        k, q = np.abs(k) + 1, -np.abs(q)
+    tiles, q = ref.pack(k, v), bf16(q)
+    k, v = ref.unpack(tiles)
+    kv4, lens, a0 = torch.from_numpy(tiles[None]).cuda(), ints([L]), torch.rand(1, hkv, cap, device="cuda")
+    acc, more = a0.clone(), {}
+    if sparse:
+        more = {"kmean": moba.kv4_pool(kv4, lens, sparse[0]), "block_size": sparse[0], "topk": sparse[1]}
+    out, lse = moba.kv4_attend(q.cuda(), kv4, lens, acc=acc, **more)
+    ok()
+    q = f64(q)
+    mask = ref.seen(q, L, n, f64(more["kmean"])[0, 0] if sparse else None, *(sparse or ()))
+    z = np.where(mask, np.einsum("ngd,sd->ngs", q, k[0, :L]) / np.sqrt(128), -np.inf)
+    d = 140 * 2 * U * np.einsum("ngd,sd->ngs", np.abs(q), np.abs(k[0, :L])).max(-1) / np.sqrt(128)
+    return f64(out), f64(lse).T, (f64(acc) - f64(a0))[0, 0], z, d, v[0, :L]
+
+
+SIZES = [1e5, 1e7, 3e7, 1e9, 1e20, 1e36, -1e31]
+
+
+@pytest.mark.parametrize("sparse", [None, (128, 3)])
+@pytest.mark.parametrize("n", [1, 9, 100])
+@pytest.mark.parametrize("size", SIZES)
+def test_scores_of_any_size_give_finite_results(size, n, sparse):
+    """Scores far beyond what fp32 holds to a whole: the result is the value of the best key, or lies between those of
+    the keys that the scores' error (d, as above) does not tell apart from it; the others weigh less than e^-30 each."""
+    out, lse, _, z, d, v = scores_of_size(size, n, sparse)
+    near = z >= (z.max(-1) - 2 * d - 30)[..., None]
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    assert (np.abs(lse - z.max(-1)) <= d + np.log(len(v)) + 4 * U * np.abs(lse)).all()
+    for i in range(n):
+        for g in range(out.shape[1]):
+            some = v[near[i, g]]
+            # rounded to bf16, the weights to fp16 (the sum of them is not): 2^-8 and 2^-10, and 700 times e^-30
+            tol = (2.0**-8 + 2.0**-10) * np.abs(some).max(0) + 2.0**-30
+            assert (out[i, g] >= some.min(0) - tol).all() and (out[i, g] <= some.max(0) + tol).all()
