@@ -1134,6 +1134,13 @@ __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams
 
 // ------------------------------------------------------------------ accumulated weights
 
+// log2 of a row's sum, for its weights 2^(score - this). A row without keys has scores of minus infinity alone. One that
+// is not finite has no sum: 0 leaves its scores as they are, not finite, and those that are masked at minus infinity.
+__device__ __forceinline__ float kv4_log2_sum(float lse) {
+  const float x = lse * 1.4426950408889634f;
+  return fabsf(x) < INFINITY ? x : 0.f;
+}
+
 constexpr int kKv4WeightThreads = 128, kKv4WeightTiles = 8;
 
 // acc[key] += sum over the rows of the kv head of 2^(score - lse), one warp per
@@ -1175,7 +1182,7 @@ __global__ void __launch_bounds__(kKv4WeightThreads, HOLD ? 2 : 5) kv4_weight_ke
       const int row2 = r0 + 2 * qd + x;
       const bool on = row2 < rows;
       pos[x] = on ? pos0 + row2 / p.G : -1;
-      le[x] = on ? p.lse[(int64_t)(h * p.G + row2 % p.G) * p.total + t0 + row2 / p.G] * 1.4426950408889634f : 0.f;
+      le[x] = on ? kv4_log2_sum(p.lse[(int64_t)(h * p.G + row2 % p.G) * p.total + t0 + row2 / p.G]) : 0.f;
     }
   };
   const bool one = rows <= 8;
@@ -1304,13 +1311,11 @@ __global__ void __launch_bounds__(kKv4SeenThreads) kv4_seen_kernel(Kv4AttnParams
     const Kv4Unit u = p.units[ui];
     if (u.tiles == 0) continue;
     const int before = p.before[ui];
-    // log2 of the rows' sums; a row without keys has scores of minus infinity alone
     float le[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const int rr = u.row0 + r;
-      const float e = r < u.rows ? p.lse[(int64_t)(h * p.G + rr % p.G) * p.total + u.t0 + rr / p.G] : 0.f;
-      le[r] = e != -INFINITY ? e * 1.4426950408889634f : 0.f;
+      le[r] = r < u.rows ? kv4_log2_sum(p.lse[(int64_t)(h * p.G + rr % p.G) * p.total + u.t0 + rr / p.G]) : 0.f;
     }
     int block = -1, at = -1;  // the block that was looked up, and its place in the list
 #pragma unroll

@@ -665,10 +665,10 @@ __global__ void __launch_bounds__(kKv4ColThreads, 2) kv4_chunk_weight_kernel(Kv4
       for (int c = lane; c < kTile; c += 32) {
         const int row = i * kTile + c, tok = row / p.G;
         const bool on = row < rows && pos0 + tok >= 0;
-        // a row without keys, or behind the last: the score plus minus infinity
+        // a row without keys, or behind the last: the score minus infinity
         const float scale = on ? __ldcg(p.qscale + ui * kKv4ChunkRows + (i & 1) * kTile + c) : 1.f;
-        const float lse = on ? __ldcg(p.lse + (int64_t)(h * p.G + row % p.G) * p.total + t0 + tok) : INFINITY;
-        sh->row[k & 1][c] = make_float2(scale, -lse * 1.4426950408889634f);
+        const float sum = on ? kv4_log2_sum(__ldcg(p.lse + (int64_t)(h * p.G + row % p.G) * p.total + t0 + tok)) : INFINITY;
+        sh->row[k & 1][c] = make_float2(scale, -sum);
         sh->pos[k & 1][c] = row < rows ? pos0 + tok : INT32_MAX;
       }
       mbar_arrive(&sh->row_full[k & 1]);

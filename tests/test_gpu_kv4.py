@@ -711,29 +711,31 @@ def test_outputs_lie_in_the_memory_of_the_stream_that_writes_them(name):
     ok()
 
 
-def test_tensors_dropped_after_a_call_on_another_stream_are_not_handed_out_at_once():
+@pytest.mark.parametrize("cycles", [200_000_000, 2_000_000_000])
+def test_tensors_dropped_after_a_call_on_another_stream_are_not_handed_out_at_once(cycles):
     kv4, _ = random_cache([1000], 2, 1024, 2)
     L = ints([1000])
     side = torch.cuda.Stream()
     want = moba.kv4_load(kv4, L, 1000)
-    shape = want[0].shape
-    at = kv4.data_ptr()
+    at, size = kv4.data_ptr(), kv4.shape
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(200_000_000)  # a tenth of a second of work before the call
+        torch.cuda._sleep(cycles)  # a tenth of a second of work, or one, before the call
     got = moba.kv4_load(kv4, L, 1000, stream=side)
-    places = {x.data_ptr() for x in got}
-    size = kv4.shape
     del kv4
-    taken = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(4)]  # while the call still waits
-    assert at not in {x.data_ptr() for x in taken}
-    torch.cuda.current_stream().wait_stream(side)
-    torch.cuda._sleep(200_000_000)
+    taken = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    waiting = not side.query()  # the host has not slept itself
+    assert not waiting or at not in {x.data_ptr() for x in taken}
+    here = torch.cuda.current_stream()
+    here.wait_stream(side)
+    torch.cuda._sleep(cycles)
     copy = [x.clone() for x in got]  # read here, later
+    places, shape = {x.data_ptr() for x in got}, got[0].shape
     del got
     with torch.cuda.stream(side):
-        taken = [torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
-    assert not places & {x.data_ptr() for x in taken}
+        taken = [torch.empty(shape, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    waiting = not here.query()
+    assert not waiting or not places & {x.data_ptr() for x in taken}
     ok()
     assert all(torch.equal(x, y) for x, y in zip(copy, want))
 
@@ -970,3 +972,30 @@ def test_scores_of_any_size_give_finite_results(size, n, sparse):
             # rounded to bf16, the weights to fp16 (the sum of them is not): 2^-8 and 2^-10, and 700 times e^-30
             tol = (2.0**-8 + 2.0**-10) * np.abs(some).max(0) + 2.0**-30
             assert (out[i, g] >= some.min(0) - tol).all() and (out[i, g] <= some.max(0) + tol).all()
+
+
+@pytest.mark.parametrize("n,kept", [(2, True), (2, False), (9, True), (100, True)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_query_that_is_not_finite_spoils_the_weights_of_its_own_keys_alone(n, kept, bad, monkeypatch):
+    hkv, G, L, cap = 2, 4, 700, 768
+    if not kept:
+        monkeypatch.setenv("MOBA_TEST_KEPT_SCORES", "0")
+    kv4, _ = random_cache([L], hkv, cap, 5)
+    q = bf16(np.random.default_rng(1).standard_normal((n, hkv * G, 128))).cuda()
+    dirty = q.clone()
+    row = n // 2 - 1
+    dirty[row, 1, 5] = bad
+    kmean = moba.kv4_pool(kv4, ints([L]), 128)
+    for more in ({}, {"kmean": kmean, "block_size": 128, "topk": 2}):
+        a, b = (torch.zeros(1, hkv, cap, device="cuda") for _ in "ab")
+        moba.kv4_attend(q, kv4, ints([L]), acc=a, **more)
+        moba.kv4_attend(dirty, kv4, ints([L]), acc=b, **more)
+        ok()
+        own = L - n + row  # the row's position
+        assert torch.equal(a[:, 1], b[:, 1]) and torch.equal(a[0, 0, own + 1:], b[0, 0, own + 1:])
+        spoilt = ~b[0, 0, :own + 1].isfinite()
+        if not more:
+            assert spoilt.all() if bad != bad else spoilt.any()
+        else:  # its own block, and one other
+            blocks = spoilt.nonzero()[:, 0].div(128, rounding_mode="floor").unique().tolist()
+            assert own // 128 in blocks and len(blocks) <= 2
