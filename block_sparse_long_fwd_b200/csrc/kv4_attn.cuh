@@ -1134,11 +1134,14 @@ __global__ void __launch_bounds__(kKv4JoinThreads) kv4_join_kernel(Kv4AttnParams
 
 // ------------------------------------------------------------------ accumulated weights
 
-// log2 of a row's sum, for its weights 2^(score - this). A row without keys has scores of minus infinity alone. One that
-// is not finite has no sum: 0 leaves its scores as they are, not finite, and those that are masked at minus infinity.
+// log2 of a row's sum, for its weights 2^(score - this). It comes from lse, a number of fp32, and is off by up to 3.5
+// half units of its last place, of which a large one is coarse: so that no weight exceeds one, those are taken 4 whole
+// ones higher (2^-21 of them; below 2^16 that would be at most 2^-5, and the scores' own error is larger). A row without
+// keys has scores of minus infinity alone. One that is not finite has no sum: 0 leaves its scores as they are, not
+// finite, and those that are masked at minus infinity.
 __device__ __forceinline__ float kv4_log2_sum(float lse) {
   const float x = lse * 1.4426950408889634f;
-  return fabsf(x) < INFINITY ? x : 0.f;
+  return !(fabsf(x) < INFINITY) ? 0.f : fabsf(x) < 65536.f ? x : fmaf(fabsf(x), 4.76837158203125e-07f, x);
 }
 
 constexpr int kKv4WeightThreads = 128, kKv4WeightTiles = 8;

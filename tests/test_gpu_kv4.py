@@ -974,6 +974,21 @@ def test_scores_of_any_size_give_finite_results(size, n, sparse):
             assert (out[i, g] >= some.min(0) - tol).all() and (out[i, g] <= some.max(0) + tol).all()
 
 
+@pytest.mark.parametrize("sparse", [None, (128, 3)])
+@pytest.mark.parametrize("n,kept", [(1, True), (1, False), (9, True), (100, True)])
+@pytest.mark.parametrize("size", SIZES)
+def test_weights_of_scores_of_any_size(size, n, kept, sparse, monkeypatch):
+    # a row gives a key a weight of one at most, and none to the keys far from its best
+    if not kept:
+        monkeypatch.setenv("MOBA_TEST_KEPT_SCORES", "0")
+    _, _, grown, z, d, v = scores_of_size(size, n, sparse)
+    L, rows = len(v), n * z.shape[1]
+    most = (z >= (z.max(-1) - 2 * d - 30)[..., None]).sum((0, 1))
+    # one rounding of fp32 for each row, at magnitudes of rows + 1, and L times e^-30
+    assert np.isfinite(grown).all() and (grown[L:] == 0).all()
+    assert (grown[:L] >= -2 * U).all() and (grown[:L] <= most + (rows + 2) * (rows + 1) * U + 2.0**-30).all()
+
+
 @pytest.mark.parametrize("n,kept", [(2, True), (2, False), (9, True), (100, True)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_a_query_that_is_not_finite_spoils_the_weights_of_its_own_keys_alone(n, kept, bad, monkeypatch):
