@@ -1014,3 +1014,108 @@ def test_a_query_that_is_not_finite_spoils_the_weights_of_its_own_keys_alone(n, 
         else:  # its own block, and one other
             blocks = spoilt.nonzero()[:, 0].div(128, rounding_mode="floor").unique().tolist()
             assert own // 128 in blocks and len(blocks) <= 2
+
+
+@pytest.mark.parametrize("sparse", [None, (128, 2)])
+@pytest.mark.parametrize("news", [[1, 1, 1], [9, 3, 11], [100, 0, 70]])
+def test_rows_before_the_first_sequence_are_left_alone(news, sparse):
+    hkv, G, cap, lengths, lead, pad = 2, 4, 768, [700, 333, 130], 5, 2
+    kv4, vals = random_cache(lengths, hkv, cap, 5)
+    T = sum(news)
+    cu = ints(lead + np.concatenate(([0], np.cumsum(news))))
+    q = bf16(np.random.default_rng(1).standard_normal((lead + T + pad, hkv * G, 128)))
+    kmean = moba.kv4_pool(kv4, ints(lengths), sparse[0]) if sparse else None
+    more = {"kmean": kmean, "block_size": sparse[0], "topk": sparse[1]} if sparse else {}
+    out = torch.full((lead + T + pad, hkv * G, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((hkv * G, lead + T + pad), 7.0, device="cuda")
+    acc = torch.zeros(3, hkv, cap, device="cuda")
+    moba.kv4_attend(q.cuda(), kv4, ints(lengths), cu=cu, acc=acc, out=out, lse=lse, **more)
+    k = bf16(np.random.default_rng(2).standard_normal((lead + T + pad, hkv, 128)))
+    store = moba.kv4_cache(3, hkv, 128)
+    moba.kv4_append(k.cuda(), k.cuda(), store, ints([0, 7, 20]), cu=cu)
+    loaded, _ = moba.kv4_load(store, ints([128] * 3), 128)
+    ok()
+    rest = torch.ones(lead + T + pad, dtype=torch.bool, device="cuda")
+    rest[lead:lead + T] = False
+    assert (out[rest] == 7).all() and (lse[:, rest] == 7).all()
+    check_attend((out[lead:lead + T], lse[:, lead:lead + T], acc, torch.zeros_like(acc)), f64(q)[lead:lead + T], vals,
+                 lengths, news, hkv, sparse, f64(kmean) if sparse else None)
+    want, at = np.zeros((3, 128, hkv, 128)), lead
+    for b, (start, n) in enumerate(zip([0, 7, 20], news)):
+        want[b, start:start + n] = ref.stored(f64(k)[at:at + n])
+        at += n
+    assert np.array_equal(f64(loaded), want)
+
+
+@pytest.mark.parametrize("cu", [[0, 1, 500], [0, 2, 1], [-3, 1, 2], [0, 2, 1, 2]])
+def test_offsets_outside_the_rows_are_read_as_no_query_and_reported(cu):
+    batch = len(cu) - 1
+    kv4, vals = random_cache([300] * batch, 1, 320, 5)
+    for G in (1, 40):
+        q = bf16(np.random.default_rng(1).standard_normal((2, G, 128))).cuda()
+        acc = torch.zeros(batch, 1, 320, device="cuda")
+        moba.kv4_attend(q, kv4, ints([300] * batch), cu=ints(cu), acc=acc)
+        assert moba.device_status() == moba.MOBA_ERR_DEVICE_CHECK
+        want = moba.kv4_attend(q[:1], kv4[:1], ints([300]))  # and the next call is as ever
+        ok()
+        check_attend((*want, None, None), f64(q)[:1], vals[:1], [300], [1], 1)
+
+
+def test_calls_from_two_threads_at_once():
+    import threading
+
+    lengths = [900, 1500]
+    kv4, _ = random_cache(lengths, 2, 1536, 2)
+    lens, kmean = ints(lengths), moba.kv4_pool(kv4, ints(lengths), 128)
+    cases = []
+    for i, n in enumerate((1, 40)):
+        q = bf16(np.random.default_rng(i).standard_normal((2 * n, 8, 128))).cuda()
+        more = {"kmean": kmean, "block_size": 128, "topk": 3} if i else {}
+        acc = torch.zeros(2, 2, 1536, device="cuda")
+        cases.append((q, more, (*moba.kv4_attend(q, kv4, lens, acc=acc, **more), acc)))
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        q, more, _ = cases[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                acc = torch.zeros(2, 2, 1536, device="cuda")
+                got[i].append((*moba.kv4_attend(q, kv4, lens, acc=acc, **more), acc))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    ok()
+    for i in (0, 1):
+        assert len(got[i]) == 50
+        for r in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(r, cases[i][2]))
+
+
+def test_captured_eviction_takes_the_weights_and_lengths_of_its_replay():
+    hkv, cap, rng = 2, 1024, np.random.default_rng(3)
+    kv4, vals = random_cache([1000, 700], hkv, cap, 2)
+    lengths, acc = ints([1000, 700]), torch.zeros(2, hkv, cap, device="cuda")
+    dst, dst_acc = moba.kv4_cache(2, hkv, 320), torch.zeros(2, hkv, 320, device="cuda")
+    moba.kv4_evict(kv4, acc, lengths, 300, 20, dst, dst_acc)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        new, kept = moba.kv4_evict(kv4, acc, lengths, 300, 20, dst, dst_acc)
+        k, _ = moba.kv4_load(dst, new, 300)
+    for now in ([1000, 700], [640, 0], [299, 301]):
+        a = rng.random((2, hkv, cap)).astype(np.float32)
+        acc.copy_(torch.from_numpy(a))
+        lengths.copy_(ints(now))
+        g.replay()
+        ok()
+        assert new.tolist() == [min(L, 300) for L in now]
+        for b, L in enumerate(now):
+            for h in range(hkv):
+                want = ref.evict(a[b, h].astype(np.float64), L, 300, 20)
+                assert np.array_equal(kept[b, h, :len(want)].cpu().numpy(), want) and (kept[b, h, len(want):] == -1).all()
+                assert np.array_equal(f64(k[b, :len(want), h]), vals[b][0][h, want]) and (k[b, len(want):] == 0).all()
