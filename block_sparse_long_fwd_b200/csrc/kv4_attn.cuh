@@ -654,11 +654,13 @@ __device__ __forceinline__ float kv4_cut(float x) { return x > 15.f ? 15.f : x; 
 // S^T = K Q^T (keys x rows; the codes' own order is the operand's), finds the
 // weights in registers, transposes them 8 x 8, and widens the values' codes into
 // the A operand of O^T += V^T P^T. 16 warps of 128 registers (12 of 168 took 276
-// us where these took 262). Bound by the issue slots, not HBM: 311 instructions
-// for 16 keys and up to 8 rows. 1M tokens of 8 heads: 238 us, 5.1 TB/s, 78 % of
-// a copy's rate. Where there are few tiles the chain counts: 12 us for 4096
-// tokens of one head; 47 for 128K tokens of 8, of which the plan takes 4, the
-// tiles 27 and the two joins 6.
+// us where these took 262). 311 instructions for 16 keys and up to 8 rows. 1M
+// tokens of 8 heads: 238 us, 5.1 TB/s, 78 % of a copy's rate. Neither HBM nor
+// the issue slots are full (a ragged batch uses 64 % of them at 4.5 TB/s): its
+// warps wait in turn for the pipes of half-precision and logic operations, for
+// their own last result and for the scheduler. Where there are few tiles the
+// chain counts: 12 us for 4096 tokens of one head; 47 for 128K tokens of 8, of
+// which the plan takes 4, the tiles 27 and the two joins 6.
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(Kv4AttnParams p) {
   constexpr int NT = C::NT, R = C::R;

@@ -81,14 +81,16 @@ cudaError_t set_kv4_chunk_smem() {
 
 // Rows of a sequence and kv head, on average, above which the tcgen05 kernel
 // (256 rows a unit) takes over from mma.sync (16 rows a unit, every key widened
-// for each of them). At 32K tokens, 32 / 8 heads, one sequence: 32 rows 43
+// for each of them): one kernel for all sequences of a call, since the host
+// does not know the offsets. At 32K tokens, 32 / 8 heads, one sequence: 32 rows 43
 // against 44 us, 64 rows 45 against 65, 2048 rows 293 against 1430; 16
 // sequences of 8K: 16 rows 162 against 70, 64 rows 173 against 219.
 constexpr int kKv4ManyRows = 48;
 
 // With a gate the tcgen05 kernel goes over all keys and masks, where mma.sync goes over the blocks that its 16 rows
-// chose, at most 16 topk blocks of the capacity, at some four times the cost a row and key. So the former takes over
-// where those are a third of the cache. 512 tokens of 32 / 8 heads: at 32K tokens, block 512, top-12 (all of it) 487
+// chose, at most 16 topk blocks, at some four times the cost a row and key. So the former takes over where those are a
+// third of the cache: of its capacity, since the host does not know the lengths (a short sequence in a large cache is
+// left to mma.sync). 512 tokens of 32 / 8 heads: at 32K tokens, block 512, top-12 (all of it) 487
 // against 1306 us; at 128K, block 4096, top-12 1372 against 4949; at 128K, block 128, top-12 (a fifth) 2777 against
 // 2101, and each pick more costs 36 against 95.
 constexpr int kKv4Union = 3 * moba::Kv4Many::R;
@@ -332,7 +334,8 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
   const size_t o_chosen = c.take(gp.kmean && (acc || masked) ? (size_t)gnu * gp.blocks * 4 : 0);
   const size_t o_scores = c.take((size_t)clusters * gp.R * gp.means * 8);
   const size_t o_part = c.take((size_t)2 * p.ctas * p.R * 130 * 4);
-  // the scores of few rows are kept for their weights, up to a GiB of them (sized by the capacity, which alone is known)
+  // the scores of few rows are kept for their weights, up to a GiB of them (sized by the capacity and by the unit slots,
+  // which alone are known: up to two slots for a sequence's one unit)
   const size_t seen = few && acc ? (size_t)nu * items * 4 * moba::kKv4Tile * 8 : 0;
   const bool keep = seen > 0 && seen <= kept_scores_limit();
   const size_t o_seen = c.take(keep ? seen : 0);
@@ -363,8 +366,8 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
     } else if (chunk) {
       launch_chained(moba::kv4_prep_kernel, dim3((unsigned)nu, moba::kKv4ChunkRows * 16 / moba::kKv4PrepThreads),
                      dim3(moba::kKv4PrepThreads), 0, st, p);
-      launch_chained(masked ? moba::kv4_chunk_kernel<true> : moba::kv4_chunk_kernel<false>, dim3(p.ctas), dim3(moba::kKv4ChunkThreads), moba::kKv4ChunkSmemBytes, st,
-                     p);
+      launch_chained(masked ? moba::kv4_chunk_kernel<true> : moba::kv4_chunk_kernel<false>, dim3(p.ctas),
+                     dim3(moba::kKv4ChunkThreads), moba::kKv4ChunkSmemBytes, st, p);
     } else {
       launch_kv4_attn<moba::Kv4Many>(p, st);
     }
@@ -375,8 +378,9 @@ int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu, const void*
     else
       launch_chained(moba::kv4_join_kernel<1>, dim3((unsigned)(nu * p.R / split)), dim3(moba::kKv4JoinThreads), 0, st, p);
     if (acc && chunk) {
-      launch_chained(masked ? moba::kv4_chunk_weight_kernel<true> : moba::kv4_chunk_weight_kernel<false>, dim3((unsigned)((capacity + 255) / 256), batch * heads_kv),
-                     dim3(moba::kKv4ColThreads), moba::kKv4ColSmemBytes, st, p);
+      launch_chained(masked ? moba::kv4_chunk_weight_kernel<true> : moba::kv4_chunk_weight_kernel<false>,
+                     dim3((unsigned)((capacity + 255) / 256), batch * heads_kv), dim3(moba::kKv4ColThreads),
+                     moba::kKv4ColSmemBytes, st, p);
     } else if (keep) {
       launch_chained(moba::kv4_seen_kernel,
                      dim3((unsigned)((capacity + moba::kKv4SeenKeys - 1) / moba::kKv4SeenKeys), batch * heads_kv),

@@ -398,14 +398,36 @@ int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch,
  * acc        if not NULL: acc[b][g][j] += the sum, over the query rows of
  *            the sequence and the q heads of kv head g, of the softmax weight
  *            of token j. In a fixed order.
- *            (With at most 8 rows a sequence and kv head on average, their
- *            scores stay in scratch until then: 32 bytes a sequence, kv head
- *            and token of the capacity, or of the chosen blocks, up to 1 GiB;
- *            where they would need more, they are computed again.)
+ *            A weight carries the rounding of lse to fp32: it is off by up
+ *            to 2^-22 |lse| of itself (2^-20 |lse| from |lse| = 45,000 on,
+ *            where it is taken lower so that none exceeds one).
  * out        device bf16 output [total][heads_q][head_dim]. It must not
  *            overlap q, but without acc it may be q itself (with acc the
  *            queries are read again once rows of out have been written).
  * lse        device fp32 output [heads_q][total], natural log.
+ *
+ * A row whose scores are not finite has results that are not. Scores that
+ * fp32 holds give finite ones; beyond some 2^20 in magnitude it does not tell
+ * neighbouring ones apart.
+ *
+ * One kernel serves all sequences of a call. It is chosen by the rows a
+ * sequence and kv head on average (total * heads_q / heads_kv / batch), and
+ * with a gate also by topk * block_size against the capacity: a batch of long
+ * chunks and single tokens, or chunks of short sequences in a large cache, is
+ * faster in two calls, or in a cache of its size.
+ *
+ * Scratch, by capacity since the lengths are on the device:
+ *   acc, at most 8 rows a sequence and kv head on average: their scores, 32
+ *     bytes for each kv head, token of the capacity (with a gate, of as many
+ *     blocks as 8 rows can choose) and group of 8 rows, of which there are
+ *     total * heads_q / heads_kv / 8 + batch; up to 1 GiB, else they are
+ *     computed again;
+ *   a gate: its scores, 8 bytes for each block and row of up to 592 groups of
+ *     8, 16 or 32 rows at a time (2.5 GB at most, at 16,384 blocks), and with
+ *     acc, or where it goes over all keys, 4 bytes for each block, kv head
+ *     and such a group;
+ *   many rows: 64 KB for each kv head and 256 rows, or part of them;
+ *   2 * 148 partial results of 8, 16 or 256 rows, 520 bytes each.
  */
 int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu,
                     const void* kv4, const int32_t* lengths,
