@@ -397,7 +397,8 @@ def kv4_pool(kv4: torch.Tensor, lengths: torch.Tensor, block_size: int, kmean=No
     if stream is not None:
         stream = _lend(stream, kv4, lengths, kmean)
     if kmean is None:
-        kmean = kv4.new_empty(shape, dtype=torch.float32) if stream is None else _empty(kv4, stream, shape, torch.float32)
+        kmean = kv4.new_empty(shape, dtype=torch.float32) if stream is None else \
+            _empty(kv4, stream, shape, torch.float32)
         mp = kmean.data_ptr()
     if shape[2]:
         _call(dev, stream, lib().moba_kv4_pool, kv4.data_ptr(), lp, batch, hkv, HEAD_DIM, cap, block_size, mp)
@@ -443,7 +444,8 @@ def kv4_attend(q: torch.Tensor, kv4: torch.Tensor, lengths: torch.Tensor, cu=Non
         out = torch.empty_like(q) if stream is None else _empty(q, stream, q.shape, torch.bfloat16)
         op = out.data_ptr()
     if lse is None:
-        lse = kv4.new_empty((hq, T), dtype=torch.float32) if stream is None else _empty(kv4, stream, (hq, T), torch.float32)
+        lse = kv4.new_empty((hq, T), dtype=torch.float32) if stream is None else \
+            _empty(kv4, stream, (hq, T), torch.float32)
         ep = lse.data_ptr()
     if T:
         _call(dev, stream, lib().moba_kv4_attend, qp, T, cp, kv4.data_ptr(), lp, mp, batch, hq, hkv, HEAD_DIM, cap,

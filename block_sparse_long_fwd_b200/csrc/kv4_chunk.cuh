@@ -24,6 +24,8 @@
 // time; what bounds it is the chain score - weights - product of two tiles.
 #pragma once
 
+#include <type_traits>
+
 #include "kv4_attn.cuh"
 
 namespace moba {
@@ -227,7 +229,14 @@ __global__ void __launch_bounds__(kKv4ChunkThreads, 1) kv4_chunk_kernel(Kv4AttnP
       if (s1 <= s0) continue;
       done += s1 - s0;
       if (X == 1 && u.rows <= kTile) continue;
-      const float qs = __ldcg(p.qscale + (int64_t)ui * kKv4ChunkRows + row);
+      // A row's scale is applied with the reference, in one step: score minus reference, exact but for the reference's
+      // own coarseness, so that the largest is 12 above it, or by roundings upwards as little as -4 where fp32 numbers
+      // are 8 apart. Rows of large queries (some 64 and more) may have scores beyond that, of 2^27: theirs have the
+      // scale applied before, and so lie on one grid with the reference, which is 0 to 12 below the largest. (The loop is
+      // there twice for it: a branch within, on the row or on its reference, took 4 to 9 % of the kernel's time.)
+      const float scale = __ldcg(p.qscale + (int64_t)ui * kKv4ChunkRows + row);
+      const bool large = scale >= 0.03125f;
+      const float before = large ? scale : 1.f, qs = large ? 1.f : scale;
       const int pos = row < u.rows ? u.pos0 + (u.row0 + row) / p.G : -1;
       const int first_pos = u.pos0 + (u.row0 + X * kTile) / p.G;
       float ref = kKv4Low, l = 0.f;
@@ -236,98 +245,101 @@ __global__ void __launch_bounds__(kKv4ChunkThreads, 1) kv4_chunk_kernel(Kv4AttnP
       uint32_t on = ~0u;
       int block = -1;
       const int row32 = u.row0 + (row & ~31);
-      for (int s = s0; s < s1; ++s, ++sx) {
-        if constexpr (MASKED) {
-          if (s * kTile / p.pick_B != block) {
-            block = s * kTile / p.pick_B;
-            on = (row & ~31) < u.rows ? kv4_picks(p, u.b, u.h, u.t0, row32, block) : 0;
+      auto run = [&](auto is_large) -> bool {
+        constexpr bool LARGE = decltype(is_large)::value;
+        for (int s = s0; s < s1; ++s, ++sx) {
+          if constexpr (MASKED) {
+            if (s * kTile / p.pick_B != block) {
+              block = s * kTile / p.pick_B;
+              on = (row & ~31) < u.rows ? kv4_picks(p, u.b, u.h, u.t0, row32, block) : 0;
+            }
           }
-        }
-        if (!mbar_wait(&sh->s_full[X], sx & 1, abort_flag)) goto done;
-        __syncwarp();
-        tc_fence_after();
-        uint32_t r[128];
-        {
-          uint32_t (&r0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[0]);
-          uint32_t (&r1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[32]);
-          uint32_t (&r2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[64]);
-          uint32_t (&r3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[96]);
-          tmem_ld32(tS, r0);
-          tmem_ld32(tS + 32, r1);
-          tmem_ld32(tS + 64, r2);
-          tmem_ld32(tS + 96, r3);
-          tmem_ld_wait();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->s_free);
-        if ((s + 1) * kTile - 1 > first_pos || (MASKED && on != ~0u)) {
-          const int lim = !MASKED || on >> lane & 1u ? pos - s * kTile : -1;  // keys e > lim are masked
-#pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (e > lim) r[e] = __float_as_uint(-INFINITY);
-        }
-        float mx8[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          float m = fmax3(__uint_as_float(r[c]), __uint_as_float(r[c + 8]), __uint_as_float(r[c + 16]));
-#pragma unroll
-          for (int e = 24; e < 120; e += 16) m = fmax3(m, __uint_as_float(r[e + c]), __uint_as_float(r[e + 8 + c]));
-          mx8[c] = fmaxf(m, __uint_as_float(r[120 + c]));
-        }
-        const float mx = qs * fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-        // the reference moves as in kv4_attn.cuh: weights stay under 2^15
-        const bool move = mx > __fadd_rd(ref, 15.f);
-        float factor = 1.f;
-        if (move) {
-          const float to = __fadd_ru(mx, -12.f);
-          factor = ex2_approx(ref - to);
-          ref = to;
-        }
-        uint32_t pk[64];
-        {
-          uint64_t c2 = f2_pack(qs, qs);
-          const uint64_t nm2 = f2_pack(-ref, -ref);
-          // a coarse reference: scores rounded as the largest was then lie on one grid with it, and the largest 0 to 15 above
-          if (fabsf(ref) >= kKv4Coarse && ref > kKv4Low) {
-#pragma unroll
-            for (int e = 0; e < 128; ++e) r[e] = __float_as_uint(__fmul_rn(__uint_as_float(r[e]), qs));
-            c2 = f2_pack(1.f, 1.f);
-          }
-          uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-          for (int e = 0; e < 128; e += 2) {
-            const uint64_t x2 = f2_fma((uint64_t)r[e] | ((uint64_t)r[e + 1] << 32), c2, nm2);
-            const float a = ex2_approx(f2_lo(x2)), b = ex2_approx(f2_hi(x2));
-            sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(a, b));
-            pk[e >> 1] = pack_half2(a, b);
-          }
-          const uint64_t s01 = f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]));
-          l = l * factor + (f2_lo(s01) + f2_hi(s01));
-        }
-        if (s > s0) {
-          if (!mbar_wait(&sh->pv_done[X], (sx - 1) & 1, abort_flag)) goto done;
+          if (!mbar_wait(&sh->s_full[X], sx & 1, abort_flag)) return false;
           __syncwarp();
           tc_fence_after();
-        }
-        // warp-collective: the branch is the warp's, the other rows multiply by 1
-        if (s > s0 && __any_sync(0xffffffffu, move)) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + c * 32, o);
+          uint32_t r[128];
+          {
+            uint32_t (&r0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[0]);
+            uint32_t (&r1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[32]);
+            uint32_t (&r2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[64]);
+            uint32_t (&r3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[96]);
+            tmem_ld32(tS, r0);
+            tmem_ld32(tS + 32, r1);
+            tmem_ld32(tS + 64, r2);
+            tmem_ld32(tS + 96, r3);
             tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
-            tmem_st32(tO + c * 32, o);
           }
-        }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->s_free);
+          if constexpr (LARGE) {
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) tmem_st16(tP + ch * 16, pk + ch * 16);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&sh->p_full[X]);
-      }
+            for (int e = 0; e < 128; ++e) r[e] = __float_as_uint(__fmul_rn(__uint_as_float(r[e]), before));
+          }
+          if ((s + 1) * kTile - 1 > first_pos || (MASKED && on != ~0u)) {
+            const int lim = !MASKED || on >> lane & 1u ? pos - s * kTile : -1;  // keys e > lim are masked
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (e > lim) r[e] = __float_as_uint(-INFINITY);
+          }
+          float mx8[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float m = fmax3(__uint_as_float(r[c]), __uint_as_float(r[c + 8]), __uint_as_float(r[c + 16]));
+#pragma unroll
+            for (int e = 24; e < 120; e += 16) m = fmax3(m, __uint_as_float(r[e + c]), __uint_as_float(r[e + 8 + c]));
+            mx8[c] = fmaxf(m, __uint_as_float(r[120 + c]));
+          }
+          const float top = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+          const float mx = __fmul_ru(qs, top);
+          // the reference moves as in kv4_attn.cuh: weights stay under 2^15
+          const bool move = mx > __fadd_rd(ref, 15.f);
+          float factor = 1.f;
+          if (move) {
+            const float to = __fadd_ru(mx, -12.f);
+            factor = ex2_approx(ref - to);
+            ref = to;
+          }
+          uint32_t pk[64];
+          {
+            const uint64_t c2 = f2_pack(qs, qs), nm2 = f2_pack(-ref, -ref);
+            uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+            for (int e = 0; e < 128; e += 2) {
+              const uint64_t x2 = f2_fma((uint64_t)r[e] | ((uint64_t)r[e + 1] << 32), c2, nm2);
+              const float a = ex2_approx(f2_lo(x2)), b = ex2_approx(f2_hi(x2));
+              sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(a, b));
+              pk[e >> 1] = pack_half2(a, b);
+            }
+            const uint64_t s01 = f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]));
+            l = l * factor + (f2_lo(s01) + f2_hi(s01));
+          }
+          if (s > s0) {
+            if (!mbar_wait(&sh->pv_done[X], (sx - 1) & 1, abort_flag)) return false;
+            __syncwarp();
+            tc_fence_after();
+          }
+          // warp-collective: the branch is the warp's, the other rows multiply by 1
+          if (s > s0 && __any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+              tmem_st32(tO + c * 32, o);
+            }
+          }
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) tmem_st16(tP + ch * 16, pk + ch * 16);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&sh->p_full[X]);
+        }
+        return true;
+      };
+      if (!(__any_sync(0xffffffffu, large) ? run(std::true_type()) : run(std::false_type()))) goto done;
       // epilogue: the row's result, or its part of it
       if (!mbar_wait(&sh->pv_done[X], (sx - 1) & 1, abort_flag)) goto done;
       __syncwarp();
@@ -667,8 +679,8 @@ __global__ void __launch_bounds__(kKv4ColThreads, 2) kv4_chunk_weight_kernel(Kv4
         const bool on = row < rows && pos0 + tok >= 0;
         // a row without keys, or behind the last: the score minus infinity
         const float scale = on ? __ldcg(p.qscale + ui * kKv4ChunkRows + (i & 1) * kTile + c) : 1.f;
-        const float sum = on ? kv4_log2_sum(__ldcg(p.lse + (int64_t)(h * p.G + row % p.G) * p.total + t0 + tok)) : INFINITY;
-        sh->row[k & 1][c] = make_float2(scale, -sum);
+        const float lse = on ? __ldcg(p.lse + (int64_t)(h * p.G + row % p.G) * p.total + t0 + tok) : 0.f;
+        sh->row[k & 1][c] = make_float2(scale, on ? -kv4_log2_sum(lse) : -INFINITY);
         sh->pos[k & 1][c] = row < rows ? pos0 + tok : INT32_MAX;
       }
       mbar_arrive(&sh->row_full[k & 1]);

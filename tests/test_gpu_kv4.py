@@ -1119,3 +1119,19 @@ def test_captured_eviction_takes_the_weights_and_lengths_of_its_replay():
                 want = ref.evict(a[b, h].astype(np.float64), L, 300, 20)
                 assert np.array_equal(kept[b, h, :len(want)].cpu().numpy(), want) and (kept[b, h, len(want):] == -1).all()
                 assert np.array_equal(f64(k[b, :len(want), h]), vals[b][0][h, want]) and (k[b, len(want):] == 0).all()
+
+
+@pytest.mark.parametrize("n", [9, 100])
+@pytest.mark.parametrize("kscale,vscale", [(2.0**-9, 2.0**-9), (1.0, 5000.0), (6000.0, 1.0), (2000.0, 2.0**-12), (2.0**-6, 1.0)])
+def test_many_rows_over_keys_and_values_of_every_size(n, kscale, vscale):
+    # queries as large as the keys are small, row by row: a unit holds small and large ones (some 64 and more) side by side
+    rng = np.random.default_rng(23)
+    L, hkv, G, cap = 600, 2, 4, 640
+    k, v = rng.standard_normal((hkv, cap, 128)) * kscale, rng.standard_normal((hkv, cap, 128)) * vscale
+    tiles = ref.pack(f64(bf16(k)), f64(bf16(v)))
+    size = np.where(rng.random((n, hkv * G, 1)) < 0.5, 1.0, 2.0 ** rng.integers(-6, 3, (n, hkv * G, 1)))
+    q = bf16(rng.standard_normal((n, hkv * G, 128)) / kscale * size)
+    a = torch.zeros(1, hkv, cap, device="cuda")
+    out, lse = moba.kv4_attend(q.cuda(), torch.from_numpy(tiles[None]).cuda(), ints([L]), acc=a)
+    ok()
+    check_attend((out, lse, a, torch.zeros_like(a)), f64(q), [ref.unpack(tiles)], [L], [n], hkv)
