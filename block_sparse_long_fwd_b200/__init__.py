@@ -100,7 +100,7 @@ def _lend(stream, *tensors):
     """The stream as torch knows it. The caller's tensors that it will use may be dropped right after the call: their
     memory is handed out again only behind the stream's work.
     """
-    given = [x for x in tensors if x is not None]
+    given = [x for x in tensors if x is not None and x.is_cuda]  # the calls refuse the others themselves
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream, device=given[0].device)
     for x in given:

@@ -1135,3 +1135,31 @@ def test_many_rows_over_keys_and_values_of_every_size(n, kscale, vscale):
     out, lse = moba.kv4_attend(q.cuda(), torch.from_numpy(tiles[None]).cuda(), ints([L]), acc=a)
     ok()
     check_attend((out, lse, a, torch.zeros_like(a)), f64(q), [ref.unpack(tiles)], [L], [n], hkv)
+
+
+def test_a_captured_call_on_a_given_stream():
+    # the captured stream itself, and one that is forked from it and joined again
+    lengths = [900, 1500]
+    kv4, _ = random_cache(lengths, 2, 1536, 2)
+    lens = ints(lengths)
+    q = bf16(np.random.default_rng(1).standard_normal((2, 8, 128))).cuda()
+    want = moba.kv4_attend(q, kv4, lens)
+    whole = moba.kv4_load(kv4, lens, 1500)
+    torch.cuda.synchronize()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        x = q * 1
+        a = moba.kv4_attend(x, kv4, lens, stream=main)
+        side.wait_stream(main)
+        b = moba.kv4_attend(x, kv4, lens, stream=side)
+        c = moba.kv4_load(kv4, lens, 1500, stream=side)
+        del x
+        main.wait_stream(side)
+        taken = [torch.full_like(q, 3.0) for _ in range(4)]  # nothing of this takes a place that is still read
+    for _ in range(3):
+        g.replay()
+        ok()
+        for got, to in ((a, want), (b, want), (c, whole)):
+            assert all(torch.equal(x, y) for x, y in zip(got, to))
+        assert all((t == 3).all() for t in taken)
