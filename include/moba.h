@@ -414,7 +414,10 @@ int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch,
  * sequence and kv head on average (total * heads_q / heads_kv / batch), and
  * with a gate also by topk * block_size against the capacity: a batch of long
  * chunks and single tokens, or chunks of short sequences in a large cache, is
- * faster in two calls, or in a cache of its size.
+ * faster in two calls, or in a cache of its size. Many rows with a gate mostly
+ * go over every key and mask: without acc, moba_kv4_load and
+ * moba_fwd_chunk_means are faster for a long chunk (512 tokens of 32 / 8 heads
+ * at 32K, block 512, top-12: 488 us here, some 200 there).
  *
  * Scratch, by capacity since the lengths are on the device:
  *   acc, at most 8 rows a sequence and kv head on average: their scores, 32
@@ -427,7 +430,7 @@ int moba_kv4_pool(const void* kv4, const int32_t* lengths, int batch,
  *     acc, or where it goes over all keys, 4 bytes for each block, kv head
  *     and such a group;
  *   many rows: 64 KB for each kv head and 256 rows, or part of them;
- *   2 * 148 partial results of 8, 16 or 256 rows, 520 bytes each.
+ *   296 partial results of 8, 16 or 256 rows, 520 bytes a row.
  */
 int moba_kv4_attend(const void* q, int64_t total, const int32_t* cu,
                     const void* kv4, const int32_t* lengths,
